@@ -440,6 +440,131 @@ int blockpilot_mlp(const void* last_logits, int64_t ld, const float* row_lse, co
                    int block, float* z, int32_t* choice, int32_t* bsize, void* ws,
                    size_t ws_bytes, tv_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Paged 4-bit KV cache: tv_rope, kv4_append, kv4_gather, tree_verify_attn_kv4
+ * (no counterpart in the source pages, which start from rotated q/k and a
+ * contiguous prefix: these calls are what stands before and after a
+ * verification step).
+ *
+ * cache  uint8 [n_pages, Hkv, page_size * (d + 4)], 16-byte aligned, d in
+ *   {64, 128}, page_size P in {16, 32, 64, 128}.  One (page, KV head) block:
+ *     K codes   [d/32][P][16 bytes]  chunk c of token t: its dims 32c..32c+31
+ *     V codes   [P/16][d][8 bytes]   dim by dim, the 16 tokens of a group
+ *     K scales  bf16 [P], V scales bf16 [P]
+ *   Eight codes make a little-endian 32-bit word: item e (a dim of a key, a
+ *   token of a value) sits in nibble e/2 + 4*(e%2).  A code is n + 8 with n in
+ *   -7..7 and stands for s * n.  A row (token, head) x has one scale
+ *     s = max(bf16_up(max|x| / 7), 2^-100),  n = rint(x / s)   (ties to even)
+ *   in fp32 (bf16_up rounds up to bf16); a row with a NaN or infinity gets
+ *   s = NaN and reads back as NaN as a whole.  132 bytes per token and head
+ *   for K and V at d = 128, against 512 in bf16.
+ * block_table  int32 [B, table_ld]: page of tokens [P*i, P*(i+1)) of request r
+ *   at [r, i].  Only entries that a token needs are read.  An entry outside
+ *   [0, n_pages) is bad: nothing is read or written through it, and 1 is
+ *   written to *err (device int32, may be NULL; never cleared by the calls).
+ * Requests may share pages for reading; a page that kv4_append writes belongs
+ * to one request.
+ * Rotation tables are fp32 [max_pos, rot_dim], the cosines of rot_dim/2
+ * frequencies followed by their sines, 16-byte aligned; rot_dim is a multiple
+ * of 16 (0: no rotation, the table may be NULL) and the dims from rot_dim on
+ * are left as they are.  Pair i is (x[i], x[i + rot_dim/2]) or, interleaved,
+ * (x[2i], x[2i + 1]):  y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin, each
+ * product and sum rounded to fp32 by itself.
+ * -------------------------------------------------------------------------- */
+/* Bytes of a cache of n_pages pages (0 for a shape outside the above). */
+size_t kv4_cache_size(int n_pages, int page_size, int Hkv, int d);
+
+/* --------------------------------------------------------------------------
+ * tv_rope — rotates query (and key) rows at their positions, e.g. the
+ * candidate nodes' rows at the pos that tv_tree_prep gives.
+ *   q [n, ldq] dtype, Hq heads of d from the row's start (ldq in elements, so
+ *   a slice of a fused projection's output can be passed); k likewise with
+ *   Hkv heads, or NULL.  Rows are 16-byte aligned.  d % 16 == 0, d <= 512.
+ *   pos int32 [n] in [0, max_pos): a row with another position is not written
+ *   and 1 is written to *err.
+ * Outputs: q_out [n, Hq, d], k_out [n, Hkv, d] dtype (k_out NULL iff k is),
+ *   contiguous, not overlapping the inputs.
+ * -------------------------------------------------------------------------- */
+int tv_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, int n, int Hq, int Hkv,
+            int d, const int32_t* pos, const float* table, int max_pos, int rot_dim, int interleaved,
+            void* q_out, void* k_out, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kv4_append — rotates keys, quantises keys and values and appends them to
+ * the requests' cached tokens.
+ *   k, v [total_rows, ldk / ldv] dtype, Hkv heads of d from the row's start
+ *   row_off int32 [B+1]: request r's rows start at row_off[r]
+ *   path    int32 [B, path_ld] or NULL.  NULL: all rows row_off[r] ..
+ *           row_off[r+1]-1 are appended in order.  Else the rows row_off[r] +
+ *           path[r, j] up to the first negative entry, at most
+ *           min(path_ld, max_new): accept_longest_path's path as it is.
+ *   max_new upper bound of the appended rows per request (launch geometry)
+ *   pos     int32 [total_rows] rotation position of each source row, or NULL:
+ *           the token's index in its request
+ *   table, max_pos, rot_dim, interleaved: the rotation of the keys (rot_dim 0:
+ *           keys come rotated already, e.g. from tv_rope)
+ *   cache_len int32 [B]: tokens cached before; row j becomes token
+ *           cache_len[r] + j.  Not changed by the call.
+ * Outputs: the cache blocks of those tokens (other tokens keep their codes);
+ *   new_len int32 [B] or NULL: cache_len[r] + rows appended (not the same
+ *   array as cache_len).
+ * A row with a bad page entry, a token past the table, a source row outside
+ * [0, total_rows) or a position outside [0, max_pos) is skipped, and 1 is
+ * written to *err; so is a request with more rows than max_new (the first
+ * max_new are appended) or a negative cache_len (nothing is).
+ * -------------------------------------------------------------------------- */
+int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype, int total_rows,
+               const int32_t* row_off, const int32_t* path, int path_ld, int B, int max_new, const int32_t* pos,
+               const float* table, int max_pos, int rot_dim, int interleaved, void* cache, int n_pages,
+               int page_size, const int32_t* block_table, int table_ld, const int32_t* cache_len, int Hkv, int d,
+               int32_t* new_len, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kv4_gather — cached tokens back as rows (the contiguous prefix that
+ * tree_verify_attn reads; a request that moves; a check of the cache).
+ *   start   int32 [B] or NULL (= 0): first token of each request
+ *   out_off int32 [B+1]: request r's tokens start[r] + i go to output rows
+ *           out_off[r] + i, i < out_off[r+1] - out_off[r]
+ *   max_rows upper bound of the rows per request (launch geometry)
+ *   total_rows rows of the outputs
+ * Outputs: k_out, v_out [total_rows, Hkv, d] dtype: s * n, rounded once.
+ * Tokens with a bad page entry or past the table, and all rows of a request
+ * whose start or out_off is out of range, are not written, and 1 is written
+ * to *err; so it is for more rows than max_rows (the first max_rows are
+ * written).
+ * -------------------------------------------------------------------------- */
+int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
+               const int32_t* start, const int32_t* out_off, int B, int max_rows, int total_rows, int Hkv, int d,
+               int dtype, void* k_out, void* v_out, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * tree_verify_attn_kv4 — tree_verify_attn with the prefix in a paged 4-bit
+ * cache: node i attends to the first vis_i cached tokens of its request and
+ * to the nodes set in its ancestor row.  One node per request is plain
+ * decoding.  A node that sees nothing gets o = 0 and lse = -inf.
+ *   q [total_nodes, ldq], k_tree / v_tree [total_nodes, ldk / ldv] dtype:
+ *           Hq / Hkv heads of d from each row's start, rows 16-byte aligned
+ *   cache_len int32 [B]: cached tokens of each request (clamped to
+ *           [0, table_ld * page_size]; a clamped one writes 1 to *err)
+ *   node_off, node_cnt, anc, anc_words, vis_prefix, max_nodes, scale: as in
+ *           tree_verify_attn (nodes outside [0, total_nodes) do not exist)
+ *   d in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 64
+ * A cached token with a bad page entry is not visible (1 is written to *err).
+ * What a node does not see does not reach its output, whatever it holds: NaN
+ * in other nodes' rows, stale tokens behind cache_len.
+ * Outputs: out [total_nodes, Hq, d] dtype; lse float [total_nodes, Hq] or
+ *   NULL.  Rows of nodes that node_cnt leaves out are not written.
+ * Workspace: tree_verify_attn_kv4_workspace_size(...) bytes, 256-byte
+ *   aligned; its first int32 is a status word as in tree_verify_attn.
+ * -------------------------------------------------------------------------- */
+size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype);
+int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pages, int page_size,
+                         const int32_t* block_table, int table_ld, const int32_t* cache_len, const void* k_tree,
+                         int64_t ldk, const void* v_tree, int64_t ldv, const int32_t* node_off,
+                         const int32_t* node_cnt, const uint64_t* anc, int anc_words, const int32_t* vis_prefix,
+                         int B, int max_nodes, int total_nodes, int Hq, int Hkv, int d, int dtype, float scale,
+                         void* out, float* lse, void* ws, size_t ws_bytes, int32_t* err, tv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,12 +28,13 @@ Modules
   graft      successor-table update, stage templates, template retrieval
   dcut       prefix-product scores and batch-global budget selection
   mlp        BlockPilot block-size predictor
+  kv4        paged 4-bit KV cache: rotation, quantisation, append, attention
 
 Parity status: every function is pinned by tests in ``tests/test_oracle_*.py``
 except the *shape* of the Graft retrieval template, which the pages describe
 only qualitatively (see ``graft.stage_template``: "parity unpinned" for the
 template's exact slots; the retrieval given a template is pinned).
 """
-from . import accept, alpha, attention, dcut, graft, mlp, tree, vocab  # noqa: F401
+from . import accept, alpha, attention, dcut, graft, kv4, mlp, tree, vocab  # noqa: F401
 
-__all__ = ["accept", "alpha", "attention", "dcut", "graft", "mlp", "tree", "vocab"]
+__all__ = ["accept", "alpha", "attention", "dcut", "graft", "kv4", "mlp", "tree", "vocab"]

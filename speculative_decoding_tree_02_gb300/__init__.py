@@ -25,6 +25,7 @@ __all__ = [
     "accept_longest_path", "graft_adj_update", "graft_retrieve", "dcut_select", "blockpilot_mlp",
     "stage_templates", "assemble_hybrid", "LIB_PATH", "load_library", "EXPORTS",
     "graft_stage_decide", "graft_replace", "dcut_choose_rho", "best_first_template", "accept_rejection_sampling",
+    "tv_rope", "kv4_new_cache", "kv4_append", "kv4_gather", "tree_verify_attn_kv4", "tree_verify_attn_kv4_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtreeverify.so")
@@ -57,6 +58,14 @@ _SIGS = {
     "dcut_select_workspace_size": (_SZ, [_I, _I, _I]),
     "dcut_select": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "blockpilot_mlp_workspace_size": (_SZ, [_I, _I, _I]),
+    "kv4_cache_size": (_SZ, [_I, _I, _I, _I]),
+    "tv_rope": (_I, [_P, _I64, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "kv4_append": (_I, [_P, _I64, _P, _I64, _I, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I, _I, _P, _I, _P,
+                        _I, _I, _P, _P, _P]),
+    "kv4_gather": (_I, [_P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "tree_verify_attn_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "tree_verify_attn_kv4": (_I, [_P, _I64, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _I, _I,
+                                  _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
     "blockpilot_mlp": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
 EXPORTS = tuple(_SIGS)
@@ -442,3 +451,202 @@ def blockpilot_mlp(last_logits, row_lse, W1, W2, b1=None, b2=None, block=16, ws=
         _ptr(last_logits), last_logits.stride(0), _ptr(row_lse), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2),
         B, V, H, C, block, _ptr(z), _ptr(choice), _ptr(bsize), _ptr(ws), ws.numel(), _stream()))
     return z, choice, bsize
+
+
+# --------------------------------------------------- paged 4-bit KV cache, rotation
+# These calls sit on the decoding path, where the host's time per call counts:
+# pointers go to the library as plain integers.
+def _dense(t: Optional[torch.Tensor], name: str, dtype, dev, shape) -> Optional[int]:
+    """Address of a contiguous tensor of this dtype, device and shape (None in ``shape``: any size); None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype, dev, n, heads, d):
+    """(address, elements between rows) of [n, heads, d] rows whose heads are packed; the row stride is free, so a
+    slice of a fused projection's output can be passed."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 3 or (t.shape[0] != n) or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, d)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be packed")
+    return t.data_ptr(), (s0 if n > 1 else heads * d)
+
+
+def _call_on(dev, fn: str, *args):
+    """Calls the library on ``dev`` and its current stream (the last argument)."""
+    if dev.type != "cuda":
+        raise ValueError("libtreeverify takes device tensors")
+    f = getattr(load_library(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _act_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return TV_BF16
+    if t.dtype == torch.float32:
+        return TV_F32
+    raise TypeError(f"{name}: unsupported dtype {t.dtype}: float32 or bfloat16")
+
+
+def _cache_geometry(cache, page_size):
+    """(n_pages, Hkv, d) of a cache tensor."""
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor [n_pages, Hkv, page_size * (d + 4)]")
+    n_pages, Hkv, nbytes = cache.shape
+    d = nbytes // page_size - 4 if page_size > 0 else 0
+    if d <= 0 or page_size * (d + 4) != nbytes:
+        raise ValueError(f"cache blocks of {nbytes} bytes do not fit page_size {page_size}")
+    return n_pages, Hkv, d
+
+
+def _rope_args(rope, dev):
+    if rope is None:
+        return None, 0, 0
+    return _dense(rope, "rope", torch.float32, dev, (None, None)), rope.shape[0], rope.shape[1]
+
+
+def _new_err(err, dev):
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+    return err, _dense(err, "err", torch.int32, dev, (1,))
+
+
+def tv_rope(q, k, pos, rope, interleaved=False, outputs=None, err=None):
+    """Rotates q [n, Hq, d] and k [n, Hkv, d] (or None) at ``pos`` int32 [n] with the table ``rope`` float32
+    [max_pos, rot_dim] (cosines, then sines).  Row strides are free.  Returns q_out, k_out, err."""
+    n, Hq, d = q.shape
+    dev = q.device
+    dt = _act_dtype(q, "q")
+    Hkv = k.shape[1] if k is not None else 0
+    if outputs is None:
+        outputs = (torch.empty((n, Hq, d), dtype=q.dtype, device=dev),
+                   torch.empty((n, Hkv, d), dtype=q.dtype, device=dev) if k is not None else None)
+    q_out, k_out = outputs
+    if (k is None) != (k_out is None):
+        raise ValueError("k and its output go together")
+    err, perr = _new_err(err, dev)
+    table, max_pos, rot = _rope_args(rope, dev)
+    pq, ldq = _rows(q, "q", q.dtype, dev, n, Hq, d)
+    pk, ldk = _rows(k, "k", q.dtype, dev, n, Hkv, d) if k is not None else (None, 0)
+    _call_on(dev, "tv_rope", pq, ldq, pk, ldk, dt, n, Hq, Hkv, d, _dense(pos, "pos", torch.int32, dev, (n,)), table,
+             max_pos, rot, int(interleaved), _dense(q_out, "q_out", q.dtype, dev, (n, Hq, d)),
+             _dense(k_out, "k_out", q.dtype, dev, (n, Hkv, d)), perr)
+    return q_out, k_out, err
+
+
+def kv4_new_cache(n_pages, page_size, Hkv, d, device="cuda"):
+    """A zeroed cache: uint8 [n_pages, Hkv, page_size * (d + 4)]."""
+    if load_library().kv4_cache_size(max(n_pages, 1), page_size, Hkv, d) == 0 or n_pages < 0:
+        raise ValueError(f"no 4-bit cache of page size {page_size}, {Hkv} heads of {d}")
+    return torch.zeros((n_pages, Hkv, page_size * (d + 4)), dtype=torch.uint8, device=device)
+
+
+def kv4_append(k, v, cache, page_size, block_table, cache_len, row_off, max_new, path=None, pos=None, rope=None,
+               interleaved=False, new_len=None, err=None):
+    """Appends rows of k, v [rows, Hkv, d] to the cache (in place); keys are rotated with ``rope`` (None: they come
+    rotated) at ``pos`` (None: the token's index).  ``path`` int32 [B, m] picks rows of each request up to its first
+    negative entry, as accept_longest_path returns it.  Returns new_len int32 [B], err int32 [1]."""
+    dev = cache.device
+    n_pages, Hkv, d = _cache_geometry(cache, page_size)
+    dt = _act_dtype(k, "k")
+    n = k.shape[0]
+    B = cache_len.numel()
+    pk, ldk = _rows(k, "k", k.dtype, dev, n, Hkv, d)
+    pv, ldv = _rows(v, "v", k.dtype, dev, n, Hkv, d)
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    err, perr = _new_err(err, dev)
+    table, max_pos, rot = _rope_args(rope, dev)
+    i32 = torch.int32
+    _call_on(dev, "kv4_append", pk, ldk, pv, ldv, dt, n, _dense(row_off, "row_off", i32, dev, (B + 1,)),
+             _dense(path, "path", i32, dev, (B, None)), path.shape[1] if path is not None else 0, B, max_new,
+             _dense(pos, "pos", i32, dev, (n,)), table, max_pos, rot, int(interleaved), cache.data_ptr(), n_pages,
+             page_size, _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             _dense(cache_len, "cache_len", i32, dev, (B,)), Hkv, d, _dense(new_len, "new_len", i32, dev, (B,)), perr)
+    return new_len, err
+
+
+def kv4_gather(cache, page_size, block_table, out_off, max_rows, start=None, total_rows=None, dtype=torch.bfloat16,
+               outputs=None, err=None):
+    """Cached tokens start[r] .. (0 without ``start``) of each request as rows out_off[r] .. out_off[r+1]-1 of k, v
+    [total_rows, Hkv, d].  Give ``outputs`` (their length and dtype count) or ``total_rows``.  Returns k, v, err."""
+    dev = cache.device
+    n_pages, Hkv, d = _cache_geometry(cache, page_size)
+    B = out_off.numel() - 1
+    if outputs is None:
+        if total_rows is None:
+            raise ValueError("kv4_gather needs outputs or total_rows")
+        outputs = tuple(torch.empty((total_rows, Hkv, d), dtype=dtype, device=dev) for _ in range(2))
+    k, v = outputs
+    n = k.shape[0]
+    dt = _act_dtype(k, "k")
+    err, perr = _new_err(err, dev)
+    i32 = torch.int32
+    _call_on(dev, "kv4_gather", cache.data_ptr(), n_pages, page_size,
+             _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             _dense(start, "start", i32, dev, (B,)), _dense(out_off, "out_off", i32, dev, (B + 1,)), B, max_rows, n,
+             Hkv, d, dt, _dense(k, "k", k.dtype, dev, (n, Hkv, d)), _dense(v, "v", k.dtype, dev, (n, Hkv, d)), perr)
+    return k, v, err
+
+
+def tree_verify_attn_kv4_workspace(B, max_nodes, Hq, Hkv, d, dtype=torch.bfloat16, device="cuda"):
+    """A workspace for tree_verify_attn_kv4 calls of up to these sizes (one call at a time)."""
+    code = TV_F32 if dtype == torch.float32 else TV_BF16
+    return _ws(load_library().tree_verify_attn_kv4_workspace_size(B, max_nodes, Hq, Hkv, d, code), device)
+
+
+def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_tree, node_off, anc, max_nodes,
+                         vis_prefix=None, node_cnt=None, scale=None, out=None, lse=None, want_lse=True, ws=None,
+                         err=None):
+    """tree_verify_attn with the prefix in a paged 4-bit cache.  q, k_tree, v_tree: [n, heads, d], row strides free.
+    Returns out, lse, err."""
+    dev = q.device
+    n, Hq, d = q.shape
+    n_pages, Hkv, dc = _cache_geometry(cache, page_size)
+    if dc != d:
+        raise ValueError(f"the cache holds heads of {dc}, q has {d}")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    dt = _act_dtype(q, "q")
+    B = node_off.numel() - 1
+    if scale is None:
+        scale = 1.0 / d ** 0.5
+    pq, ldq = _rows(q, "q", q.dtype, dev, n, Hq, d)
+    pk, ldk = _rows(k_tree, "k_tree", q.dtype, dev, n, Hkv, d)
+    pv, ldv = _rows(v_tree, "v_tree", q.dtype, dev, n, Hkv, d)
+    if out is None:
+        out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
+    err, perr = _new_err(err, dev)
+    need = load_library().tree_verify_attn_kv4_workspace_size(B, max_nodes, Hq, Hkv, d, dt)
+    if ws is None or ws.numel() < need:
+        ws = _ws(need, dev)
+    i32 = torch.int32
+    _call_on(dev, "tree_verify_attn_kv4", pq, ldq, cache.data_ptr(), n_pages, page_size,
+             _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             _dense(cache_len, "cache_len", i32, dev, (B,)), pk, ldk, pv, ldv,
+             _dense(node_off, "node_off", i32, dev, (B + 1,)), _dense(node_cnt, "node_cnt", i32, dev, (B,)),
+             _dense(anc, "anc", torch.int64, dev, (n, None)), anc.shape[1],
+             _dense(vis_prefix, "vis_prefix", i32, dev, (n,)), B, max_nodes, n, Hq, Hkv, d, dt, float(scale),
+             _dense(out, "out", q.dtype, dev, (n, Hq, d)), _dense(lse, "lse", torch.float32, dev, (n, Hq)),
+             _dense(ws, "ws", torch.uint8, dev, (None,)), ws.numel(), perr)
+    return out, lse, err

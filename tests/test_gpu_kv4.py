@@ -1,0 +1,555 @@
+"""GPU parity of the paged 4-bit KV cache calls (tv_rope, kv4_append,
+kv4_gather, tree_verify_attn_kv4) against oracle/kv4.py.
+
+Rotation, append and gather are compared bit for bit: the definition fixes
+every rounding.  Attention is compared with the fp64 oracle within
+``kv4.attention_tolerance`` (bounds derived there from the roundings)."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev, host
+from oracle import kv4 as ok
+from oracle import tree as otree
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+# ------------------------------------------------------------------- helpers
+def act(x, bf16):
+    """float32 array -> (device tensor, the float32 values it holds)."""
+    t = torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda()
+    t = t.to(torch.bfloat16) if bf16 else t
+    return t, t.float().cpu().numpy()
+
+
+def bits(t):
+    t = t.contiguous()
+    return host(t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32))
+
+
+def rounded(x, bf16):
+    """float32 values -> the bits of the rows' type."""
+    return ok.bf16_bits(x).view(np.int16) if bf16 else np.ascontiguousarray(x, np.float32).view(np.int32)
+
+
+def fused(rng, n, Hq, Hkv, d, bf16):
+    """q, k, v as slices of one projection's rows: [n, Hq + 2 Hkv, d]."""
+    t, x = act(rng.standard_normal((n, Hq + 2 * Hkv, d)), bf16)
+    cut = (slice(0, Hq), slice(Hq, Hq + Hkv), slice(Hq + Hkv, None))
+    return [t[:, c] for c in cut], [x[:, c] for c in cut]
+
+
+def random_pool(rng, n_pages, H, P, d):
+    """(cache uint8, kn, ks, vn, vs) of a pool with a quantised row in every slot."""
+    kn, vn = rng.integers(-7, 8, (2, n_pages, H, P, d))
+    ks, vs = ok.f32(ok.bf16_bits(rng.uniform(0.2, 0.4, (2, n_pages, H, P)).astype(np.float32)))
+    cache = np.zeros((n_pages, H, P * (d + 4)), np.uint8)
+    slot, dim = np.meshgrid(np.arange(P), np.arange(d), indexing="ij")
+    for at, n in ((ok._k_at(P, slot, dim), kn), (ok._v_at(P, d, slot, dim), vn)):
+        byte, sh = (np.asarray(x).ravel() for x in at)
+        code = ((n + 8).reshape(n_pages, H, -1) << sh).astype(np.uint8)
+        for nib in (0, 4):
+            m = sh == nib
+            cache[:, :, byte[m]] |= code[:, :, m]
+    for off, s in ((P * d, ks), (P * d + 2 * P, vs)):
+        b = ok.bf16_bits(s)
+        cache[:, :, off:off + 2 * P:2] = b & 255
+        cache[:, :, off + 1:off + 2 * P:2] = b >> 8
+    return cache, kn, ks, vn, vs
+
+
+def tables(rng, lens, P, spare=1, extra_cols=1):
+    """Block table over randomly ordered pages (unused entries -1) and the page count."""
+    used = [(n + P - 1) // P for n in lens]
+    n_pages = sum(used) + spare
+    perm = rng.permutation(n_pages)
+    t = np.full((len(lens), max(used) + extra_cols), -1, np.int32)
+    o = 0
+    for r, u in enumerate(used):
+        t[r, :u] = perm[o:o + u]
+        o += u
+    return t, n_pages
+
+
+def prefixes(pool, table, lens, P):
+    """Per request the (K, V) values of its cached tokens."""
+    _, kn, ks, vn, vs = pool
+    out = []
+    for r, n in enumerate(lens):
+        t = np.arange(n)
+        pg, sl = np.clip(table[r, t // P], 0, len(kn) - 1), t % P   # (a bad page: masked by its caller)
+        out.append((ok.values(kn[pg, :, sl], ks[pg, :, sl]), ok.values(vn[pg, :, sl], vs[pg, :, sl])))
+    return out
+
+
+def forest(rng, counts, kind):
+    """(parent, node_off, anc, see) of one tree per request."""
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    words = max(1, (max(counts) + 63) // 64)
+    par, anc, see = [], np.zeros((off[-1], words), np.uint64), np.zeros((off[-1], max(max(counts), 1)), bool)
+    for r, n in enumerate(counts):
+        for i in range(n):
+            if kind == "chain":
+                p = i - 1
+            elif kind == "roots":
+                p = -1 if i % 5 == 0 else i - 1
+            else:
+                p = -1 if i == 0 else int(rng.integers(0, i))
+            par.append(p)
+            g = off[r] + i
+            if p >= 0:
+                see[g] = see[off[r] + p]
+                anc[g] = anc[off[r] + p]
+            see[g, i] = True
+            anc[g, i // 64] |= np.uint64(1) << np.uint64(i % 64)
+    return np.array(par, np.int32), off, anc, see
+
+
+class Case:
+    """One tree_verify_attn_kv4 call and what the oracle says about it."""
+
+    def __init__(self, seed, counts, lens, Hq, Hkv, d, P, bf16=True, kind="random", vis=False, node_cnt=None,
+                 scale=None):
+        rng = np.random.default_rng(seed)
+        self.d, self.P, self.bf16, self.lens, self.scale, self.node_cnt = d, P, bf16, list(lens), scale, node_cnt
+        self.table, n_pages = tables(rng, lens, P)
+        self.pool = random_pool(rng, n_pages, Hkv, P, d)
+        self.cache = self.pool[0].copy()
+        _, self.off, self.anc, self.see = forest(rng, counts, kind)
+        n = int(self.off[-1])
+        (self.q, self.k, self.v), (self.hq, self.hk, self.hv) = fused(rng, n, Hq, Hkv, d, bf16)
+        self.max_nodes = max(counts)
+        self.vis = None
+        if vis:
+            self.vis = np.concatenate([rng.integers(-2, m + 3, c) for m, c in zip(lens, counts)]).astype(np.int32)
+        self.page_ok = None
+
+    def prefix(self):
+        return prefixes(self.pool, self.table, self.lens, self.P)
+
+    def args(self):
+        return (self.q, dev(self.cache), self.P, dev(self.table), dev(np.array(self.lens, np.int32)), self.k, self.v,
+                dev(self.off), dev(self.anc.view(np.int64)), self.max_nodes)
+
+    def kwargs(self):
+        nc = None if self.node_cnt is None else dev(np.array(self.node_cnt, np.int32))
+        return dict(vis_prefix=dev(self.vis), node_cnt=nc, scale=self.scale)
+
+    def oracle(self):
+        return ok.attention(self.hq, self.prefix(), self.hk, self.hv, self.off, self.see, self.vis, self.node_cnt,
+                            self.scale, self.page_ok)
+
+    def check(self, out, lse, want=None):
+        o, l, av, sa = want or self.oracle()
+        tol, ltol = ok.attention_tolerance(o, l, av, sa, self.d, self.bf16)
+        got, gl = out.float().cpu().numpy().astype(np.float64), host(lse).astype(np.float64)
+        rows = ~np.isnan(l)
+        err = np.abs(got - o)[rows]
+        assert (err <= tol[rows]).all(), f"out: {np.nanmax(err / tol[rows]):.3f} of the tolerance"
+        fin = rows & np.isfinite(l)
+        assert np.array_equal(gl[rows & ~fin], l[rows & ~fin])
+        ratio = np.abs(gl[fin] - l[fin]) / ltol[fin]
+        assert (ratio <= 1).all(), f"lse: {ratio.max():.3f} of the tolerance"
+
+    def run(self, tv, **kw):
+        out, lse, err = tv.tree_verify_attn_kv4(*self.args(), **(self.kwargs() | kw))
+        return out, lse, err
+
+
+# ------------------------------------------------------------------ rotation
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot,inter", [
+    (1, 32, 8, 128, 128, False), (37, 4, 1, 64, 64, True), (130, 7, 7, 128, 64, False), (5, 1, 3, 64, 16, True),
+    (9, 3, 0, 256, 96, False), (2, 2, 2, 16, 0, False)])
+def test_rope_matches_bit_for_bit(tv, n, Hq, Hkv, d, rot, inter, bf16):
+    rng = np.random.default_rng(n + rot)
+    table = ok.rope_table(200, rot) if rot else None
+    pos = rng.integers(0, 200, n).astype(np.int32)
+    (q, k, _), (hq, hk, _) = fused(rng, n, Hq, max(Hkv, 1), d, bf16)
+    k = k if Hkv else None
+    qo, ko, err = tv.tv_rope(q, k, dev(pos), dev(table), interleaved=inter)
+    assert int(err) == 0
+    assert np.array_equal(bits(qo), rounded(ok.rotate(hq, pos, table, inter), bf16))
+    if Hkv:
+        assert np.array_equal(bits(ko), rounded(ok.rotate(hk, pos, table, inter), bf16))
+
+
+def test_rope_skips_rows_with_a_bad_position(tv):
+    rng = np.random.default_rng(0)
+    (q, k, _), (hq, _, _) = fused(rng, 6, 4, 2, 64, True)
+    pos = np.array([0, -1, 7, 8, 2 ** 31 - 1, 3], np.int32)
+    table = ok.rope_table(8, 64)
+    out = tuple(torch.full((6, h, 64), 3.0, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    qo, ko, err = tv.tv_rope(q, k, dev(pos), dev(table), outputs=out)
+    assert int(err) == 1
+    good = [0, 2, 5]
+    assert np.array_equal(bits(qo)[good], rounded(ok.rotate(hq[good], pos[good], table, False), True))
+    bad = [1, 3, 4]
+    assert (qo[bad] == 3).all() and (ko[bad] == 3).all()
+
+
+# ------------------------------------------------------------ append, gather
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("P,H,d,lens,counts,rot,inter", [
+    (16, 2, 64, [0, 5, 31], [1, 40, 3], 64, False),
+    (64, 1, 128, [63, 64, 10], [1, 130, 0], 128, True),
+    (32, 3, 128, [17], [200], 64, False),
+    (128, 1, 64, [127, 3], [2, 1], 0, False)])
+def test_append_and_gather_match_bit_for_bit(tv, P, H, d, lens, counts, rot, inter, bf16):
+    rng = np.random.default_rng(P + d)
+    table, n_pages = tables(rng, [a + b for a, b in zip(lens, counts)], P)
+    cache = rng.integers(0, 256, (n_pages, H, P * (d + 4))).astype(np.uint8)   # stale codes everywhere
+    n = sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, n, 1, H, d, bf16)
+    rope = ok.rope_table(512, rot) if rot else None
+    want = cache.copy()
+    want_len = ok.append(want, P, table, lens, hk, hv, off, rope=rope, interleaved=inter)
+    c = dev(cache)
+    new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(np.array(lens, np.int32)), dev(off), max(counts),
+                                 rope=dev(rope), interleaved=inter)
+    assert int(err) == 0 and np.array_equal(host(new_len), want_len)
+    assert np.array_equal(host(c), want)
+    start = dev(np.array(lens, np.int32))
+    dt = torch.bfloat16 if bf16 else torch.float32
+    K, V, err = tv.kv4_gather(c, P, dev(table), dev(off), max(counts), start=start, total_rows=n, dtype=dt)
+    assert int(err) == 0
+    parts = ok.gather(want, P, table, lens, counts)
+    assert np.array_equal(bits(K), rounded(np.concatenate([p[0] for p in parts]), bf16))
+    assert np.array_equal(bits(V), rounded(np.concatenate([p[1] for p in parts]), bf16))
+
+
+def test_append_by_path_with_given_positions(tv):
+    rng = np.random.default_rng(3)
+    P, H, d, B, N = 16, 2, 128, 3, 7
+    lens = [15, 0, 30]
+    path = np.array([[0, 2, 3, 6, -1, 5], [-1, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4, 6]], np.int32)
+    table, n_pages = tables(rng, [40, 10, 40], P)
+    off = (np.arange(B + 1) * N).astype(np.int32)
+    pos = rng.integers(0, 100, B * N).astype(np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, B * N, 4, H, d, True)
+    rope = ok.rope_table(100, d)
+    for max_new in (6, 4):
+        cache = np.zeros((n_pages, H, P * (d + 4)), np.uint8)
+        want_len = ok.append(cache, P, table, lens, hk, hv, off, path[:, :max_new], pos, rope)
+        c = torch.zeros(cache.shape, dtype=torch.uint8, device="cuda")
+        new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(np.array(lens, np.int32)), dev(off), max_new,
+                                     path=dev(path), pos=dev(pos), rope=dev(rope))
+        assert int(err) == 0 and np.array_equal(host(new_len), want_len)
+        assert np.array_equal(host(c), cache)
+
+
+def test_append_rows_with_nan_infinity_zero_and_extreme_values(tv):
+    rng = np.random.default_rng(4)
+    P, H, d = 16, 1, 64
+    x = rng.standard_normal((8, H, d)).astype(np.float32)
+    x[0, 0, 5] = np.nan
+    x[1, 0, 60] = np.inf
+    x[2, 0, 0] = -np.inf
+    x[3] = 0
+    x[4] *= np.float32(1e-35)
+    x[5] *= np.float32(5e37)
+    x[6, 0] = np.linspace(-7, 7, d).round() / 2          # exact ties
+    table = np.array([[0]], np.int32)
+    cache = np.zeros((1, H, P * (d + 4)), np.uint8)
+    ok.append(cache, P, table, [2], x, x, [0, 8])
+    c = torch.zeros(cache.shape, dtype=torch.uint8, device="cuda")
+    _, err = tv.kv4_append(dev(x), dev(x), c, P, dev(table), dev(np.array([2], np.int32)),
+                           dev(np.array([0, 8], np.int32)), 8)
+    assert int(err) == 0
+    got, want = ok.read_block(host(c)[0, 0], P, d), ok.read_block(cache[0, 0], P, d)
+    for g, w in zip(got, want):
+        finite = ~np.isnan(w) if w.ndim == 1 else ~np.isnan(want[1])[:, None] & np.ones_like(w, bool)
+        assert np.array_equal(np.isnan(g), np.isnan(w)) and np.array_equal(g[finite], w[finite])
+
+
+def test_append_and_gather_skip_what_is_out_of_range(tv):
+    rng = np.random.default_rng(5)
+    P, H, d, B = 16, 1, 64, 4
+    lens = np.array([10, 30, -3, 5], np.int32)
+    counts = [20, 8, 4, 4]
+    table = np.array([[0, -1], [1, 2], [3, 4], [99, 5]], np.int32)    # a missing page, a short table, a page id too large
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, 36, 1, H, d, True)
+    before = rng.integers(0, 256, (6, H, P * (d + 4))).astype(np.uint8)
+    want = before.copy()
+    ok.append(want, P, table[[0, 1, 3]], lens[[0, 1, 3]], hk[[*range(28), *range(32, 36)]],
+              hv[[*range(28), *range(32, 36)]], [0, 20, 28, 32])
+    c = dev(before)
+    new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(lens), dev(off), 20)
+    assert int(err) == 1 and host(new_len).tolist()[:2] == [30, 38]
+    assert np.array_equal(host(c), want)
+    # a path that points outside the rows
+    path = np.array([[0, 1000, 2], [0, 1, -1], [0, 0, 0], [-1, 0, 0]], np.int32)
+    c = dev(before)
+    lens2 = np.array([0, 0, 0, 0], np.int32)
+    _, err = tv.kv4_append(k, v, c, P, dev(np.array([[0], [1], [2], [3]], np.int32)), dev(lens2), dev(off), 3,
+                           path=dev(path))
+    assert int(err) == 1
+    got = host(c)
+    want = before.copy()
+    ok.append(want, P, np.array([[1], [2]]), [0, 0], hk, hv, [20, 28, 36], path[1:3])
+    assert np.array_equal(got[1:], want[1:])
+    # gather: a bad page and a start past the table leave their rows as they were
+    for start, tbl in (([0, 16], [[0, -1], [1, 2]]), ([0, 28], [[0, 3], [1, 2]])):
+        K, V = (torch.full((32, H, d), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        _, _, err = tv.kv4_gather(dev(want), P, dev(np.array(tbl, np.int32)), dev(np.array([0, 24, 32], np.int32)), 24,
+                                  start=dev(np.array(start, np.int32)), outputs=(K, V))
+        assert int(err) == 1
+        w = ok.gather(want, P, np.array(tbl), [0], [16 if tbl[0][1] < 0 else 24])[0][0]
+        assert np.array_equal(bits(K)[:len(w)], rounded(w, True))
+        assert (K[len(w):24] == 9).all() and (tbl[0][1] < 0 or (K[28:] == 9).all())
+    K, V = (torch.full((32, H, d), 9.0, device="cuda") for _ in range(2))
+    _, _, err = tv.kv4_gather(dev(want), P, dev(table), dev(np.array([0, 8, 8, 8, 40], np.int32)), 40,
+                              outputs=(K, V))                        # out_off past the outputs
+    assert int(err) == 1 and (K[8:] == 9).all() and (K[:8] != 9).any()
+
+
+# ----------------------------------------------------------------- attention
+ATTN = [
+    # counts, lens, Hq, Hkv, d, P, kind, vis
+    ([1], [1], 1, 1, 128, 16, "chain", False),
+    ([1], [0], 4, 1, 64, 16, "chain", False),
+    ([1, 1, 1], [129, 5, 777], 32, 8, 128, 64, "chain", False),
+    ([16, 16], [200, 385], 8, 2, 128, 64, "chain", False),
+    ([60], [128], 4, 1, 64, 16, "random", False),
+    ([61, 3], [300, 0], 8, 2, 128, 128, "random", False),
+    ([113, 20, 1], [130, 128, 127], 4, 1, 128, 16, "random", True),
+    ([33], [512], 7, 1, 128, 32, "random", True),
+    ([9, 2], [1000, 255], 28, 4, 64, 64, "roots", True),
+    ([150], [140], 2, 2, 128, 32, "chain", True),
+    ([5], [260], 64, 1, 128, 16, "roots", False),
+    ([4, 4], [96, 17], 48, 1, 64, 32, "chain", False),
+]
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("counts,lens,Hq,Hkv,d,P,kind,vis", ATTN)
+def test_attention_matches_the_oracle(tv, counts, lens, Hq, Hkv, d, P, kind, vis, bf16):
+    c = Case(len(counts) * 1000 + lens[0], counts, lens, Hq, Hkv, d, P, bf16, kind, vis)
+    out, lse, err = c.run(tv)
+    assert int(err) == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_large_logits_and_scale(tv, bf16):
+    c = Case(7, [20, 3], [300, 140], 8, 2, 128, 64, bf16, scale=2.5)   # peaked softmax, growing maxima
+    out, lse, _ = c.run(tv)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_node_cnt_leaves_other_rows(tv, bf16):
+    c = Case(8, [16, 16, 9], [100, 300, 64], 8, 2, 128, 32, bf16, "chain", node_cnt=[5, 0, 9])
+    n = int(c.off[-1])
+    out = torch.full((n, 8, 128), 5.0, dtype=c.q.dtype, device="cuda")
+    lse = torch.full((n, 8), 5.0, device="cuda")
+    c.run(tv, out=out, lse=lse)
+    c.check(out, lse)
+    left = [i for i in range(n) if not (i < 5 or i >= 32)]
+    assert (out[left] == 5).all() and (lse[left] == 5).all()
+    without, none, _ = c.run(tv, want_lse=False)
+    assert none is None and torch.equal(without[:5], out[:5])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_rows_that_see_nothing(tv, bf16):
+    c = Case(9, [12, 6], [50, 0], 8, 2, 128, 16, bf16, "chain")
+    c.vis = np.zeros(18, np.int32)
+    c.vis[3] = 20
+    for i in (1, 3, 14):                       # no ancestor bits at all, not even the node itself
+        c.anc[i] = 0
+        c.see[i] = False
+    out, lse, _ = c.run(tv)
+    c.check(out, lse)
+    assert (out[[1, 14]] == 0).all() and torch.isneginf(lse[[1, 14]]).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_ignores_whatever_it_does_not_see(tv, bf16):
+    """NaN and infinities in tree rows that a node does not see, in rows of other requests, in rows beyond node_cnt,
+    and NaN scales behind the end of the cached tokens."""
+    c = Case(10, [24, 24, 10], [70, 129, 33], 8, 2, 128, 64, bf16, "random", node_cnt=[24, 12, 10])
+    clean = c.run(tv)
+    want = c.oracle()
+    d, P = c.d, c.P
+    for r, n in enumerate(c.lens):             # stale tokens: NaN scales, any codes
+        pg = c.table[r, n // P] if n % P else -1
+        if pg >= 0:
+            c.cache[pg, :, P * d + 2 * (n % P):P * d + 2 * P] = 0xFF
+            c.cache[pg, :, P * d + 2 * P + 2 * (n % P):] = 0xFF
+    poison = [24 + 12, 24 + 20, 47]            # nodes that node_cnt leaves out
+    for i, bad in zip(poison, (NAN, float("inf"), -float("inf"))):
+        c.k[i], c.v[i], c.q[i] = bad, bad, bad
+    leaf = 23                                  # the last node is nobody's ancestor
+    c.k[leaf], c.v[leaf] = NAN, NAN
+    out, lse, err = c.run(tv)
+    assert int(err) == 0
+    rows = [i for i in range(58) if i != leaf and not 36 <= i < 48]
+    assert torch.equal(out[rows], clean[0][rows]) and torch.equal(lse[rows], clean[1][rows])
+    assert torch.isnan(out[leaf]).all() and torch.isnan(lse[leaf]).all()
+    c.check(clean[0], clean[1], want)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_nan_and_infinity_reach_exactly_the_rows_that_see_them(tv, bf16):
+    c = Case(11, [10, 4], [40, 40], 8, 2, 128, 16, bf16, "chain")
+    clean = c.run(tv)
+    c.v[4, 1, 7] = float("inf")                # node 4 of request 0, KV head 1, dim 7
+    c.v[6, 0, 3] = NAN
+    out, lse, _ = c.run(tv)
+    exp = clean[0].clone()
+    exp[4:10, 4:, 7] = float("inf")
+    exp[6:10, :4, 3] = NAN
+    assert torch.equal(torch.isnan(out), torch.isnan(exp)) and torch.equal(torch.isinf(out), torch.isinf(exp))
+    ok_ = torch.isfinite(exp)
+    assert torch.equal(out[ok_], exp[ok_]) and torch.equal(lse, clean[1])
+    # a cached token whose row was not finite: every row that sees it is NaN
+    pg = c.table[1, 2]
+    c.cache[pg, 0, c.P * 128 + 2 * 3:c.P * 128 + 2 * 3 + 2] = [0xC0, 0x7F]
+    out, lse, _ = c.run(tv)
+    assert torch.isnan(out[10:, :4]).all() and torch.isnan(lse[10:, :4]).all()
+    assert torch.equal(out[10:, 4:], clean[0][10:, 4:])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_attention_bad_pages_are_not_visible(tv, bf16):
+    c = Case(12, [5, 5], [200, 90], 8, 2, 128, 32, bf16)
+    c.table[0, 2] = -1
+    c.table[1, 1] = 10 ** 6
+    c.page_ok = [np.arange(200) // 32 != 2, np.arange(90) // 32 != 1]
+    out, lse, err = c.run(tv)
+    assert int(err) == 1
+    c.check(out, lse)
+
+
+def test_attention_clamps_lengths(tv):
+    c = Case(13, [4, 4], [96, 64], 8, 2, 128, 32)
+    args = list(c.args())
+    c.table = c.table[:, :3].copy()
+    args[3] = dev(c.table)
+    args[4] = dev(np.array([1000, -7], np.int32))     # 3 pages of 32 hold 96 tokens
+    out, lse, err = tv.tree_verify_attn_kv4(*args)
+    assert int(err) == 1
+    c.lens = [96, 0]
+    c.check(out, lse)
+
+
+def test_attention_is_the_same_twice_on_another_stream_and_in_a_graph(tv):
+    c = Case(14, [16, 16, 1], [900, 1300, 40], 32, 8, 128, 64, True, "chain")
+    args, kw = c.args(), c.kwargs()
+    ws = [tv.tree_verify_attn_kv4_workspace(3, 16, 32, 8, 128) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    one = tv.tree_verify_attn_kv4(*args, **kw, ws=ws[0], err=err)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        two = tv.tree_verify_attn_kv4(*args, **kw, ws=ws[1], err=err)
+    three = tv.tree_verify_attn_kv4(*args, **kw, ws=ws[0], err=err)    # at the same time, in its own workspace
+    torch.cuda.synchronize()
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1]) and torch.equal(one[0], three[0])
+    out, lse = torch.empty_like(one[0]), torch.empty_like(one[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tv.tree_verify_attn_kv4(*args, **kw, out=out, lse=lse, ws=ws[0], err=err)
+    for lens in ([900, 1300, 40], [1, 129, 0], [640, 5, 33]):          # lengths change between replays
+        args[4].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        c.lens = lens
+        c.check(out, lse)
+    assert int(err) == 0 and int(ws[0][:4].view(torch.int32)) == 0
+
+
+def test_cache_offsets_pass_32_bits(tv):
+    """Pages behind the first 4 GB of the pool."""
+    P, H, d = 128, 8, 128
+    n_pages = 32500                            # 135168 bytes each: 4.39 GB
+    cache = torch.empty((n_pages, H, P * (d + 4)), dtype=torch.uint8, device="cuda")
+    c = Case(15, [3], [130], 32, H, d, P)
+    far = np.array([[n_pages - 1, n_pages - 3, -1]], np.int32)
+    for i in range(2):
+        cache[int(far[0, i])] = dev(c.cache[c.table[0, i]])
+    args = list(c.args())
+    args[1], args[3] = cache, dev(far)
+    out, lse, err = tv.tree_verify_attn_kv4(*args)
+    assert int(err) == 0
+    c.check(out, lse)
+    K, V, err = tv.kv4_gather(cache, P, dev(far), dev(np.array([0, 130], np.int32)), 130, total_rows=130)
+    want = c.prefix()[0]
+    assert np.array_equal(bits(K), rounded(want[0], True)) and np.array_equal(bits(V), rounded(want[1], True))
+    rng = np.random.default_rng(0)
+    (_, k, v), (_, hk, hv) = fused(rng, 6, 1, H, d, True)
+    tv.kv4_append(k, v, cache, P, dev(far), dev(np.array([126], np.int32)), dev(np.array([0, 6], np.int32)), 6)
+    K, V, err = tv.kv4_gather(cache, P, dev(far), dev(np.array([0, 6], np.int32)), 6,
+                              start=dev(np.array([126], np.int32)), total_rows=6)
+    assert np.array_equal(bits(K), rounded(ok.values(*ok.quantise(hk)), True))
+    assert np.array_equal(bits(V), rounded(ok.values(*ok.quantise(hv)), True))
+
+
+def test_gathered_prefix_feeds_the_contiguous_attention(tv):
+    """The same step over the 4-bit cache and over its gathered bf16 rows: the values are the same but for the rows'
+    rounding to bf16 (at most 2^-8 of each key and value)."""
+    c = Case(16, [16, 16], [300, 520], 32, 8, 128, 64, True, "chain")
+    out, lse, _ = c.run(tv)
+    off = np.concatenate([[0], np.cumsum(c.lens)]).astype(np.int32)
+    K, V, _ = tv.kv4_gather(dev(c.cache), c.P, dev(c.table), dev(off), max(c.lens), total_rows=int(off[-1]))
+    args = c.args()
+    o2, l2 = tv.tree_verify_attn(c.q.contiguous(), K, V, dev(off), c.k.contiguous(), c.v.contiguous(), dev(c.off),
+                                 args[8], 16, max(c.lens))
+    _, _, av, sa = c.oracle()
+    # keys off by 2^-8 move a score by 2^-8 sum|q k| and a weight by twice that relatively; values by 2^-8;
+    # both calls round weights and outputs to bf16
+    bound = av * (2 * 2.0 ** -8 * sa[..., None] + 5 * 2.0 ** -8)
+    assert (np.abs((out - o2).float().cpu().numpy()) <= bound + 1e-6).all()
+    assert (np.abs(host(lse) - host(l2)) <= 2.0 ** -8 * sa + 1e-4).all()
+
+
+# ------------------------------------------------------------ a run together
+@pytest.mark.parametrize("Hq,Hkv,d,P", [(8, 2, 128, 16), (4, 1, 64, 32)])
+def test_prompt_then_verification_steps(tv, Hq, Hkv, d, P):
+    """Prompts into the cache, then steps of: node positions, rotation, attention over the cache, acceptance, append
+    of the accepted path with the lengths kept on the device; the oracle keeps its own cache."""
+    rng = np.random.default_rng(d)
+    B, N, V, steps = 3, 12, 50, 4
+    prompt = [20, 1, 70]
+    table, n_pages = tables(rng, [p + steps * N for p in prompt], P, spare=0)
+    rope = ok.rope_table(256, d)
+    cache = np.zeros((n_pages, Hkv, P * (d + 4)), np.uint8)
+    c = torch.zeros(cache.shape, dtype=torch.uint8, device="cuda")
+    off = np.concatenate([[0], np.cumsum(prompt)]).astype(np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, int(off[-1]), Hq, Hkv, d, True)
+    zero = np.zeros(B, np.int32)
+    lens = ok.append(cache, P, table, zero, hk, hv, off, rope=rope)
+    dlen, err = tv.kv4_append(k, v, c, P, dev(table), dev(zero), dev(off), max(prompt), rope=dev(rope))
+    tab, dt = dev(table), dev(rope)
+    for step in range(steps):
+        par, noff, anc, see = forest(rng, [N] * B, "random")
+        (q, k, v), (hq, hk, hv) = fused(rng, B * N, Hq, Hkv, d, True)
+        tok = rng.integers(0, V, B * N).astype(np.int32)
+        amax = rng.integers(0, V, B * N).astype(np.int32)
+        for i in range(B * N):                 # most children carry their parent's choice
+            p = par[i]
+            if p >= 0 and rng.random() < 0.7:
+                tok[i] = amax[noff[i // N] + p]
+        depth, pos, danc, _, _ = tv.tv_tree_prep(dev(par), dev(noff), dlen, None, N)
+        rd, rpos, _, _ = otree.tree_prep(par, noff, lens)
+        assert np.array_equal(host(pos), rpos)
+        qr, kr, _ = tv.tv_rope(q, k, pos, dt, err=err)
+        out, lse, _ = tv.tree_verify_attn_kv4(qr, c, P, tab, dlen, kr, v, dev(noff), danc, N, err=err)
+        hqr = ok.f32(ok.bf16_bits(ok.rotate(hq, rpos, rope, False)))
+        hkr = ok.f32(ok.bf16_bits(ok.rotate(hk, rpos, rope, False)))
+        pre = ok.gather(cache, P, table, zero, lens)
+        o, l, av, sa = ok.attention(hqr, pre, hkr, hv, noff, see)
+        tol, ltol = ok.attention_tolerance(o, l, av, sa, d, True)
+        assert (np.abs(out.float().cpu().numpy() - o) <= tol).all() and (np.abs(host(lse) - l) <= ltol).all()
+        acc, _, path, _, _ = tv.accept_longest_path(dev(par), dev(tok), dev(amax), dev(noff), max_nodes=N)
+        # the cache takes the rotated rows; acceptance gives the path as it is
+        hpath = host(path)
+        lens = ok.append(cache, P, table, lens, hkr, hv, noff, hpath)
+        dlen, _ = tv.kv4_append(kr, v, c, P, tab, dlen, dev(noff), N, path=path, err=err)
+        assert np.array_equal(host(dlen), lens) and int(err) == 0
+        assert np.array_equal(host(c), cache)
