@@ -1,4 +1,6 @@
-// tree_verify_attn_kv4 entry point: host validation, workspace, dispatch.
+// tree_verify_attn_kv4 entry point: host validation, workspace, dispatch by type
+// (bf16 rows on the tensor cores, fp32 rows on the CUDA cores: their products
+// would lose bits in a bf16 MMA).
 #include "kv4.cuh"
 
 using namespace tv;
@@ -10,8 +12,8 @@ bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
 }  // namespace
 
 TV_API size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype) {
-  if (!shape_ok(B, max_nodes, Hq, Hkv, d) || B == 0 || max_nodes == 0) return 0;
-  return 256;
+  if (!shape_ok(B, max_nodes, Hq, Hkv, d) || B == 0 || max_nodes == 0 || Hq / Hkv > 64) return 0;
+  return dtype == TV_BF16 ? kv4::attn_tc_workspace(max_nodes, Hq, Hkv, d) : 256;
 }
 
 TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pages, int page_size,
@@ -47,6 +49,7 @@ TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, i
                         node_cnt, anc, vis_prefix, out, lse, err, ldq, ldk, ldv, n_pages, page_size, table_ld,
                         anc_words, B, max_nodes, total_nodes, Hq, Hkv, d, dtype, scale};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == TV_BF16) return kv4::attn_tc(a, ws, st);
   if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return TV_ECUDA;
   return kv4::attn_simt(a, st);
 }

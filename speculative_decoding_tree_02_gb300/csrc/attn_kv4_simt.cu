@@ -15,10 +15,7 @@
 namespace tv {
 namespace kv4 {
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
   constexpr int kDl = D / 32;            // dims per lane of the value product
   __shared__ float sq[D];
@@ -31,11 +28,10 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
   if (ln >= sp.cnt) return;
   const int gn = sp.n0 + ln, h = hq / (a.Hq / a.Hkv);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int raw = a.cache_len[r], len = prefix_len(a, r);
-  if (raw != len && a.err && threadIdx.x == 0) *a.err = 1;
+  const int len = prefix_len(a, r);
   const int vis = a.vis_prefix ? min(max(a.vis_prefix[gn], 0), len) : len;
-  const T* q = static_cast<const T*>(a.q) + gn * a.ldq + static_cast<int64_t>(hq) * D;
-  for (int i = threadIdx.x; i < D; i += 128) sq[i] = to_f32(q[i]);
+  const float* q = static_cast<const float*>(a.q) + gn * a.ldq + static_cast<int64_t>(hq) * D;
+  for (int i = threadIdx.x; i < D; i += 128) sq[i] = q[i];
   __syncthreads();
   const float c2 = a.scale * kLog2e;
   float m = -INFINITY, l = 0.f, o[kDl];
@@ -115,8 +111,8 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
     const bool seen = ((bits >> lane) & 1u) && j < sp.cnt;
     float x = 0.f;
     if (seen) {
-      const T* kr = static_cast<const T*>(a.k_tree) + (sp.n0 + j) * a.ldk + static_cast<int64_t>(h) * D;
-      for (int i = 0; i < D; ++i) x = fmaf(to_f32(kr[i]), sq[i], x);
+      const float* kr = static_cast<const float*>(a.k_tree) + (sp.n0 + j) * a.ldk + static_cast<int64_t>(h) * D;
+      for (int i = 0; i < D; ++i) x = fmaf(kr[i], sq[i], x);
       x *= c2;
     }
     const float p = weigh(x, seen);
@@ -125,9 +121,9 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
       const int t = __ffs(static_cast<int>(todo)) - 1;
       todo &= todo - 1;
       const float pt = __shfl_sync(0xffffffffu, p, t);
-      const T* vr = static_cast<const T*>(a.v_tree) + (sp.n0 + j0 + t) * a.ldv + static_cast<int64_t>(h) * D;
+      const float* vr = static_cast<const float*>(a.v_tree) + (sp.n0 + j0 + t) * a.ldv + static_cast<int64_t>(h) * D;
 #pragma unroll
-      for (int i = 0; i < kDl; ++i) o[i] = fmaf(pt, to_f32(vr[lane + 32 * i]), o[i]);
+      for (int i = 0; i < kDl; ++i) o[i] = fmaf(pt, vr[lane + 32 * i], o[i]);
     }
   }
 #pragma unroll
@@ -150,24 +146,15 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) acc = fmaf(f[w], so[w][i], acc);
     acc = L == 0.f ? 0.f : acc / L;
-    if constexpr (sizeof(T) == 4) {
-      static_cast<float*>(a.out)[at * D + i] = acc;
-    } else {
-      uint16_t b;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(acc));
-      static_cast<uint16_t*>(a.out)[at * D + i] = b;
-    }
+    static_cast<float*>(a.out)[at * D + i] = acc;
   }
   if (threadIdx.x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 int attn_simt(const AttnArgs& a, cudaStream_t st) {
   const dim3 grid(a.Hq, a.max_nodes, a.B);
-  if (a.dtype == TV_BF16)
-    return a.d == 128 ? launch_pdl(attn_simt_kernel<uint16_t, 128>, grid, dim3(128), 0, st, a)
-                      : launch_pdl(attn_simt_kernel<uint16_t, 64>, grid, dim3(128), 0, st, a);
-  return a.d == 128 ? launch_pdl(attn_simt_kernel<float, 128>, grid, dim3(128), 0, st, a)
-                    : launch_pdl(attn_simt_kernel<float, 64>, grid, dim3(128), 0, st, a);
+  return a.d == 128 ? launch_pdl(attn_simt_kernel<128>, grid, dim3(128), 0, st, a)
+                    : launch_pdl(attn_simt_kernel<64>, grid, dim3(128), 0, st, a);
 }
 
 }  // namespace kv4

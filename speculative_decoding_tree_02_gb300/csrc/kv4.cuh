@@ -95,11 +95,14 @@ __device__ __forceinline__ Span node_span(const AttnArgs& a, int r) {
 }
 __device__ __forceinline__ int prefix_len(const AttnArgs& a, int r) {
   const int cap = a.table_ld * a.page_size;
-  const int len = a.cache_len[r];
-  return min(max(len, 0), cap);
+  const int raw = a.cache_len[r], len = min(max(raw, 0), cap);
+  if (raw != len && a.err) *a.err = 1;
+  return len;
 }
 
-int attn_simt(const AttnArgs& a, cudaStream_t st);
+int attn_simt(const AttnArgs& a, cudaStream_t st);            // fp32 rows
+int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st);    // bf16 rows
+size_t attn_tc_workspace(int max_nodes, int Hq, int Hkv, int d);
 
 }  // namespace kv4
 }  // namespace tv
