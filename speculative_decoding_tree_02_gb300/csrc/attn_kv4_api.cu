@@ -9,11 +9,14 @@ namespace {
 bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
   return B >= 0 && max_nodes >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && (d == 64 || d == 128);
 }
+bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 32; }
 }  // namespace
 
 TV_API size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype) {
   if (!shape_ok(B, max_nodes, Hq, Hkv, d) || B == 0 || max_nodes == 0 || Hq / Hkv > 64) return 0;
-  return dtype == TV_BF16 ? kv4::attn_tc_workspace(max_nodes, Hq, Hkv, d) : 256;
+  if (dtype != TV_BF16) return 256;
+  return few_rows(max_nodes, Hq, Hkv) ? kv4::attn_mma_workspace(B, max_nodes, Hq, Hkv, d)
+                                      : kv4::attn_tc_workspace(B, max_nodes, Hq, Hkv, d);
 }
 
 TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pages, int page_size,
@@ -49,7 +52,7 @@ TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, i
                         node_cnt, anc, vis_prefix, out, lse, err, ldq, ldk, ldv, n_pages, page_size, table_ld,
                         anc_words, B, max_nodes, total_nodes, Hq, Hkv, d, dtype, scale};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == TV_BF16) return kv4::attn_tc(a, ws, st);
+  if (dtype == TV_BF16) return few_rows(max_nodes, Hq, Hkv) ? kv4::attn_mma(a, ws, st) : kv4::attn_tc(a, ws, st);
   if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return TV_ECUDA;
   return kv4::attn_simt(a, st);
 }

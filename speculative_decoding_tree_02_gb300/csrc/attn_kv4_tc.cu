@@ -35,7 +35,7 @@
 #include <algorithm>
 
 #include "kv4.cuh"
-#include "tc_common.cuh"
+#include "kv4_device.cuh"
 
 namespace tv {
 namespace kv4 {
@@ -45,24 +45,22 @@ using namespace tc;
 
 constexpr int kKeys = 128;        // keys per tile
 constexpr int kStages = 6;        // staged tiles
-constexpr float kLow = -3.3895314e38f;   // reference of a row that has seen nothing
 
 enum Bar { RAW_FULL = 0, RAW_EMPTY = RAW_FULL + kStages, K_FULL = RAW_EMPTY + kStages, V_FULL = K_FULL + 2,
            S_FULL = V_FULL + 2, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2, PV_DONE = P_FULL + 2, DRAIN = PV_DONE + 2,
            N_BARS = DRAIN + 1 };
 
 // What the producer says about a staged tile.
-struct Tile {
-  int kind;          // kPrefix, kTree, kEnd
-  int flags;         // 1: first of its unit's run, 2: last
-  int r, t, h;       // request, row tile, KV head
-  int n0, cnt;       // first node of the request, nodes
+struct alignas(16) Tile {
+  int flags;         // kFirst ..
   int key0, nkeys;   // first token (node) of the tile, how many
   int groups;        // bit i: the page of tokens 16 i .. 16 i + 15 of the tile is staged
+  int r, t, h;       // request, row tile, KV head
   int seg;           // running number of the unit in this CTA
+  int n0, cnt;       // first node of the request, nodes
   int slot;          // -1: the whole unit is here; else its partial slot
 };
-enum { kPrefix = 0, kTree = 1, kEnd = 2 };
+enum { kFirst = 1, kLast = 2, kTree = 4, kEnd = 8 };   // first, last tile of its unit's run here; tree nodes; no more
 
 template <int D, int N>
 struct Lay {
@@ -73,6 +71,13 @@ struct Lay {
   static constexpr int kProd = kMma + 1;
   static constexpr int kWarps = kProd + 1;
   static constexpr int kThreads = 32 * kWarps;
+  // Registers a thread: the compiler's share at launch (65536 over warps that
+  // come four to a scheduler), what the dequantising warps give up and what
+  // the softmax warps take.
+  static constexpr int kLaunchRegs = kWarps <= 16 ? 128 : 96;
+  static constexpr int kConvRegs = kWarps <= 16 ? 80 : 56;
+  static constexpr int kSoftRegs = kWarps <= 16 ? 192 : 136;
+  static_assert(8 * kConvRegs + 4 * kGroups * kSoftRegs + 2 * kLaunchRegs <= kWarps * kLaunchRegs, "register split");
   static constexpr uint32_t kStage = kKeys * (D + 4);
   static constexpr uint32_t kQHalf = N * 128;                 // N rows x 64 dims
   static constexpr uint32_t kQ = 0;                           // two buffers
@@ -92,7 +97,7 @@ struct Lay {
   static constexpr uint32_t kWarpMax = kAnc + 16 * N;                     // [groups][4][32]
   static constexpr uint32_t kSums = kWarpMax + 512 * kGroups;             // long long [kWarps]
   static constexpr uint32_t kBytes = kSums + 8 * kWarps + 1024;           // + alignment slack
-  static_assert(sizeof(Tile) <= 64 && N_BARS <= 32 && kRef % 16 == 0 && kSums % 8 == 0, "layout");
+  static_assert(sizeof(Tile) == 48 && N_BARS <= 32 && kRef % 16 == 0 && kSums % 8 == 0, "layout");
   // tensor memory: K0 K1 V0 V1 (64 columns each), S0 S1 (N each), O (N)
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t tK = 0, tV = 128, tS = 256, tO = 256 + 2 * N;
@@ -104,15 +109,10 @@ struct TcArgs {
   int4* desc;        // [grid] pieces of the unit that starts in a CTA and ends in another
   float2* ml;        // [2 grid][N]
   float* o;          // [2 grid][N][D]
+  const int4* extents;   // [B * tiles] from extent_kernel, or NULL
   int nq, tiles, grid;
-  int by_node;       // a unit's key range depends on its nodes (per-node prefixes, several tree tiles)
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -139,54 +139,41 @@ __device__ __forceinline__ bool wg_any(int id, bool p) {
       : "memory");
   return r != 0;
 }
-// Eight codes -> four bf16 pairs (items 2i, 2i + 1) of n = code - 8, exact.
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t* r) {
-  const uint32_t bias = 0x43084308u;   // bf16 136, 136
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;   // bf16 128 + code
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&bias));
-    r[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-// Key tiles of a unit: prefix tiles over the tokens that any of its rows sees,
-// then tree tiles from the lowest visible ancestor on.
+// Key tiles of a row tile (entry = request x row tile): prefix tiles over the
+// tokens that any of its rows sees, then tree tiles from the lowest visible
+// node on.  They follow from the lengths alone unless nodes have prefixes of
+// their own or the tree spans several key tiles; then extent_kernel works them
+// out first.
 struct Extent {
-  int n0, cnt, len;       // nodes of the request, visible prefix of the row tile
-  int np, t0, nt;         // prefix tiles, first tree tile, tree tiles
+  int len, np, t0, nt;    // visible prefix, prefix tiles, first tree tile, tree tiles
 };
-__device__ __forceinline__ Extent extent_plain(const TcArgs& p, int e) {
-  Extent x;
-  const int r = e / p.tiles, t = e % p.tiles;
-  const Span s = node_span(p.a, r);
-  x.n0 = s.n0;
-  x.cnt = s.cnt;
-  x.len = prefix_len(p.a, r);
-  const bool live = t * p.nq < s.cnt;
-  x.np = live ? (x.len + kKeys - 1) / kKeys : 0;
-  x.t0 = 0;
-  x.nt = live ? 1 : 0;
-  return x;
-}
-// One entry by a whole warp, lanes = nodes.
-__device__ __forceinline__ Extent extent_by_node(const TcArgs& p, int e, int lane) {
-  Extent x;
-  const int r = e / p.tiles, t = e % p.tiles;
-  const Span s = node_span(p.a, r);
-  x.n0 = s.n0;
-  x.cnt = s.cnt;
+__device__ __forceinline__ Extent extent_of(const TcArgs& p, int e) {
+  if (p.extents) {
+    const int4 v = p.extents[e];
+    return Extent{v.x, (v.x + kKeys - 1) / kKeys, v.y, v.z};
+  }
+  const int r = e / p.tiles;
+  const bool live = e % p.tiles * p.nq < node_span(p.a, r).cnt;
   const int len = prefix_len(p.a, r);
-  const int first = t * p.nq, last = min(first + p.nq, s.cnt);
+  return Extent{len, live ? (len + kKeys - 1) / kKeys : 0, 0, live ? 1 : 0};
+}
+// One warp per entry, lanes = nodes.
+__global__ void __launch_bounds__(128) extent_kernel(const AttnArgs a, int nq, int tiles, int4* out) {
+  griddep_wait();
+  griddep_release();
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (e >= a.B * tiles) return;
+  const int r = e / tiles, first = e % tiles * nq;
+  const Span s = node_span(a, r);
+  const int len = prefix_len(a, r), last = min(first + nq, s.cnt);
   int vis = 0, lo = 1 << 30, hi = -1;           // 64-node words of the masks that are not empty
   for (int i = first + lane; i < last; i += 32) {
-    vis = max(vis, p.a.vis_prefix ? min(max(p.a.vis_prefix[s.n0 + i], 0), len) : len);
-    const uint64_t* row = p.a.anc + static_cast<int64_t>(s.n0 + i) * p.a.anc_words;
-    for (int w0 = 0; w0 < p.a.anc_words; w0 += 8) {
+    vis = max(vis, a.vis_prefix ? min(max(a.vis_prefix[s.n0 + i], 0), len) : len);
+    const uint64_t* row = a.anc + static_cast<int64_t>(s.n0 + i) * a.anc_words;
+    for (int w0 = 0; w0 < a.anc_words; w0 += 8) {
       uint64_t v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = w0 + k < p.a.anc_words ? row[w0 + k] : 0ull;
+      for (int k = 0; k < 8; ++k) v[k] = w0 + k < a.anc_words ? row[w0 + k] : 0ull;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (v[k]) {
@@ -195,35 +182,20 @@ __device__ __forceinline__ Extent extent_by_node(const TcArgs& p, int e, int lan
         }
     }
   }
-  x.len = __reduce_max_sync(0xffffffffu, vis);
+  vis = __reduce_max_sync(0xffffffffu, vis);
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   const bool live = first < s.cnt;
-  x.np = live ? (x.len + kKeys - 1) / kKeys : 0;
-  // at least one tile for a live unit: its rows are written even if they see nothing
+  // at least one tile for a live entry: its rows are written even if they see nothing
   const int top = live ? (s.cnt - 1) / kKeys : 0;
-  x.t0 = min(lo / 2, top);
-  x.nt = live ? max(0, min(hi / 2, top) - x.t0) + 1 : 0;
-  return x;
+  const int t0 = min(lo / 2, top), nt = live ? max(0, min(hi / 2, top) - t0) + 1 : 0;
+  if (lane == 0) out[e] = make_int4(live ? vis : 0, t0, nt, 0);
 }
-__device__ __forceinline__ Extent extent_of(const TcArgs& p, int e, int lane) {
-  return p.by_node ? extent_by_node(p, e, lane) : extent_plain(p, e);
-}
-// Tiles of entries e0 + lane (all KV heads of each), 0 past the end.
-__device__ __forceinline__ long long entry_tiles(const TcArgs& p, int e0, int end, int lane) {
-  long long mine = 0;
-  if (!p.by_node) {
-    if (e0 + lane < end) {
-      const Extent x = extent_plain(p, e0 + lane);
-      mine = x.np + x.nt;
-    }
-  } else {
-    for (int i = 0; i < 32 && e0 + i < end; ++i) {
-      const Extent x = extent_by_node(p, e0 + i, lane);
-      if (lane == i) mine = x.np + x.nt;
-    }
-  }
-  return mine * p.a.Hkv;
+// Tiles of entry e, all KV heads; 0 past the end.
+__device__ __forceinline__ long long entry_tiles(const TcArgs& p, int e, int end) {
+  if (e >= end) return 0;
+  const Extent x = extent_of(p, e);
+  return static_cast<long long>(x.np + x.nt) * p.a.Hkv;
 }
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -272,12 +244,11 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
 
   // ---- this CTA's run: tiles [w0, w1) of the list of all units
   const int E = a.B * p.tiles;
-  const int per = p.by_node ? (E + L::kWarps - 1) / L::kWarps           // entries per warp
-                            : ((E + L::kWarps - 1) / L::kWarps + 31) / 32 * 32;
+  const int per = ((E + L::kWarps - 1) / L::kWarps + 31) / 32 * 32;     // entries per warp
   const int e_lo = min(warp * per, E), e_hi = min(e_lo + per, E);
   {
     long long s = 0;
-    for (int e = e_lo; e < e_hi; e += 32) s += entry_tiles(p, e, e_hi, lane);
+    for (int e = e_lo; e < e_hi; e += 32) s += entry_tiles(p, e + lane, e_hi);
     s = warp_sum_ll(s);
     if (lane == 0) sums[warp] = s;
   }
@@ -296,7 +267,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
   if (work && w0 >= before && w0 < before + sums[warp]) {   // this warp's entries hold the first tile
     long long at = before;
     for (int e = e_lo; e < e_hi; e += 32) {
-      const long long c = entry_tiles(p, e, e_hi, lane);
+      const long long c = entry_tiles(p, e + lane, e_hi);
       long long x = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -329,105 +300,98 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
     // ================= producer
     int e = static_cast<int>(start[0]);
     long long pos = w0;
-    Extent x = extent_of(p, e, lane);
+    Extent x = extent_of(p, e);
     int nb = x.np + x.nt;
-    long long off = w0 - start[1];
+    const long long off = w0 - start[1];
     int h = static_cast<int>(off / nb), blk = static_cast<int>(off % nb);
     int seg = 0, seg_blk = blk;                  // first tile of the running unit in this CTA
     const int per_tile = kKeys >> ps_shift;      // pages of a tile
-    const int end_of_list = E;
     int issued = 0;
-    bool ok = true;
-    // the next tile, and this lane's page of it
-    Tile nx;
-    int npage;
-    auto gen = [&]() {
-      npage = -1;
-      if (pos >= w1) {
-        nx.kind = kEnd;
-        nx.flags = 0;
-        return;
-      }
-      while (blk == nb) {                        // next unit
-        blk = 0;
-        ++seg;
-        if (++h == a.Hkv) {
-          h = 0;
-          do {
-            ++e;
-            x = extent_of(p, e, lane);
-            nb = x.np + x.nt;
-          } while (nb == 0 && e + 1 < end_of_list);
+    // Pass it works out tile it and asks for its pages' numbers, then issues
+    // tile it - 1, whose numbers have arrived meanwhile.
+    Tile cur, nx;
+    int page = -1, npage = -1;
+    cur.flags = nx.flags = 0;
+    for (int it = 0;; ++it) {
+      if (!(nx.flags & kEnd)) {
+        npage = -1;
+        if (pos >= w1) {
+          nx.flags = kEnd;
+        } else {
+          if (blk == nb) {                       // next unit
+            blk = seg_blk = 0;
+            ++seg;
+            if (++h == a.Hkv) {
+              h = 0;
+              do {
+                x = extent_of(p, ++e);
+                nb = x.np + x.nt;
+              } while (nb == 0 && e + 1 < E);
+            }
+          }
+          nx.r = e / p.tiles;
+          nx.t = e % p.tiles;
+          const Span sp = node_span(a, nx.r);
+          const bool tree = blk >= x.np;
+          nx.h = h;
+          nx.n0 = sp.n0;
+          nx.cnt = sp.cnt;
+          nx.seg = seg;
+          const bool last = blk == nb - 1 || pos == w1 - 1;
+          const bool whole = seg_blk == 0 && pos + (nb - 1 - blk) < w1;
+          nx.flags = (blk == seg_blk ? kFirst : 0) | (last ? kLast : 0) | (tree ? kTree : 0);
+          nx.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (seg_blk == 0 ? 1 : 0);
+          if (!tree) {
+            nx.key0 = blk * kKeys;
+            nx.nkeys = min(kKeys, x.len - nx.key0);
+            if (lane < per_tile && (lane << ps_shift) < nx.nkeys)
+              npage = a.block_table[static_cast<int64_t>(nx.r) * a.table_ld + (nx.key0 >> ps_shift) + lane];
+          } else {
+            nx.key0 = (x.t0 + blk - x.np) * kKeys;
+            nx.nkeys = min(kKeys, sp.cnt - nx.key0);
+          }
+          if (last && blk != nb - 1 && seg_blk == 0 && lane == 0) {
+            // a unit that starts here and goes on: its pieces, for the joining kernel
+            const long long u1 = pos + (nb - blk);           // position after the unit
+            const long long k = (u1 * G + W - 1) / W - 1;    // CTA of its last tile
+            p.desc[blockIdx.x] = make_int4(static_cast<int>(k) - static_cast<int>(blockIdx.x) + 1, nx.r, nx.t, h);
+          }
+          ++blk;
+          ++pos;
         }
-        seg_blk = 0;
       }
-      nx.kind = blk < x.np ? kPrefix : kTree;
-      nx.r = e / p.tiles;
-      nx.t = e % p.tiles;
-      nx.h = h;
-      nx.n0 = x.n0;
-      nx.cnt = x.cnt;
-      nx.seg = seg;
-      const bool last = blk == nb - 1 || pos == w1 - 1;
-      const bool whole = seg_blk == 0 && pos + (nb - 1 - blk) < w1;
-      nx.flags = (blk == seg_blk ? 1 : 0) | (last ? 2 : 0);
-      nx.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (seg_blk == 0 ? 1 : 0);
-      if (nx.kind == kPrefix) {
-        nx.key0 = blk * kKeys;
-        nx.nkeys = min(kKeys, x.len - nx.key0);
-        if (lane < per_tile && (lane << ps_shift) < nx.nkeys)
-          npage = a.block_table[static_cast<int64_t>(nx.r) * a.table_ld + (nx.key0 >> ps_shift) + lane];
-      } else {
-        nx.key0 = (x.t0 + blk - x.np) * kKeys;
-        nx.nkeys = min(kKeys, x.cnt - nx.key0);
-      }
-      if (blk == nb - 1 || pos == w1 - 1) {
-        // the unit that starts here and goes on: its pieces, for the joining kernel
-        if (seg_blk == 0 && blk != nb - 1 && lane == 0) {
-          const long long u1 = pos + (nb - blk);            // position after the unit
-          const long long k = (u1 * G + W - 1) / W - 1;     // CTA of its last tile
-          p.desc[blockIdx.x] = make_int4(static_cast<int>(k) - static_cast<int>(blockIdx.x) + 1, nx.r, nx.t, h);
+      if (it > 0) {
+        const int i = it - 1, st = i % kStages;
+        if (i >= kStages && !warp_wait(bar(RAW_EMPTY + st), ((i / kStages) - 1) & 1, abort_flag, err, 41)) break;
+        const bool wanted = !(cur.flags & (kTree | kEnd)) && lane < per_tile && (lane << ps_shift) < cur.nkeys;
+        const bool good = wanted && page >= 0 && page < a.n_pages;
+        if (wanted && !good && a.err) *a.err = 1;
+        const unsigned have = __ballot_sync(0xffffffffu, good);
+        if (lane == 0) {
+          Tile* t = reinterpret_cast<Tile*>(sm + L::kTiles + 64 * st);
+          cur.groups = 0;
+          for (int gr = 0; gr < 8; ++gr) cur.groups |= ((have >> ((16 * gr) >> ps_shift)) & 1) << gr;
+          *t = cur;
+          if (have)
+            mbar_expect_tx(bar(RAW_FULL + st), __popc(have) * blk_bytes);
+          else
+            mbar_arrive(bar(RAW_FULL + st));
         }
+        __syncwarp();
+        if (good)
+          bulk_load(sb + L::kRaw + st * L::kStage + lane * blk_bytes,
+                    a.cache + (static_cast<int64_t>(page) * a.Hkv + cur.h) * blk_bytes, blk_bytes, bar(RAW_FULL + st));
+        issued = it;
+        if (cur.flags & kEnd) break;
       }
-      ++blk;
-      ++pos;
-    };
-    gen();
-    for (int it = 0; ok; ++it) {
-      const Tile cur = nx;
-      const int page = npage;
-      if (cur.kind != kEnd) gen();
-      const int st = it % kStages;
-      if (it >= kStages)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(RAW_EMPTY + st), ((it / kStages) - 1) & 1, abort_flag, err, 41));
-      if (!ok) break;
-      const bool wanted = cur.kind == kPrefix && lane < per_tile && (lane << ps_shift) < cur.nkeys;
-      const bool good = wanted && page >= 0 && page < a.n_pages;
-      if (wanted && !good && a.err) *a.err = 1;
-      const unsigned have = __ballot_sync(0xffffffffu, good);
-      if (lane == 0) {
-        Tile* t = reinterpret_cast<Tile*>(sm + L::kTiles + 64 * st);
-        *t = cur;
-        int groups = 0;
-        for (int i = 0; i < 8; ++i) groups |= ((have >> ((16 * i) >> ps_shift)) & 1) << i;
-        t->groups = groups;
-        if (have)
-          mbar_expect_tx(bar(RAW_FULL + st), __popc(have) * blk_bytes);
-        else
-          mbar_arrive(bar(RAW_FULL + st));
-      }
-      __syncwarp();
-      if (good)
-        bulk_load(sb + L::kRaw + st * L::kStage + lane * blk_bytes,
-                  a.cache + (static_cast<int64_t>(page) * a.Hkv + cur.h) * blk_bytes, blk_bytes, bar(RAW_FULL + st));
-      issued = it + 1;
-      if (cur.kind == kEnd) break;
+      cur = nx;
+      page = npage;
     }
     // after an expired wait: copies in flight land before the CTA ends
     if (*abort_flag) {
       for (int it = max(0, issued - kStages); it < issued; ++it) {
-        const uint64_t t0 = gtime();
-        while (!mbar_try(bar(RAW_FULL + it % kStages), (it / kStages) & 1) && gtime() - t0 < kTimeoutNs) {
+        const long long t0 = clock64();
+        while (!mbar_try(bar(RAW_FULL + it % kStages), (it / kStages) & 1) && clock64() - t0 < kWaitClocks) {
         }
       }
     }
@@ -438,13 +402,14 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
       constexpr uint32_t idO = idesc_bf16(128, N, 1);
       int ns = 0, npv = 0, total = -1;
       uint32_t firsts = 0;                       // bit j & 7: tile j is the first of its unit
-      uint64_t since = 0;
+      uint32_t idle = 0;                         // polls without progress
+      long long since = 0;
       bool ok = true;
       while (ok && (total < 0 || npv < total)) {
         bool prog = false;
         if (total < 0 && mbar_test(bar(RAW_FULL + ns % kStages), (ns / kStages) & 1)) {
           const Tile& t = tile_at(ns % kStages);
-          if (t.kind == kEnd) {
+          if (t.flags & kEnd) {
             total = ns;
             prog = true;
           } else if (mbar_test(bar(K_FULL + (ns & 1)), (ns >> 1) & 1) &&
@@ -456,7 +421,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
               umma_bf16_ts(tmem + L::tS + N * (ns & 1), tmem + L::tK + 64 * (ns & 1) + 8 * kk,
                            sdesc(q + (kk >> 2) * L::kQHalf + (kk & 3) * 32, 16, 1024), idS, kk > 0);
             umma_commit(bar(S_FULL + (ns & 1)));
-            firsts = (firsts & ~(1u << (ns & 7))) | (static_cast<uint32_t>(t.flags & 1) << (ns & 7));
+            firsts = (firsts & ~(1u << (ns & 7))) | (static_cast<uint32_t>(t.flags & kFirst) << (ns & 7));
             mbar_arrive(bar(RAW_EMPTY + ns % kStages));
             ++ns;
             prog = true;
@@ -475,29 +440,40 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
           ++npv;
           prog = true;
         }
-        if (prog) since = 0;
-        else if (!still_waiting(since, abort_flag, err, 42)) ok = false;
+        if (prog) {
+          idle = 0;
+        } else if ((++idle & 255) == 0) {
+          if (idle == 256) since = clock64();
+          if (*abort_flag) {
+            ok = false;
+          } else if (clock64() - since > kWaitClocks) {
+            *abort_flag = 1;
+            atomicExch(err, 42);
+            ok = false;
+          }
+        }
       }
       umma_commit(bar(DRAIN));
-      mbar_wait(bar(DRAIN), 0, abort_flag, err, 43);
+      if (!mbar_try(bar(DRAIN), 0)) wait_slow(bar(DRAIN), 0, abort_flag, err, 43);
     }
   } else if (warp < 4) {
     // ================= keys: thread = key
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kConvRegs));
     for (int it = 0;; ++it) {
       const int st = it % kStages, b = it & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 44))) break;
+      if (!warp_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 44)) break;
       const Tile& t = tile_at(st);
-      const int kind = t.kind;
-      if (kind == kEnd) break;
-      const bool first = t.flags & 1;
+      const int flags = t.flags;
+      if (flags & kEnd) break;
       // S(it - 2) has read this K buffer, and every S of the unit before last its Q buffer
       if (it >= 2 &&
-          !__all_sync(0xffffffffu, mbar_wait(bar(S_FULL + b), ((it >> 1) - 1) & 1, abort_flag, err, 45)))
+          !warp_wait(bar(S_FULL + b), ((it >> 1) - 1) & 1, abort_flag, err, 45))
         break;
       tc_fence_after();
-      if (first) {
+      if (flags & kFirst) {
         uint8_t* qs = sm + L::kQ + (t.seg & 1) * L::kQBytes;
         const int node0 = t.t * p.nq, rows = min(p.nq, t.cnt - node0) * g;
+#pragma unroll 2
         for (int i = threadIdx.x; i < N * (D / 8); i += 128) {
           const int rr = i / (D / 8), c = i % (D / 8);
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -510,28 +486,29 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       const uint32_t dst = tmem + L::tK + 64 * b + lane_off;
-      if (kind == kPrefix) {
+      if (!(flags & kTree)) {
         const uint8_t* blk = raw + st * L::kStage + (own >> ps_shift) * blk_bytes;
         const int slot = own & (a.page_size - 1);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(blk + ((2 * c + i) * a.page_size + slot) * 16);
-            decode8(w.x, r + 16 * i);
-            decode8(w.y, r + 16 * i + 4);
-            decode8(w.z, r + 16 * i + 8);
-            decode8(w.w, r + 16 * i + 12);
-          }
-          tmem_st32(dst + 32 * c, r);
+        const uint4* from = reinterpret_cast<const uint4*>(blk + slot * 16);
+        uint4 w = *from;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {       // rolled: the roles share the instruction caches
+          uint32_t r[16];
+          const uint4 now = w;
+          from += a.page_size;
+          if (c + 1 < D / 32) w = *from;
+          decode8(now.x, r);
+          decode8(now.y, r + 4);
+          decode8(now.z, r + 8);
+          decode8(now.w, r + 12);
+          tmem_st16(dst + 16 * c, r);
         }
       } else {
         const bool live = own < t.nkeys;
         const uint16_t* row = static_cast<const uint16_t*>(a.k_tree) +
                               static_cast<int64_t>(t.n0 + t.key0 + (live ? own : 0)) * a.ldk +
                               static_cast<int64_t>(t.h) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t r[32];
 #pragma unroll
@@ -552,33 +529,40 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
     }
   } else if (warp < 8) {
     // ================= values: thread = dim
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kConvRegs));
     for (int it = 0;; ++it) {
       const int st = it % kStages, b = it & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 46))) break;
+      if (!warp_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 46)) break;
       const Tile& t = tile_at(st);
-      const int kind = t.kind;
-      if (kind == kEnd) break;
+      const int flags = t.flags;
+      if (flags & kEnd) break;
       if (it >= 2 &&
-          !__all_sync(0xffffffffu, mbar_wait(bar(PV_DONE + b), ((it >> 1) - 1) & 1, abort_flag, err, 47)))
+          !warp_wait(bar(PV_DONE + b), ((it >> 1) - 1) & 1, abort_flag, err, 47))
         break;
       tc_fence_after();
       const uint32_t dst = tmem + L::tV + 64 * b + lane_off;
       if (32 * (warp & 3) < D) {                 // d = 64: the upper lanes' results are not used
-        if (kind == kPrefix) {
+        if (!(flags & kTree)) {
           const uint8_t* base = raw + st * L::kStage + a.page_size * (D / 2) + own * 8;
           const int gshift = ps_shift - 4;       // groups of 16 tokens per page
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int gr = 4 * c + i;
-              const uint2 w = *reinterpret_cast<const uint2*>(base + (gr >> gshift) * blk_bytes +
-                                                              (gr & ((1 << gshift) - 1)) * (D * 8));
-              decode8(w.x, r + 8 * i);
-              decode8(w.y, r + 8 * i + 4);
+          auto word = [&](int gr) {
+            return *reinterpret_cast<const uint2*>(base + (gr >> gshift) * blk_bytes +
+                                                   (gr & ((1 << gshift) - 1)) * (D * 8));
+          };
+          uint2 w0 = word(0), w1 = word(1);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16];
+            const uint2 a0 = w0, a1 = w1;
+            if (c < 3) {
+              w0 = word(2 * c + 2);
+              w1 = word(2 * c + 3);
             }
-            tmem_st32(dst + 32 * c, r);
+            decode8(a0.x, r);
+            decode8(a0.y, r + 4);
+            decode8(a1.x, r + 8);
+            decode8(a1.y, r + 12);
+            tmem_st16(dst + 16 * c, r);
           }
         } else {
           // a value that is not finite must not meet the zero weights of rows that do not see it: it is taken
@@ -594,7 +578,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int k0 = 32 * c + 2 * i;
-              uint32_t lo = 0u, hi = 0u;
+              uint32_t lo = 0u, hi = 0u;         // (a part without nodes is stored as zeros)
               if (k0 < nk) lo = *from;
               from += a.ldv;
               if (k0 + 1 < nk) hi = *from;
@@ -618,27 +602,30 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
     }
   } else {
     // ================= softmax: thread = key, columns = rows c0 .. c0 + C - 1 of the row tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftRegs));
     const int wg = (warp - L::kSoft0) >> 2, wid = 1 + wg;
     const int c0 = wg * C;
     const float c2 = a.scale * kLog2e;
-    float* ref = reinterpret_cast<float*>(sm + L::kRef);        // [2][N]
-    float* corr_s = reinterpret_cast<float*>(sm + L::kCorr);
-    float* inv_s = reinterpret_cast<float*>(sm + L::kInv);
-    int* vis_s = reinterpret_cast<int*>(sm + L::kVis);
-    int* row_s = reinterpret_cast<int*>(sm + L::kRow);
-    uint32_t* anc_s = reinterpret_cast<uint32_t*>(sm + L::kAnc);   // [4][N]
+    // a row's reference (what its scores are taken over) is kept negated; -0 (and a row sum of 0): none yet
+    float* nref = reinterpret_cast<float*>(sm + L::kRef) + c0;
+    float* shift_s = nref + N;
+    float* corr_s = reinterpret_cast<float*>(sm + L::kCorr) + c0;
+    float* inv_s = reinterpret_cast<float*>(sm + L::kInv) + c0;
+    int* vis_s = reinterpret_cast<int*>(sm + L::kVis) + c0;
+    int* row_s = reinterpret_cast<int*>(sm + L::kRow) + c0;
+    uint32_t* anc_s = reinterpret_cast<uint32_t*>(sm + L::kAnc) + c0;   // [4][N]
     int* wmax = reinterpret_cast<int*>(sm + L::kWarpMax) + wg * 128;
     const int tid = threadIdx.x - 32 * L::kSoft0 - 128 * wg;    // 0..127 in the warpgroup
-    int par = 0;                                                // ref[par] is current
-    float l[C];
+    uint64_t l[C / 2];                                          // this key's share of the rows' sums
 #pragma unroll
-    for (int c = 0; c < C; ++c) l[c] = 0.f;
+    for (int c = 0; c < C / 2; ++c) l[c] = 0ull;
+    bool force = false;                                         // a row of the unit has no reference yet
     for (int it = 0;; ++it) {
       const int st = it % kStages, b = it & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 48))) break;
+      if (!warp_wait(bar(RAW_FULL + st), (it / kStages) & 1, abort_flag, err, 48)) break;
       const Tile t = tile_at(st);
-      if (t.kind == kEnd) break;
-      const bool first = t.flags & 1, last = t.flags & 2, tree = t.kind == kTree;
+      if (t.flags & kEnd) break;
+      const bool first = t.flags & kFirst, last = t.flags & kLast, tree = t.flags & kTree;
       float sk = c2, sv = 1.f;
       bool valid = own < t.nkeys;
       if (!tree) {
@@ -648,6 +635,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
         sk = valid ? c2 * bf16_at(reinterpret_cast<const uint16_t*>(blk + k_scale(a.page_size, D, slot))) : 0.f;
         sv = valid ? bf16_at(reinterpret_cast<const uint16_t*>(blk + v_scale(a.page_size, D, slot))) : 0.f;
       }
+      const int key = valid && !tree ? t.key0 + own : 0x7fffffff;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(RAW_EMPTY + st));
       if (first || tree) {
@@ -657,142 +645,143 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
           const bool live = rr < p.nq * g && ln < t.cnt;
           const int gn = t.n0 + ln;
           if (first) {
-            ref[par * N + rr] = kLow;
-            row_s[rr] = live ? gn * a.Hq + t.h * g + rr % g : -1;
-            vis_s[rr] = live ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
+            nref[tid] = -0.f;
+            row_s[tid] = live ? gn * a.Hq + t.h * g + rr % g : -1;
+            vis_s[tid] = live ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
           }
           if (tree) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int word = (t.key0 >> 6) + w;
               const uint64_t v = live && word < a.anc_words ? a.anc[static_cast<int64_t>(gn) * a.anc_words + word] : 0ull;
-              anc_s[(2 * w) * N + rr] = static_cast<uint32_t>(v);
-              anc_s[(2 * w + 1) * N + rr] = static_cast<uint32_t>(v >> 32);
+              anc_s[(2 * w) * N + tid] = static_cast<uint32_t>(v);
+              anc_s[(2 * w + 1) * N + tid] = static_cast<uint32_t>(v >> 32);
             }
           }
         }
         wg_sync(wid);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(S_FULL + b), (it >> 1) & 1, abort_flag, err, 49))) break;
+      if (!warp_wait(bar(S_FULL + b), (it >> 1) & 1, abort_flag, err, 49)) break;
       tc_fence_after();
-      const uint32_t tS = tmem + L::tS + N * b + c0 + lane_off;
-      uint32_t x[C];
-      // scores of this key in base-2 units, minus the rows' references; -inf where the row does not see the key
-      auto scores = [&](bool sub) {
-        tmem_ld(tS, x);
+      // scores in base-2 units over the rows' references, two rows to a register pair; -inf: not seen
+      uint64_t y[C / 2];
+      {
+        uint32_t x[C];
+        tmem_ld(tmem + L::tS + N * b + c0 + lane_off, x);
         tmem_ld_wait();
-        const uint32_t* words = anc_s + (warp & 3) * N + c0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) pin(x[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S_FREE + b));
+        const uint64_t sk2 = pair(sk, sk);
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(ref + par * N + c0 + c);
-          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            pin(x[c + i]);
-            x[c + i] = __float_as_uint(fmaf(__uint_as_float(x[c + i]), sk, sub ? -m[i] : 0.f));
-          }
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nref + c);
+          y[c / 2] = fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sk2, m.x);
+          y[c / 2 + 1] = fma2(pair(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sk2, m.y);
         }
-        if (tree) {
+      }
+      if (__builtin_expect(tree || a.vis_prefix != nullptr || !__all_sync(0xffffffffu, valid), 0)) {
+        const uint32_t* words = anc_s + (warp & 3) * N;
 #pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(words + c);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(valid && ((w[i] >> lane) & 1u))) x[c + i] = __float_as_uint(-INFINITY);
-          }
-        } else if (a.vis_prefix) {
-          const int key = valid ? t.key0 + own : 0x7fffffff;
-#pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            const int4 v4 = *reinterpret_cast<const int4*>(vis_s + c0 + c);
-            const int v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key >= v[i]) x[c + i] = __float_as_uint(-INFINITY);
-          }
-        } else if (!__all_sync(0xffffffffu, valid)) {
-          if (!valid) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) x[c] = __float_as_uint(-INFINITY);
-          }
+        for (int c = 0; c < C; c += 2) {
+          float lo, hi;
+          split(y[c / 2], lo, hi);
+          const bool s0 = tree ? valid && ((words[c] >> lane) & 1u) : key < vis_s[c];
+          const bool s1 = tree ? valid && ((words[c + 1] >> lane) & 1u) : key < vis_s[c + 1];
+          y[c / 2] = pair(s0 ? lo : -INFINITY, s1 ? hi : -INFINITY);
         }
-      };
-      bool slow = first;
-      if (!first) {
-        scores(true);
+      }
+      bool slow = first || force;
+      if (!slow) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < C; ++c) mx[c & 1] = fmaxf(mx[c & 1], __uint_as_float(x[c]));
+        for (int c = 0; c < C / 2; ++c) {
+          float lo, hi;
+          split(y[c], lo, hi);
+          mx[c & 1] = max3(mx[c & 1], lo, hi);
+        }
         slow = wg_any(wid, fmaxf(mx[0], mx[1]) > 8.f);
       }
-      if (slow) {
+      if (__builtin_expect(slow, 0)) {
         // new references: the rows' maxima so far
-        scores(false);
         int mine = static_cast<int>(0x80000000);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          int v = static_cast<int>(x[c]);
+          float lo, hi;
+          split(y[c / 2], lo, hi);
+          int v = __float_as_int(c & 1 ? hi : lo);
           v ^= (v >> 31) & 0x7fffffff;           // order of floats as order of integers
           v = __reduce_max_sync(0xffffffffu, v);
           if ((lane & (C - 1)) == c) mine = v;
         }
         if (lane < C) wmax[(warp & 3) * 32 + lane] = mine;
         wg_sync(wid);
-        if (lane < C) {                          // every warp writes the same values
+        bool none = false;
+        float sh = 0.f, next = 0.f;
+        if (lane < C) {                          // every warp works out the same
           int v = wmax[lane];
 #pragma unroll
           for (int w = 1; w < 4; ++w) v = max(v, wmax[32 * w + lane]);
           v ^= (v >> 31) & 0x7fffffff;
-          const float old = ref[par * N + c0 + lane];
-          const float now = fmaxf(old, __int_as_float(v));
-          ref[(par ^ 1) * N + c0 + lane] = now;
-          corr_s[c0 + lane] = ex2(old - now);
+          const float top = __int_as_float(v), old = nref[lane];
+          const bool unset = __float_as_uint(old) == 0x80000000u;
+          sh = unset ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+          if (top != top) sh = top;
+          next = unset && top == -INFINITY ? -0.f : old - sh;
+          none = row_s[lane] >= 0 && unset && top == -INFINITY;
+          corr_s[lane] = unset ? 0.f : ex2(-sh);
+          shift_s[lane] = -sh;
         }
+        force = __any_sync(0xffffffffu, none);
+        wg_sync(wid);                            // all have read the old references
+        if (lane < C) nref[lane] = next;
         __syncwarp();
-        par ^= 1;
-        if (first) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] = 0.f;
-        } else {
-          if (!__all_sync(0xffffffffu,
-                          mbar_wait(bar(PV_DONE + (b ^ 1)), ((it - 1) >> 1) & 1, abort_flag, err, 50)))
-            break;
+        for (int c = 0; c < C; c += 4) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(shift_s + c);
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(corr_s + c);
+          y[c / 2] = add2(y[c / 2], m.x);
+          y[c / 2 + 1] = add2(y[c / 2 + 1], m.y);
+          l[c / 2] = mul2(l[c / 2], f.x);
+          l[c / 2 + 1] = mul2(l[c / 2 + 1], f.y);
+        }
+        if (!first) {
+          if (!warp_wait(bar(PV_DONE + (b ^ 1)), ((it - 1) >> 1) & 1, abort_flag, err, 50)) break;
           tc_fence_after();
           uint32_t o[C];
           tmem_ld(tmem + L::tO + c0 + lane_off, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(corr_s + c0 + c);
-            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              pin(o[c + i]);
-              o[c + i] = __float_as_uint(__uint_as_float(o[c + i]) * f[i]);
-              l[c + i] *= f[i];
-            }
+          for (int c = 0; c < C; ++c) {
+            pin(o[c]);
+            o[c] = __float_as_uint(__uint_as_float(o[c]) * corr_s[c]);
           }
           tmem_st(tmem + L::tO + c0 + lane_off, o);
           tmem_st_wait();
+          tc_fence_before();
         }
-        scores(true);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(S_FREE + b));
       // weights
       uint32_t pk[C / 2];
+      const uint64_t sv2 = pair(sv, sv);
 #pragma unroll
-      for (int c = 0; c < C; c += 2) {
-        const float e0 = ex2(__uint_as_float(x[c])), e1 = ex2(__uint_as_float(x[c + 1]));
-        l[c] += e0;
-        l[c + 1] += e1;
-        pk[c >> 1] = pack_bf16(e0 * sv, e1 * sv);
+      for (int c = 0; c < C / 2; ++c) {
+        float lo, hi;
+        split(y[c], lo, hi);
+        const uint64_t e = pair(ex2(lo), ex2(hi));
+        l[c] = add2(l[c], e);
+        split(mul2(e, sv2), lo, hi);
+        pk[c] = pack_bf16(lo, hi);
       }
-      if (it >= 2 &&
-          !__all_sync(0xffffffffu, mbar_wait(bar(PV_DONE + b), ((it >> 1) - 1) & 1, abort_flag, err, 51)))
-        break;
+      if (__builtin_expect(sv != sv && a.vis_prefix != nullptr, 0)) {
+        // a value row that was not finite: zero weights times its scale are NaN, rows that do not see it stay clean
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (key >= vis_s[c]) pk[c >> 1] &= c & 1 ? 0x0000ffffu : 0xffff0000u;
+      }
+      if (it >= 2 && !warp_wait(bar(PV_DONE + b), ((it >> 1) - 1) & 1, abort_flag, err, 51)) break;
       uint8_t* prow = sm + L::kP + b * L::kPBytes + own * 128;
 #pragma unroll
       for (int c = 0; c < C / 8; ++c)
@@ -801,91 +790,101 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       // the value warps' note on non-finite tree rows, read at the end of the unit (V's phase cannot move on
       // before P is given away)
-      if (last && tree &&
-          !__all_sync(0xffffffffu, mbar_wait(bar(V_FULL + b), (it >> 1) & 1, abort_flag, err, 53)))
-        break;
-      tc_fence_before();
+      if (last && tree && !warp_wait(bar(V_FULL + b), (it >> 1) & 1, abort_flag, err, 53)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(P_FULL + b));
-      if (!last) continue;
+      if (__builtin_expect(!last, 1)) continue;
 
       // ---- end of the unit's run here: sums over the keys' threads, then O^T
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(PV_DONE + b), (it >> 1) & 1, abort_flag, err, 52))) break;
-      tc_fence_after();
+      float ls[C];
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) {
+        split(l[c], ls[2 * c], ls[2 * c + 1]);
+        l[c] = 0ull;
+      }
+      force = false;
       // reduce-scatter over the lanes: lane i ends with column i % C
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         if (o >= C) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+          for (int c = 0; c < C; ++c) ls[c] += __shfl_xor_sync(0xffffffffu, ls[c], o);
         } else {
           const bool up = lane & o;
 #pragma unroll
           for (int c = 0; c < o; ++c) {
-            const float keep = up ? l[c + o] : l[c], give = up ? l[c] : l[c + o];
-            l[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            const float keep = up ? ls[c + o] : ls[c], give = up ? ls[c] : ls[c + o];
+            ls[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
           }
         }
       }
-      if (lane < C) wmax[(warp & 3) * 32 + lane] = __float_as_int(l[0]);
+      if (lane < C) wmax[(warp & 3) * 32 + lane] = __float_as_int(ls[0]);
       wg_sync(wid);
-      float lsum = 0.f;
       if (lane < C) {
+        float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) lsum += __int_as_float(wmax[32 * w + lane]);
-        inv_s[c0 + lane] = t.slot >= 0 ? 1.f : (lsum == 0.f ? 0.f : 1.f / lsum);   // partials stay unnormalised
+        for (int w = 0; w < 4; ++w) sum += __int_as_float(wmax[32 * w + lane]);
+        inv_s[lane] = t.slot >= 0 ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);   // partials stay unnormalised
         if ((warp & 3) == 0) {
-          const float m = ref[par * N + c0 + lane];
+          const float m = -nref[lane];
           if (t.slot >= 0) {
-            p.ml[static_cast<int64_t>(t.slot) * N + c0 + lane] = make_float2(m, lsum);
-          } else if (a.lse && row_s[c0 + lane] >= 0) {
-            a.lse[row_s[c0 + lane]] = lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
+            p.ml[static_cast<int64_t>(t.slot) * N + c0 + lane] = make_float2(sum == 0.f ? kLow : m, sum);
+          } else if (a.lse && row_s[lane] >= 0) {
+            a.lse[row_s[lane]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
           }
         }
       }
       __syncwarp();
+      if (!warp_wait(bar(PV_DONE + b), (it >> 1) & 1, abort_flag, err, 52)) break;
+      tc_fence_after();
       uint32_t o[C];
       tmem_ld(tmem + L::tO + c0 + lane_off, o);
       tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < C; ++c) pin(o[c]);
+      tc_fence_before();                         // O was read: the next unit's first PV may overwrite it
       if (own < D) {
-        if (dirty[t.seg & 3] == t.seg + 1) {
-          // non-finite tree values, added to the rows that see them
-          const uint16_t* col = static_cast<const uint16_t*>(a.v_tree) + static_cast<int64_t>(t.n0) * a.ldv +
-                                static_cast<int64_t>(t.h) * D + own;
-          for (int j = 0; j < t.cnt; ++j) {
-            const uint32_t v = col[static_cast<int64_t>(j) * a.ldv];
-            if ((v & 0x7f80u) != 0x7f80u || (j >> 6) >= a.anc_words) continue;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-              const int row = row_s[c0 + c];
-              if (row < 0) continue;
-              const uint64_t word = a.anc[static_cast<int64_t>(row / a.Hq) * a.anc_words + (j >> 6)];
-              if ((word >> (j & 63)) & 1ull) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(v << 16));
-            }
-          }
-        }
         if (t.slot >= 0) {
-          float* po = p.o + static_cast<int64_t>(t.slot) * N * D + c0 * D + own;
+          float* po = p.o + (static_cast<int64_t>(t.slot) * N + c0) * D + own;
 #pragma unroll
           for (int c = 0; c < C; ++c)
-            if (row_s[c0 + c] >= 0) po[c * D] = __uint_as_float(o[c]);
+            if (row_s[c] >= 0) po[c * D] = __uint_as_float(o[c]);
         } else {
           uint16_t* out = static_cast<uint16_t*>(a.out) + own;
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const int row = row_s[c0 + c];
+            const int row = row_s[c];
             if (row >= 0) {
-              const float f = __uint_as_float(o[c]) * inv_s[c0 + c];
+              const float f = __uint_as_float(o[c]) * inv_s[c];
               out[static_cast<int64_t>(row) * D] = static_cast<uint16_t>(pack_bf16(f, 0.f));
             }
           }
         }
+        if (__builtin_expect(dirty[t.seg & 3] == t.seg + 1, 0)) {
+          // tree values that are not finite, added to the rows that see them (this thread wrote these elements)
+          const uint16_t* col = static_cast<const uint16_t*>(a.v_tree) + static_cast<int64_t>(t.n0) * a.ldv +
+                                static_cast<int64_t>(t.h) * D + own;
+#pragma unroll 1
+          for (int j = 0; j < min(t.cnt, 64 * a.anc_words); ++j) {
+            const uint32_t v = col[static_cast<int64_t>(j) * a.ldv];
+            if ((v & 0x7f80u) != 0x7f80u) continue;
+#pragma unroll 1
+            for (int c = 0; c < C; ++c) {
+              const int row = row_s[c];
+              if (row < 0) continue;
+              const uint64_t word = a.anc[static_cast<int64_t>(row / a.Hq) * a.anc_words + (j >> 6)];
+              if (!((word >> (j & 63)) & 1ull)) continue;
+              const float f = __uint_as_float(v << 16);
+              if (t.slot >= 0) {
+                p.o[(static_cast<int64_t>(t.slot) * N + c0 + c) * D + own] += f;
+              } else {
+                uint16_t* o16 = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(row) * D + own;
+                *o16 = static_cast<uint16_t>(pack_bf16(bf16_at(o16) + f, 0.f));
+              }
+            }
+          }
+        }
       }
-      tc_fence_before();                         // O was read: the next unit's first PV may overwrite it
-#pragma unroll
-      for (int c = 0; c < C; ++c) l[c] = 0.f;
     }
   }
   tc_fence_before();
@@ -899,42 +898,59 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
 
 // Joins the pieces of a unit that was cut: piece 0 is slot 1 of the CTA where
 // the unit starts, piece i slot 0 of the i-th CTA after it.  CTA = (starting
-// CTA, share of the rows), thread = dim.
+// CTA, eight rows), thread = four dims of a row.
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const TcArgs p, int N) {
+__global__ void __launch_bounds__(2 * D) join_kernel(const TcArgs p, int N) {
   griddep_wait();
   griddep_release();
   const int4 d = p.desc[blockIdx.x];
   if (d.x < 2) return;
   const AttnArgs& a = p.a;
-  const int g = a.Hq / a.Hkv;
+  const int g = a.Hq / a.Hkv, c = blockIdx.y * 8 + threadIdx.x / (D / 4), dim = threadIdx.x % (D / 4) * 4;
   const Span s = node_span(a, d.y);
-  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)); };
-  const int rows = min(p.nq, s.cnt - d.z * p.nq) * g;
-  for (int c = blockIdx.y; c < rows; c += gridDim.y) {
-    float M = -INFINITY;
-    for (int i = 0; i < d.x; ++i) M = fmaxf(M, p.ml[slot(i) * N + c].x);
-    float acc = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < d.x; ++i) {
-      const float2 ml = p.ml[slot(i) * N + c];
-      const float o = p.o[(slot(i) * N + c) * D + threadIdx.x];
-      if (ml.y == 0.f) continue;                 // nothing seen in this piece
-      const float w = ex2(ml.x - M);
-      sum = fmaf(w, ml.y, sum);
-      acc = fmaf(w, o, acc);
+  if (c >= min(p.nq, s.cnt - d.z * p.nq) * g) return;
+  auto slot = [&](int i) {
+    return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * N + c;
+  };
+  float M = kLow, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAhead = 4;                      // pieces whose loads are in flight together
+  for (int i0 = 0; i0 < d.x; i0 += kAhead) {
+    float2 ml[kAhead];
+    float4 o[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      ml[k] = make_float2(kLow, 0.f);
+      if (i0 + k < d.x) {
+        ml[k] = p.ml[slot(i0 + k)];
+        o[k] = *reinterpret_cast<const float4*>(p.o + slot(i0 + k) * D + dim);
+      }
     }
-    const int64_t row = static_cast<int64_t>(s.n0 + d.z * p.nq + c / g) * a.Hq + d.w * g + c % g;
-    const float f = sum == 0.f ? 0.f : acc / sum;
-    static_cast<uint16_t*>(a.out)[row * D + threadIdx.x] = static_cast<uint16_t>(pack_bf16(f, 0.f));
-    if (threadIdx.x == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    const float old = M;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) M = fmaxf(M, ml[k].x);
+    const float keep = ex2(old - M);
+    sum *= keep;
+    acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (ml[k].y == 0.f) continue;              // nothing seen in this piece
+      const float w = ex2(ml[k].x - M);
+      sum = fmaf(w, ml[k].y, sum);
+      acc.x = fmaf(w, o[k].x, acc.x);
+      acc.y = fmaf(w, o[k].y, acc.y);
+      acc.z = fmaf(w, o[k].z, acc.z);
+      acc.w = fmaf(w, o[k].w, acc.w);
+    }
   }
+  const int64_t row = static_cast<int64_t>(s.n0 + d.z * p.nq + c / g) * a.Hq + d.w * g + c % g;
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + dim) =
+      make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+  if (dim == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
-int rows_of(int max_nodes, int g) {
-  const long long rows = static_cast<long long>(max_nodes) * g;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
+constexpr int kRows = 64;   // query rows of a unit
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -944,34 +960,49 @@ int launch(const TcArgs& p, cudaStream_t st) {
   if (!smem_limit(attn_kernel<D, N>, static_cast<int>(L::kBytes))) return TV_ECUDA;
   const int rc = launch_pdl(attn_kernel<D, N>, dim3(p.grid), dim3(L::kThreads), L::kBytes, st, p);
   if (rc != TV_OK) return rc;
-  return launch_pdl(join_kernel<D>, dim3(p.grid, 4), dim3(D), 0, st, p, N);
+  return launch_pdl(join_kernel<D>, dim3(p.grid, N / 8), dim3(2 * D), 0, st, p, N);
 }
+
+bool wants_extents(const AttnArgs& a) { return a.vis_prefix != nullptr || a.max_nodes > kKeys; }
 
 }  // namespace
 
-size_t attn_tc_workspace(int max_nodes, int Hq, int Hkv, int d) {
-  const size_t G = sm_count(), N = rows_of(max_nodes, Hq / Hkv);
-  return 256 + align256(G * sizeof(int4)) + align256(2 * G * N * sizeof(float2)) + 2 * G * N * d * sizeof(float);
+int attn_extents(const AttnArgs& a, int nq, int tiles, int4* out, cudaStream_t st) {
+  return launch_pdl(extent_kernel, dim3((a.B * tiles + 3) / 4), dim3(128), 0, st, a, nq, tiles, out);
+}
+
+// [status word (256 B)] [extents] [pieces of cut units] [partial (m, l)] [partial o]
+size_t attn_tc_workspace(int B, int max_nodes, int Hq, int Hkv, int d) {
+  const size_t G = sm_count(), N = kRows, nq = N / (Hq / Hkv);
+  const size_t entries = static_cast<size_t>(B) * ((max_nodes + nq - 1) / nq);
+  return 256 + align256(entries * sizeof(int4)) + align256(G * sizeof(int4)) + align256(2 * G * N * sizeof(float2)) +
+         2 * G * N * d * sizeof(float);
 }
 
 int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st) {
   TcArgs p{};
   p.a = a;
-  const int g = a.Hq / a.Hkv, N = rows_of(a.max_nodes, g);
+  const int g = a.Hq / a.Hkv, N = kRows;
   p.grid = sm_count();
   p.nq = N / g;
   p.tiles = (a.max_nodes + p.nq - 1) / p.nq;
-  p.by_node = a.vis_prefix != nullptr || a.max_nodes > kKeys;
+  const int entries = a.B * p.tiles;
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<int*>(base);
   base += 256;
+  int4* extents = reinterpret_cast<int4*>(base);
+  base += align256(static_cast<size_t>(entries) * sizeof(int4));
   p.desc = reinterpret_cast<int4*>(base);
   base += align256(p.grid * sizeof(int4));
   p.ml = reinterpret_cast<float2*>(base);
   base += align256(2ull * p.grid * N * sizeof(float2));
   p.o = reinterpret_cast<float*>(base);
-  if (a.d == 128) return N == 16 ? launch<128, 16>(p, st) : N == 32 ? launch<128, 32>(p, st) : launch<128, 64>(p, st);
-  return N == 16 ? launch<64, 16>(p, st) : N == 32 ? launch<64, 32>(p, st) : launch<64, 64>(p, st);
+  if (wants_extents(a)) {
+    const int rc = attn_extents(a, p.nq, p.tiles, extents, st);
+    if (rc != TV_OK) return rc;
+    p.extents = extents;
+  }
+  return a.d == 128 ? launch<128, kRows>(p, st) : launch<64, kRows>(p, st);
 }
 
 }  // namespace kv4
