@@ -456,29 +456,29 @@ def blockpilot_mlp(last_logits, row_lse, W1, W2, b1=None, b2=None, block=16, ws=
 # --------------------------------------------------- paged 4-bit KV cache, rotation
 # These calls sit on the decoding path, where the host's time per call counts:
 # pointers go to the library as plain integers.
-def _dense(t: Optional[torch.Tensor], name: str, dtype, dev, shape) -> Optional[int]:
-    """Address of a contiguous tensor of this dtype, device and shape (None in ``shape``: any size); None for None."""
+def _dense(t: Optional[torch.Tensor], name: str, dtype, dev: int, shape) -> Optional[int]:
+    """Address of a contiguous tensor of this dtype, device (index, -1: host) and shape; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t: torch.Tensor, name: str, dtype, dev, n, heads, d):
+def _rows(t: torch.Tensor, name: str, dtype, dev: int, n, heads, d):
     """(address, elements between rows) of [n, heads, d] rows whose heads are packed; the row stride is free, so a
     slice of a fused projection's output can be passed."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 3 or (t.shape[0] != n) or t.shape[1] != heads or t.shape[2] != d:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    if t.shape != (n, heads, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, d)}")
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
@@ -486,16 +486,18 @@ def _rows(t: torch.Tensor, name: str, dtype, dev, n, heads, d):
     return t.data_ptr(), (s0 if n > 1 else heads * d)
 
 
-def _call_on(dev, fn: str, *args):
-    """Calls the library on ``dev`` and its current stream (the last argument)."""
-    if dev.type != "cuda":
+def _call_on(dev: int, fn: str, *args):
+    """Calls the library on device ``dev`` and its current stream (the last argument)."""
+    if dev < 0:
         raise ValueError("libtreeverify takes device tensors")
-    f = getattr(load_library(), fn)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+    f = getattr(_LIB or load_library(), fn)
+    if dev == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise TVError(fn, status)
 
 
 def _act_dtype(t: torch.Tensor, name: str) -> int:
@@ -520,29 +522,39 @@ def _cache_geometry(cache, page_size):
 def _rope_args(rope, dev):
     if rope is None:
         return None, 0, 0
-    return _dense(rope, "rope", torch.float32, dev, (None, None)), rope.shape[0], rope.shape[1]
+    if rope.dim() != 2:
+        raise ValueError("rope must be [max_pos, rot_dim]")
+    return _dense(rope, "rope", torch.float32, dev, rope.shape), rope.shape[0], rope.shape[1]
 
 
-def _new_err(err, dev):
+def _new_err(err, like):
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
-    return err, _dense(err, "err", torch.int32, dev, (1,))
+        err = torch.zeros(1, dtype=torch.int32, device=like.device)
+    return err, _dense(err, "err", torch.int32, like.get_device(), (1,))
+
+
+def _table(t, B: int, dev: int, name="block_table"):
+    """(address, columns) of an int32 [B, columns] table."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [{B}, columns]")
+    cols = t.shape[1]
+    return _dense(t, name, torch.int32, dev, (B, cols)), cols
 
 
 def tv_rope(q, k, pos, rope, interleaved=False, outputs=None, err=None):
     """Rotates q [n, Hq, d] and k [n, Hkv, d] (or None) at ``pos`` int32 [n] with the table ``rope`` float32
     [max_pos, rot_dim] (cosines, then sines).  Row strides are free.  Returns q_out, k_out, err."""
     n, Hq, d = q.shape
-    dev = q.device
+    dev = q.get_device()
     dt = _act_dtype(q, "q")
     Hkv = k.shape[1] if k is not None else 0
     if outputs is None:
-        outputs = (torch.empty((n, Hq, d), dtype=q.dtype, device=dev),
-                   torch.empty((n, Hkv, d), dtype=q.dtype, device=dev) if k is not None else None)
+        outputs = (torch.empty((n, Hq, d), dtype=q.dtype, device=q.device),
+                   torch.empty((n, Hkv, d), dtype=q.dtype, device=q.device) if k is not None else None)
     q_out, k_out = outputs
     if (k is None) != (k_out is None):
         raise ValueError("k and its output go together")
-    err, perr = _new_err(err, dev)
+    err, perr = _new_err(err, q)
     table, max_pos, rot = _rope_args(rope, dev)
     pq, ldq = _rows(q, "q", q.dtype, dev, n, Hq, d)
     pk, ldk = _rows(k, "k", q.dtype, dev, n, Hkv, d) if k is not None else (None, 0)
@@ -564,7 +576,7 @@ def kv4_append(k, v, cache, page_size, block_table, cache_len, row_off, max_new,
     """Appends rows of k, v [rows, Hkv, d] to the cache (in place); keys are rotated with ``rope`` (None: they come
     rotated) at ``pos`` (None: the token's index).  ``path`` int32 [B, m] picks rows of each request up to its first
     negative entry, as accept_longest_path returns it.  Returns new_len int32 [B], err int32 [1]."""
-    dev = cache.device
+    dev = cache.get_device()
     n_pages, Hkv, d = _cache_geometry(cache, page_size)
     dt = _act_dtype(k, "k")
     n = k.shape[0]
@@ -572,14 +584,14 @@ def kv4_append(k, v, cache, page_size, block_table, cache_len, row_off, max_new,
     pk, ldk = _rows(k, "k", k.dtype, dev, n, Hkv, d)
     pv, ldv = _rows(v, "v", k.dtype, dev, n, Hkv, d)
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    err, perr = _new_err(err, dev)
+        new_len = torch.empty(B, dtype=torch.int32, device=cache.device)
+    err, perr = _new_err(err, cache)
     table, max_pos, rot = _rope_args(rope, dev)
     i32 = torch.int32
     _call_on(dev, "kv4_append", pk, ldk, pv, ldv, dt, n, _dense(row_off, "row_off", i32, dev, (B + 1,)),
-             _dense(path, "path", i32, dev, (B, None)), path.shape[1] if path is not None else 0, B, max_new,
+             *(_table(path, B, dev, "path") if path is not None else (None, 0)), B, max_new,
              _dense(pos, "pos", i32, dev, (n,)), table, max_pos, rot, int(interleaved), cache.data_ptr(), n_pages,
-             page_size, _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             page_size, *_table(block_table, B, dev),
              _dense(cache_len, "cache_len", i32, dev, (B,)), Hkv, d, _dense(new_len, "new_len", i32, dev, (B,)), perr)
     return new_len, err
 
@@ -588,27 +600,28 @@ def kv4_gather(cache, page_size, block_table, out_off, max_rows, start=None, tot
                outputs=None, err=None):
     """Cached tokens start[r] .. (0 without ``start``) of each request as rows out_off[r] .. out_off[r+1]-1 of k, v
     [total_rows, Hkv, d].  Give ``outputs`` (their length and dtype count) or ``total_rows``.  Returns k, v, err."""
-    dev = cache.device
+    dev = cache.get_device()
     n_pages, Hkv, d = _cache_geometry(cache, page_size)
     B = out_off.numel() - 1
     if outputs is None:
         if total_rows is None:
             raise ValueError("kv4_gather needs outputs or total_rows")
-        outputs = tuple(torch.empty((total_rows, Hkv, d), dtype=dtype, device=dev) for _ in range(2))
+        outputs = tuple(torch.empty((total_rows, Hkv, d), dtype=dtype, device=cache.device) for _ in range(2))
     k, v = outputs
     n = k.shape[0]
     dt = _act_dtype(k, "k")
-    err, perr = _new_err(err, dev)
+    err, perr = _new_err(err, cache)
     i32 = torch.int32
     _call_on(dev, "kv4_gather", cache.data_ptr(), n_pages, page_size,
-             _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             *_table(block_table, B, dev),
              _dense(start, "start", i32, dev, (B,)), _dense(out_off, "out_off", i32, dev, (B + 1,)), B, max_rows, n,
              Hkv, d, dt, _dense(k, "k", k.dtype, dev, (n, Hkv, d)), _dense(v, "v", k.dtype, dev, (n, Hkv, d)), perr)
     return k, v, err
 
 
 def tree_verify_attn_kv4_workspace(B, max_nodes, Hq, Hkv, d, dtype=torch.bfloat16, device="cuda"):
-    """A workspace for tree_verify_attn_kv4 calls of up to these sizes (one call at a time)."""
+    """A workspace for tree_verify_attn_kv4 calls of these sizes (one call at a time); a call that needs more than
+    the workspace it is given is refused."""
     code = TV_F32 if dtype == torch.float32 else TV_BF16
     return _ws(load_library().tree_verify_attn_kv4_workspace_size(B, max_nodes, Hq, Hkv, d, code), device)
 
@@ -618,13 +631,13 @@ def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_
                          err=None):
     """tree_verify_attn with the prefix in a paged 4-bit cache.  q, k_tree, v_tree: [n, heads, d], row strides free.
     Returns out, lse, err."""
-    dev = q.device
+    dev = q.get_device()
     n, Hq, d = q.shape
     n_pages, Hkv, dc = _cache_geometry(cache, page_size)
     if dc != d:
         raise ValueError(f"the cache holds heads of {dc}, q has {d}")
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    if cache.get_device() != dev:
+        raise ValueError(f"cache is on {cache.device}, expected device {dev}")
     dt = _act_dtype(q, "q")
     B = node_off.numel() - 1
     if scale is None:
@@ -633,20 +646,21 @@ def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_
     pk, ldk = _rows(k_tree, "k_tree", q.dtype, dev, n, Hkv, d)
     pv, ldv = _rows(v_tree, "v_tree", q.dtype, dev, n, Hkv, d)
     if out is None:
-        out = torch.empty((n, Hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
-    err, perr = _new_err(err, dev)
-    need = load_library().tree_verify_attn_kv4_workspace_size(B, max_nodes, Hq, Hkv, d, dt)
-    if ws is None or ws.numel() < need:
-        ws = _ws(need, dev)
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+    err, perr = _new_err(err, q)
+    if ws is None:
+        ws = tree_verify_attn_kv4_workspace(B, max_nodes, Hq, Hkv, d, q.dtype, q.device)
+    if anc.dim() != 2:
+        raise ValueError("anc must be [n, words]")
     i32 = torch.int32
     _call_on(dev, "tree_verify_attn_kv4", pq, ldq, cache.data_ptr(), n_pages, page_size,
-             _dense(block_table, "block_table", i32, dev, (B, None)), block_table.shape[1],
+             *_table(block_table, B, dev),
              _dense(cache_len, "cache_len", i32, dev, (B,)), pk, ldk, pv, ldv,
              _dense(node_off, "node_off", i32, dev, (B + 1,)), _dense(node_cnt, "node_cnt", i32, dev, (B,)),
-             _dense(anc, "anc", torch.int64, dev, (n, None)), anc.shape[1],
+             _dense(anc, "anc", torch.int64, dev, (n, anc.shape[1])), anc.shape[1],
              _dense(vis_prefix, "vis_prefix", i32, dev, (n,)), B, max_nodes, n, Hq, Hkv, d, dt, float(scale),
              _dense(out, "out", q.dtype, dev, (n, Hq, d)), _dense(lse, "lse", torch.float32, dev, (n, Hq)),
-             _dense(ws, "ws", torch.uint8, dev, (None,)), ws.numel(), perr)
+             _dense(ws, "ws", torch.uint8, dev, (ws.numel(),)), ws.numel(), perr)
     return out, lse, err

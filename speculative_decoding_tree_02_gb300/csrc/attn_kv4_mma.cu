@@ -55,6 +55,7 @@ struct MmaArgs {
   float* o;               // [2 workers][8 NB][D]
   const int4* extents;    // [B] x = visible prefix (per-node prefixes), or NULL
   int workers;
+  uint32_t magic;         // kMagic
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -161,12 +162,21 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   // ---- the loads run two chunks ahead, their page numbers three
   const int P = a.page_size, Pe = min(P, kChunk), shift = 31 - __clz(Pe);
   const uint32_t blk_e = Pe * (D + 4);           // bytes of a staged page
+  // a block of 16 keys lies in one staged page; offset of its page and its first slot
+  int pg[4], sl[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    pg[m] = ((16 * m) >> shift) * blk_e;
+    sl[m] = (16 * m) & (Pe - 1);
+  }
+  const int page_shift = 31 - __clz(P);
   int le = e, lh = h, lblk = blk, lpage = -1;    // next chunk to load, this lane's page of it
   Unit lu = u;
-  long long lpos = w0;
+  const int n = static_cast<int>(w1 - w0);       // chunks of the run
+  int lnext = 0;                                 // chunks loaded
   auto look = [&]() {                            // the page numbers of the next chunk to load
     lpage = -1;
-    if (lpos >= w1) return;
+    if (lnext >= n) return;
     if (lblk == lu.nb) {
       lblk = 0;
       if (++lh == a.Hkv) {
@@ -177,11 +187,11 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     }
     const int key = lblk * kChunk + (P > kChunk ? 0 : lane << shift);
     if (lblk < lu.np && (P > kChunk ? lane <= kC + 2 : lane < kChunk >> shift) && key < lu.len)
-      lpage = a.block_table[static_cast<int64_t>(le) * a.table_ld + key / P];
+      lpage = a.block_table[static_cast<int64_t>(le) * a.table_ld + (key >> page_shift)];
   };
   unsigned good = 0u;                            // staged pages of the two stages, 8 bits each
   auto load = [&](int st) {
-    if (lpos >= w1) return;
+    if (lnext >= n) return;
     const bool wanted = lpage != -1;
     const bool ok = wanted && lpage >= 0 && lpage < a.n_pages;
     // a lane that wants no page has -1 too: entries of -1 are told by the token they should hold
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
       }
     }
     ++lblk;
-    ++lpos;
+    ++lnext;
   };
   // ---- state of the running unit
   uint64_t nm[NB], l[NB];                        // rows 8 nb + 2t, + 1: negated references, sums
@@ -220,20 +230,18 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   bool dirty = false;
   int n0 = 0, cnt = 0;
   const float c2 = a.scale * kLog2e;
+  const uint32_t magic = p.magic;
   int seg_blk = blk;
   bool fresh = true;
   auto row_at = [&](int r) { return static_cast<int64_t>(n0 + r / g) * a.Hq + h * g + r % g; };   // output row
 
   look();
-  for (long long pos = w0 - 2;;) {
-    {                                            // the chunk after next (before the first chunk: the first two)
-      const int st = static_cast<int>(pos - w0) & 1;
-      load(st);
-      look();
-      if (++pos == w1) break;
-      if (pos < w0) continue;
-    }
-    const int it = static_cast<int>(pos - w0), st = it & 1;
+  for (int it = -2;;) {
+    load(it & 1);                                // the chunk after next (before the first chunk: the first two)
+    look();
+    if (++it == n) break;
+    if (it < 0) continue;
+    const int st = it & 1;
     if (blk == u.nb) {                           // next unit
       blk = seg_blk = 0;
       fresh = true;
@@ -304,6 +312,11 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[m][i][k] = 0.f;
     if (!tree) {
+      const uint8_t* kp[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        kp[m] = stage + (kb ? pg[m + 4 - M] + 16 * sl[m + 4 - M] : pg[m] + 16 * sl[m]) + gq * 16 + tq * 4;
+      }
 #pragma unroll 1
       for (int c = 0; c < kC; ++c) {
         uint4 q[NB];
@@ -311,12 +324,10 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
         for (int i = 0; i < NB; ++i) q[i] = *reinterpret_cast<const uint4*>(mine + L::kQ + (i * kC + c) * 512 + lane * 16);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          const int k = kb + 16 * m + gq;
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + (k >> shift) * blk_e +
-                                                                (c * Pe + (k & (Pe - 1))) * 16) + tq;
           uint32_t x[4], y[4];
-          decode8(w[0], x);                      // key g
-          decode8(w[32], y);                     // key g + 8: the same page
+          decode8(*reinterpret_cast<const uint32_t*>(kp[m]), x, magic);         // key g
+          decode8(*reinterpret_cast<const uint32_t*>(kp[m] + 128), y, magic);   // key g + 8: the same page
+          kp[m] += Pe * 16;
           const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
@@ -360,19 +371,18 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     float sv[M][2];
     const bool full = !tree && nkeys == kChunk && key0 + kChunk <= low_vis &&
                       (P > kChunk ? pages != 0 : pages == (1u << (kChunk >> shift)) - 1u);
-    uint64_t seen = 0ull;                        // bit 4 (M i + m) + k: that score counts
+    uint32_t seen = 0u;                          // bit 4 (M i + m) + k: that score counts
     {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int k = kb + 16 * m + gq + 8 * b;
           float sk = c2;
           sv[m][b] = 1.f;
           if (!tree) {
-            const uint8_t* blkp = stage + (k >> shift) * blk_e;
-            sk = c2 * bf16_at(reinterpret_cast<const uint16_t*>(blkp + k_scale(Pe, D, k & (Pe - 1))));
-            sv[m][b] = bf16_at(reinterpret_cast<const uint16_t*>(blkp + v_scale(Pe, D, k & (Pe - 1))));
+            const uint8_t* at = stage + (kb ? pg[m + 4 - M] + 2 * sl[m + 4 - M] : pg[m] + 2 * sl[m]) + Pe * D + 2 * gq + 16 * b;
+            sk = c2 * bf16_at(reinterpret_cast<const uint16_t*>(at));
+            sv[m][b] = bf16_at(reinterpret_cast<const uint16_t*>(at + 2 * Pe));
           }
           const uint64_t sk2 = pair(sk, sk);
 #pragma unroll
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 sees[q] = there && (tree ? (anc[2 * i + q] >> (k & 31)) & 1u : key0 + k < vis[2 * i + q]);
-                if (sees[q]) seen |= 1ull << (4 * M * i + 4 * m + 2 * b + q);
+                if (sees[q]) seen |= 1u << (4 * M * i + 4 * m + 2 * b + q);
                 else v[q] = -INFINITY;
               }
               y[m][i][b] = pair(v[0], v[1]);
@@ -481,26 +491,39 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
           const uint64_t w = pair(ex2(v0), ex2(v1));
           l[i] = add2(l[i], w);
           split(mul2(w, sv2), v0, v1);
-          if (__builtin_expect(!full, 0)) {
-            // zero weights times the scale of a value row that was not finite are NaN: rows that do not see it stay clean
-            if (!((seen >> (4 * M * i + 4 * m + 2 * b)) & 1ull)) v0 = 0.f;
-            if (!((seen >> (4 * M * i + 4 * m + 2 * b + 1)) & 1ull)) v1 = 0.f;
-          }
-          pb[m][i][b] = transpose8x8(tc::pack_bf16(v0, v1));
+          pb[m][i][b] = tc::pack_bf16(v0, v1);
         }
       }
+    if (__builtin_expect(!full, 0)) {
+      // zero weights times the scale of a value row that was not finite are NaN: rows that do not see it stay clean
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t two = seen >> (4 * M * i + 4 * m + 2 * b);
+            pb[m][i][b] &= (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+          }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) pb[m][i][b] = transpose8x8(pb[m][i][b]);
 
     // ---- O^T += V^T P^T
     if (!tree) {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const uint8_t* vg = stage + ((kb + 16 * m) >> shift) * blk_e + Pe * (D / 2) +
-                            (((kb + 16 * m) & (Pe - 1)) >> 4) * (D * 8) + gq * 16;
+        const uint8_t* vg = stage + (kb ? pg[m + 4 - M] + sl[m + 4 - M] * (D / 2) : pg[m] + sl[m] * (D / 2)) + Pe * (D / 2) +
+                            gq * 16;
 #pragma unroll
         for (int d = 0; d < kDm; ++d) {
           const uint4 w = *reinterpret_cast<const uint4*>(vg + d * 128);   // dims 16 d + 2g, + 1: tokens 0-7, 8-15
-          const uint32_t f[4] = {decode_pair(w.x >> (4 * tq)), decode_pair(w.z >> (4 * tq)),
-                                 decode_pair(w.y >> (4 * tq)), decode_pair(w.w >> (4 * tq))};
+          const uint32_t f[4] = {decode_pair(w.x >> (4 * tq), magic), decode_pair(w.z >> (4 * tq), magic),
+                                 decode_pair(w.y >> (4 * tq), magic), decode_pair(w.w >> (4 * tq), magic)};
 #pragma unroll
           for (int i = 0; i < NB; ++i) mma16816(o[d][i], f, pb[m][i][0], pb[m][i][1]);
         }
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     }
 
     __syncwarp();                                // the stage was read
-    if (blk != u.nb - 1 && pos != w1 - 1) {
+    if (blk != u.nb - 1 && it != n - 1) {
       ++blk;
       continue;
     }
@@ -544,7 +567,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     const bool whole = seg_blk == 0 && blk == u.nb - 1;
     const int64_t slot = 2 * worker + (seg_blk == 0 ? 1 : 0);
     if (seg_blk == 0 && blk != u.nb - 1 && lane == 0) {
-      const long long u1 = pos + (u.nb - blk);            // position after the unit
+      const long long u1 = w0 + it + (u.nb - blk);        // position after the unit
       const long long k = (u1 * G + W - 1) / W - 1;       // run of its last chunk
       p.desc[worker] = make_int4(static_cast<int>(k) - worker + 1, e, h, 0);
     }
@@ -602,8 +625,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   }
   // after an expired wait: copies in flight land before the CTA ends
   if (*abort_flag) {
-    const int loaded = static_cast<int>(lpos - w0);
-    for (int it = max(0, loaded - 2); it < loaded; ++it) {
+    for (int it = max(0, lnext - 2); it < lnext; ++it) {
       const long long t0 = clock64();
       while (!tc::mbar_try(bars + 8 * (it & 1), (it >> 1) & 1) && clock64() - t0 < kWaitClocks) {
       }
@@ -697,6 +719,7 @@ size_t attn_mma_workspace(int B, int max_nodes, int Hq, int Hkv, int d) {
 int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st) {
   MmaArgs p{};
   p.a = a;
+  p.magic = kMagic;
   const int nb = blocks_of(a.max_nodes, a.Hq / a.Hkv), R = 8 * nb;
   p.workers = sm_count() * warps_of(nb);
   char* base = static_cast<char*>(ws);

@@ -111,6 +111,7 @@ struct TcArgs {
   float* o;          // [2 grid][N][D]
   const int4* extents;   // [B * tiles] from extent_kernel, or NULL
   int nq, tiles, grid;
+  uint32_t magic;        // kMagic
 };
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -497,10 +498,10 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
           const uint4 now = w;
           from += a.page_size;
           if (c + 1 < D / 32) w = *from;
-          decode8(now.x, r);
-          decode8(now.y, r + 4);
-          decode8(now.z, r + 8);
-          decode8(now.w, r + 12);
+          decode8(now.x, r, p.magic);
+          decode8(now.y, r + 4, p.magic);
+          decode8(now.z, r + 8, p.magic);
+          decode8(now.w, r + 12, p.magic);
           tmem_st16(dst + 16 * c, r);
         }
       } else {
@@ -558,10 +559,10 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, 1) attn_kernel(const __gr
               w0 = word(2 * c + 2);
               w1 = word(2 * c + 3);
             }
-            decode8(a0.x, r);
-            decode8(a0.y, r + 4);
-            decode8(a1.x, r + 8);
-            decode8(a1.y, r + 12);
+            decode8(a0.x, r, p.magic);
+            decode8(a0.y, r + 4, p.magic);
+            decode8(a1.x, r + 8, p.magic);
+            decode8(a1.y, r + 12, p.magic);
             tmem_st16(dst + 16 * c, r);
           }
         } else {
@@ -982,6 +983,7 @@ size_t attn_tc_workspace(int B, int max_nodes, int Hq, int Hkv, int d) {
 int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st) {
   TcArgs p{};
   p.a = a;
+  p.magic = kMagic;
   const int g = a.Hq / a.Hkv, N = kRows;
   p.grid = sm_count();
   p.nq = N / g;

@@ -46,17 +46,22 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // Codes in bits 0-3 and 16-19 -> bf16 pair of n = code - 8 (128 + code - 136, exact).
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w) {
-  const uint32_t bias = 0x43084308u;   // bf16 136, 136
-  const uint32_t x = (w & 0x000f000fu) | 0x43004300u;
+// `magic` is kMagic by way of a kernel argument: with both constants known
+// the assembler takes two logic instructions, an instruction having room for
+// one immediate; the logic pipe is what bounds the dequantisation.
+constexpr uint32_t kMagic = 0x43004300u;   // bf16 128, 128
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t magic) {
+  const uint32_t bias = 0x43084308u;       // bf16 136, 136
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "n"(0x000f000f), "r"(magic));   // (w & mask) | magic
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
                                    *reinterpret_cast<const __nv_bfloat162*>(&bias));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 // A code word -> its four pairs (items 2i, 2i + 1).
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t* r) {
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t* r, uint32_t magic) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = decode_pair(w >> (4 * i));
+  for (int i = 0; i < 4; ++i) r[i] = decode_pair(w >> (4 * i), magic);
 }
 
 // Bounded waits.  The clock is read only once in many polls: a poll is a few
