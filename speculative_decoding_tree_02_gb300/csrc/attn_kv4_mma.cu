@@ -23,7 +23,7 @@
 //
 // The list of all units (request, KV head), in chunks, is cut into equal runs,
 // one per warp; a unit that a run's end cuts leaves fp32 partials that
-// join_kernel joins in run order.
+// attn_join joins in run order.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -50,9 +50,7 @@ struct Lay {
 struct MmaArgs {
   AttnArgs a;
   int* status;
-  int4* desc;             // [workers] (pieces, request, KV head): a unit that starts in a run and ends in another
-  float2* ml;             // [2 workers][8 NB]
-  float* o;               // [2 workers][8 NB][D]
+  Pieces pieces;          // runs = workers, 8 NB rows
   const int4* extents;    // [B] x = visible prefix (per-node prefixes), or NULL
   int workers;
   uint32_t magic;         // kMagic
@@ -128,7 +126,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   // at least two chunks to a run: a shorter one costs more to join than to do
   const long long G = min(static_cast<long long>(p.workers), (W + 1) / 2);
   const int worker = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp;   // neighbours on other SMs
-  if (lane == 0) p.desc[worker] = make_int4(0, 0, 0, 0);
+  if (lane == 0) p.pieces.desc[worker] = make_int4(0, 0, 0, 0);
   if (worker >= G) return;
   const long long w0 = worker * W / G, w1 = (worker + 1) * W / G;
   int e = 0;
@@ -569,7 +567,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     if (seg_blk == 0 && blk != u.nb - 1 && lane == 0) {
       const long long u1 = w0 + it + (u.nb - blk);        // position after the unit
       const long long k = (u1 * G + W - 1) / W - 1;       // run of its last chunk
-      p.desc[worker] = make_int4(static_cast<int>(k) - worker + 1, e, h, 0);
+      p.pieces.desc[worker] = make_int4(static_cast<int>(k) - worker + 1, e, 0, h);
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -590,8 +588,8 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
 #pragma unroll
           for (int d = 0; d < kDm; ++d) out[8 * d] = tc::pack_bf16(o[d][i][q] * f, o[d][i][2 + q] * f);
         } else {
-          if (gq == 0) p.ml[slot * R + r] = make_float2(sum[q] == 0.f ? kLow : -m[q], sum[q]);
-          float2* out = reinterpret_cast<float2*>(p.o + (slot * R + r) * D + 2 * gq);
+          if (gq == 0) p.pieces.ml[slot * R + r] = make_float2(sum[q] == 0.f ? kLow : -m[q], sum[q]);
+          float2* out = reinterpret_cast<float2*>(p.pieces.o + (slot * R + r) * D + 2 * gq);
 #pragma unroll
           for (int d = 0; d < kDm; ++d) out[8 * d] = make_float2(o[d][i][q], o[d][i][2 + q]);
         }
@@ -615,7 +613,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
               uint16_t* o16 = static_cast<uint16_t*>(a.out) + row_at(r) * D + dim;
               *o16 = static_cast<uint16_t>(tc::pack_bf16(bf16_at(o16) + __uint_as_float(v << 16), 0.f));
             } else {
-              p.o[(slot * R + r) * D + dim] += __uint_as_float(v << 16);
+              p.pieces.o[(slot * R + r) * D + dim] += __uint_as_float(v << 16);
             }
           }
         }
@@ -633,69 +631,11 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   }
 }
 
-// Joins the pieces of a unit that was cut: piece 0 is slot 1 of the worker
-// where the unit starts, piece i slot 0 of the i-th worker after it.  CTA =
-// starting worker, warp = row, lane = D / 32 dims.
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const MmaArgs p, int R) {
-  griddep_wait();
-  griddep_release();
-  const int4 d = p.desc[blockIdx.x];
-  if (d.x < 2) return;
-  const AttnArgs& a = p.a;
-  const int g = a.Hq / a.Hkv, lane = threadIdx.x & 31;
-  const Span s = node_span(a, d.y);
-  constexpr int kV = D / 32, kAhead = 8;         // dims per lane, pieces whose loads are in flight together
-  for (int r = threadIdx.x >> 5; r < s.cnt * g; r += 8) {
-    auto slot = [&](int i) {
-      return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * R + r;
-    };
-    float M = kLow, sum = 0.f, acc[kV];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) acc[k] = 0.f;
-    for (int i0 = 0; i0 < d.x; i0 += kAhead) {
-      float2 ml[kAhead];
-      float o[kAhead][kV];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        ml[i] = make_float2(kLow, 0.f);
-        if (i0 + i < d.x) {
-          ml[i] = p.ml[slot(i0 + i)];
-#pragma unroll
-          for (int k = 0; k < kV; ++k) o[i][k] = p.o[slot(i0 + i) * D + 32 * k + lane];
-        }
-      }
-      const float old = M;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) M = fmaxf(M, ml[i].x);
-      const float keep = ex2(old - M);
-      sum *= keep;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] *= keep;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (ml[i].y == 0.f) continue;            // nothing seen in this piece
-        const float w = ex2(ml[i].x - M);
-        sum = fmaf(w, ml[i].y, sum);
-#pragma unroll
-        for (int k = 0; k < kV; ++k) acc[k] = fmaf(w, o[i][k], acc[k]);
-      }
-    }
-    const int64_t row = static_cast<int64_t>(s.n0 + r / g) * a.Hq + d.z * g + r % g;
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int k = 0; k < kV; ++k)
-      static_cast<uint16_t*>(a.out)[row * D + 32 * k + lane] = static_cast<uint16_t>(tc::pack_bf16(acc[k] * f, 0.f));
-    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
-  }
-}
-
 int blocks_of(int max_nodes, int g) {            // blocks of eight rows
   const int rows = max_nodes * g;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 int warps_of(int nb) { return nb == 1 ? Lay<128, 1>::kWarps : Lay<128, 4>::kWarps; }
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 template <int D, int NB>
 int launch(const MmaArgs& p, cudaStream_t st) {
@@ -703,35 +643,27 @@ int launch(const MmaArgs& p, cudaStream_t st) {
   if (!smem_limit(mma_kernel<D, NB>, static_cast<int>(L::kBytes))) return TV_ECUDA;
   const int rc = launch_pdl(mma_kernel<D, NB>, dim3(p.workers / L::kWarps), dim3(32 * L::kWarps), L::kBytes, st, p);
   if (rc != TV_OK) return rc;
-  return launch_pdl(join_kernel<D>, dim3(p.workers), dim3(256), 0, st, p, 8 * NB);
+  return attn_join(p.a, p.pieces, p.workers, 8 * NB, p.a.max_nodes, st);
 }
 
 }  // namespace
 
-// [status word (256 B)] [extents] [pieces of cut units] [partial (m, l)] [partial o]
+// [status word (256 B)] [extents] [pieces of cut units]
 size_t attn_mma_workspace(int B, int max_nodes, int Hq, int Hkv, int d) {
   const int nb = blocks_of(max_nodes, Hq / Hkv);
-  const size_t G = static_cast<size_t>(sm_count()) * warps_of(nb), R = 8 * nb;
-  return 256 + align256(static_cast<size_t>(B) * sizeof(int4)) + align256(G * sizeof(int4)) +
-         align256(2 * G * R * sizeof(float2)) + 2 * G * R * d * sizeof(float);
+  return 256 + align256(static_cast<size_t>(B) * sizeof(int4)) + pieces_bytes(sm_count() * warps_of(nb), 8 * nb, d);
 }
 
 int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st) {
   MmaArgs p{};
   p.a = a;
   p.magic = kMagic;
-  const int nb = blocks_of(a.max_nodes, a.Hq / a.Hkv), R = 8 * nb;
+  const int nb = blocks_of(a.max_nodes, a.Hq / a.Hkv);
   p.workers = sm_count() * warps_of(nb);
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<int*>(base);
-  base += 256;
-  int4* extents = reinterpret_cast<int4*>(base);
-  base += align256(static_cast<size_t>(a.B) * sizeof(int4));
-  p.desc = reinterpret_cast<int4*>(base);
-  base += align256(static_cast<size_t>(p.workers) * sizeof(int4));
-  p.ml = reinterpret_cast<float2*>(base);
-  base += align256(2ull * p.workers * R * sizeof(float2));
-  p.o = reinterpret_cast<float*>(base);
+  int4* extents = reinterpret_cast<int4*>(base + 256);
+  p.pieces = pieces_at(base + 256 + align256(static_cast<size_t>(a.B) * sizeof(int4)), p.workers, 8 * nb);
   if (a.vis_prefix) {
     const int rc = attn_extents(a, a.max_nodes, 1, extents, st);
     if (rc != TV_OK) return rc;

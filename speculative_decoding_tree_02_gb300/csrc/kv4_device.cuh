@@ -64,15 +64,33 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t* r, uint32_t magic)
   for (int i = 0; i < 4; ++i) r[i] = decode_pair(w >> (4 * i), magic);
 }
 
-// Bounded waits.  The clock is read only once in many polls: a poll is a few
-// cycles, reading a timer in every one delays what is waited for.
+// Bounded waits.  A poll is a handful of instructions in a tight loop (the
+// warps that wait share the issue slots with those that work); the clock is
+// read once in 64 polls.
 constexpr long long kWaitClocks = 4000000000ll;   // about 2 s
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+__device__ __forceinline__ bool poll64(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 64;\n\t"
+      "WAIT%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT%=;\n\t"
+      "DONE%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  if (poll64(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-      if (tc::mbar_try(bar, parity)) return true;
+    if (poll64(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitClocks) break;
   }
@@ -82,15 +100,26 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatil
 }
 // By a whole warp: true when the phase is over, the same in all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
-  bool ok = tc::mbar_try(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, ok || wait_slow(bar, parity, abort_flag, err, code));
-  return ok;
+  return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, err, code));
 }
 
 // Per entry (request x row tile of nq nodes) the visible prefix, the first and
-// the number of 128-node tree tiles (see attn_kv4_tc.cu): for calls where
-// these do not follow from the lengths alone.
+// the number of 128-node tree tiles: for calls where these do not follow from
+// the lengths alone (nodes with prefixes of their own, larger trees).
+constexpr int kTreeTile = 128;
 int attn_extents(const AttnArgs& a, int nq, int tiles, int4* out, cudaStream_t st);
+
+// Partial results of units that the end of a run cuts: a run has two slots
+// (0: the unit was begun by an earlier run, 1: it begins here), R rows each.
+struct Pieces {
+  int4* desc;      // [runs] pieces, request, row tile, KV head of a unit that begins in a run and ends in another
+  float2* ml;      // [2 runs][R] reference (base-2 units), sum
+  float* o;        // [2 runs][R][d] unnormalised
+};
+inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+size_t pieces_bytes(int runs, int R, int d);
+Pieces pieces_at(char* base, int runs, int R);
+int attn_join(const AttnArgs& a, const Pieces& p, int runs, int R, int nq, cudaStream_t st);
 
 }  // namespace kv4
 }  // namespace tv
