@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(128) extent_kernel(const AttnArgs a, int nq, i
 }
 
 // Piece 0 of a cut unit is slot 1 of the run where the unit starts, piece i
-// slot 0 of the i-th run after it.  CTA = starting run, warp = row, lane =
-// D / 32 dims; the pieces are taken in run order, eight loads in flight.
+// slot 0 of the i-th run after it.  CTA = (starting run, eight rows), warp =
+// row, lane = D / 32 dims; the pieces are taken in run order, eight loads in
+// flight.  (One CTA for all 64 rows of a run took 12 us instead of JOINUS.)
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, const Pieces p, int R, int nq) {
   griddep_wait();
@@ -56,7 +57,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, const Piece
   const Span s = node_span(a, d.y);
   const int rows = min(nq, s.cnt - d.z * nq) * g;
   constexpr int kV = D / 32, kAhead = 8;
-  for (int r = threadIdx.x >> 5; r < rows; r += 8) {
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (r < rows) {
     auto slot = [&](int i) {
       return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * R + r;
     };
@@ -107,8 +109,8 @@ int attn_extents(const AttnArgs& a, int nq, int tiles, int4* out, cudaStream_t s
 }
 
 int attn_join(const AttnArgs& a, const Pieces& p, int runs, int R, int nq, cudaStream_t st) {
-  return a.d == 128 ? launch_pdl(join_kernel<128>, dim3(runs), dim3(256), 0, st, a, p, R, nq)
-                    : launch_pdl(join_kernel<64>, dim3(runs), dim3(256), 0, st, a, p, R, nq);
+  return a.d == 128 ? launch_pdl(join_kernel<128>, dim3(runs, R / 8), dim3(256), 0, st, a, p, R, nq)
+                    : launch_pdl(join_kernel<64>, dim3(runs, R / 8), dim3(256), 0, st, a, p, R, nq);
 }
 
 size_t pieces_bytes(int runs, int R, int d) {

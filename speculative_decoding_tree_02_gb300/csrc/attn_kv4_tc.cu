@@ -23,10 +23,10 @@
 // A CTA is two teams of two warpgroups that share nothing but the SM: each
 // team walks its own run of the list of all units (request, row tile, KV head;
 // a unit's tiles of 128 cached tokens, then of 128 nodes, follow one another),
-// so that one dequantises while the other takes its softmax.  In a team the
-// first warpgroup writes K and issues S, the second writes V^T beside it; then
+// so that one dequantises while the other takes its softmax.  In a team each
+// warpgroup writes half of K's columns, then, beside S, half of V^T's; then
 // both take the softmax of 32 rows each, write P, and PV runs beside the next
-// tile's K and V.  A unit cut by a run's end leaves fp32 partials that
+// tile's K.  A unit cut by a run's end leaves fp32 partials that
 // attn_join joins in run order.
 // Measured on 64 chains of 16 nodes x 32 heads over 512..4096 tokens: with
 // dequantising, softmax and MMA issue in warps of their own that hand tiles
@@ -68,7 +68,7 @@ struct Lay {
   static constexpr uint32_t kRow = kVis + 256;                // int [64] output row, -1: none
   static constexpr uint32_t kAnc = kRow + 256;                // u32 [4][64]
   static constexpr uint32_t kWarpMax = kAnc + 1024;           // int [4][64]
-  static constexpr uint32_t kPages = kWarpMax + 1024;         // u32 [kStages] staged groups of 16 tokens
+  static constexpr uint32_t kPages = kWarpMax + 1024;         // u32 [kStages] bit i: page i of the tile is staged
   static constexpr uint32_t kBars = kPages + 32;              // RAW [kStages], S, PV, DRAIN
   static constexpr uint32_t kTeam = (kBars + 64 + 1023) / 1024 * 1024;    // bytes of a team
   static constexpr uint32_t kMisc = 2 * kTeam;                // tensor memory address, abort flag, entry sums
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   // aligned by an offset, so that the compiler still knows the pointer to be one to shared memory
   uint8_t* sm0 = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const AttnArgs& a = p.a;
-  const int team = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;   // warpgroup of the team: 0 keys, 1 values
+  const int team = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;   // warpgroup of the team
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31, c0 = kCols * half;
   const int tbar = 1 + team, wid = 3 + 2 * team + half;
   const int g = a.Hq / a.Hkv;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   auto raw_bar = [&](int st) { return sb + L::kBars + 8u * st; };
   const uint32_t s_bar = sb + L::kBars + 8 * kStages, pv_bar = s_bar + 8, drain_bar = s_bar + 16;
   if (tid == 0 && half == 0) {
-    for (int i = 0; i < kStages + 3; ++i) mbar_init(sb + L::kBars + 8 * i, 1);
+    for (int i = 0; i < kStages + 3; ++i) mbar_init(sb + L::kBars + 8 * i, i == kStages + 2 ? 2 : 1);
     if (team == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -216,9 +216,9 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
 
     const uint32_t blk_bytes = static_cast<uint32_t>(a.page_size) * (D + 4);
     const int ps_shift = 31 - __clz(a.page_size), per_tile = kKeys >> ps_shift;
-    const bool loader = half == 0 && warp == 0;
+    const bool loader = half == 1 && warp == 3;
     // ---- loads (one warp): kStages tiles ahead, their page numbers one more
-    int le = e, lh = h, lblk = blk, lnext = 0, lpage = -1;
+    int le = e, lh = h, lblk = blk, lnext = 0, lpage = -1, lr = e / p.tiles, lt = e % p.tiles;
     Extent lx = x;
     auto look = [&]() {                          // this lane's page of the next tile to load
       lpage = -1;
@@ -227,13 +227,15 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         lblk = 0;
         if (++lh == a.Hkv) {
           lh = 0;
-          do lx = extent_of(p, ++le);
-          while (lx.nb == 0 && le + 1 < E);
+          do {
+            lx = extent_of(p, ++le);
+            if (++lt == p.tiles) { lt = 0; ++lr; }
+          } while (lx.nb == 0 && le + 1 < E);
         }
       }
       const int key = lblk * kKeys + (lane << ps_shift);
       if (lblk < lx.np && lane < per_tile && key < lx.len)
-        lpage = a.block_table[static_cast<int64_t>(le / p.tiles) * a.table_ld + (key >> ps_shift)];
+        lpage = a.block_table[static_cast<int64_t>(lr) * a.table_ld + (key >> ps_shift)];
     };
     auto load = [&](int st) {
       if (lnext >= n) return;
@@ -242,10 +244,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       if (wanted && !ok && a.err) *a.err = 1;
       const unsigned have = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) {
-        uint32_t groups = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) groups |= ((have >> ((16 * i) >> ps_shift)) & 1u) << i;
-        *reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) = groups;
+        *reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) = have;
         if (have) mbar_expect_tx(raw_bar(st), __popc(have) * blk_bytes);
         else mbar_arrive(raw_bar(st));
       }
@@ -265,16 +264,18 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
     }
 
-    // ---- per thread: a key of each tile (and, in the second warpgroup, a dim)
+    // ---- per thread: a key, then a dim, of each tile (half of its words)
     const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
     const int slot = tid & (a.page_size - 1), page_off = (tid >> ps_shift) * static_cast<int>(blk_bytes);
-    const int key_off = page_off + slot * 16, chunk_step = a.page_size * 16;
+    const int chunk_step = a.page_size * 16, key_off = page_off + slot * 16 + half * (D / 64) * chunk_step;
     const int scale_off = page_off + k_scale(a.page_size, D, slot);
-    int group_off[8];                            // a tile's groups of 16 tokens in the staged pages, at this dim
+    int group_off[4];                            // groups of 16 tokens of this half in the staged pages, at this dim
 #pragma unroll
-    for (int gr = 0; gr < 8; ++gr)
-      group_off[gr] = ((16 * gr) >> ps_shift) * static_cast<int>(blk_bytes) + a.page_size * (D / 2) +
-                      ((16 * gr) & (a.page_size - 1)) * (D / 2) + tid * 8;
+    for (int i = 0; i < 4; ++i) {
+      const int k0 = 64 * half + 16 * i;
+      group_off[i] = (k0 >> ps_shift) * static_cast<int>(blk_bytes) + a.page_size * (D / 2) +
+                     (k0 & (a.page_size - 1)) * (D / 2) + tid * 8;
+    }
     const float c2 = a.scale * kLog2e;
     // a row's reference (what its scores are taken over) is kept negated; -0: none yet
     float* nref = reinterpret_cast<float*>(sm + L::kRef) + c0;
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
 #pragma unroll
     for (int c = 0; c < kCols / 2; ++c) l[c] = 0ull;
     volatile int* dirty = reinterpret_cast<volatile int*>(sm + L::kPages + 16);   // non-finite tree values met
+    volatile int* low_vis = reinterpret_cast<volatile int*>(sm + L::kPages + 20);  // [2] prefix that all rows see
     bool force = false, fresh = true;            // a row without reference; a new unit
     int seg_blk = blk, r = 0, t = 0, n0 = 0, cnt = 0;
     int st = 0, turn = 0, it = 0;
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         n0 = sp.n0;
         cnt = sp.cnt;
         const int node0 = t * p.nq, rows = min(p.nq, cnt - node0) * g;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = tid + 128 * half; i < kRowsT * (D / 8); i += 256) {
           const int rr = i / (D / 8), c = i % (D / 8);
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -327,7 +329,10 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           const int rr = c0 + tid, gn = n0 + node0 + rr / g;
           nref[tid] = -0.f;
           row_s[tid] = rr < rows ? gn * a.Hq + h * g + rr % g : -1;
-          vis_s[tid] = rr < rows ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
+          const int vis = rr < rows ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
+          vis_s[tid] = vis;
+          const int lowest = __reduce_min_sync(0xffffffffu, rr < rows ? vis : 0x7fffffff);
+          if (tid == 0) low_vis[half] = lowest;
         }
         force = false;
         if (tid == 0 && half == 0) *dirty = 0;
@@ -339,19 +344,23 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       if (!warp_wait(raw_bar(st), turn, abort_flag, p.status, 41)) break;
       const uint8_t* raw = sm + L::kRaw + st * L::kStage;
 
-      // ---- this key's scales; the rows' masks over a tile of nodes
-      float sk = c2, sv = 1.f;
+      // ---- K: thread = key, half of the dims
       bool valid = tid < nkeys;
       if (!tree) {
-        valid = valid && ((*reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) >> (tid >> 4)) & 1u);
-        if (valid) {
-          sk = c2 * bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off));
-          sv = bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off + 2 * a.page_size));
-        } else {
-          sk = sv = 0.f;
+        uint4 w[D / 64];
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + key_off + c * chunk_step);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t v[16];
+          decode8(w[c].x, v, p.magic);
+          decode8(w[c].y, v + 4, p.magic);
+          decode8(w[c].z, v + 8, p.magic);
+          decode8(w[c].w, v + 12, p.magic);
+          tmem_st16(tmem + L::tK + lane_off + half * (D / 4) + 16 * c, v);
         }
       } else {
-        if (tid < kCols) {
+        if (tid < kCols) {                       // the rows' masks over the tile's nodes
           const int row = row_s[tid];
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
@@ -362,98 +371,92 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
             anc_s[(2 * w + 1) * kRowsT + tid] = static_cast<uint32_t>(v >> 32);
           }
         }
+        const uint16_t* row = static_cast<const uint16_t*>(a.k_tree) +
+                              static_cast<int64_t>(n0 + key0 + min(tid, nkeys - 1)) * a.ldk + static_cast<int64_t>(h) * D +
+                              half * (D / 2);   // (places without nodes: the last one, masked below)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + 32 * c + 8 * i);
+            v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
+          }
+          tmem_st16(tmem + L::tK + lane_off + half * (D / 4) + 16 * c, v);
+        }
       }
-      const int key = valid && !tree ? key0 + tid : 0x7fffffff;
-      if (half == 0) {
-        // ---- K: thread = key
+      tmem_st_wait();
+      tc_fence_before();
+      team_sync(tbar);
+      if (half == 0 && tid == 0) {
+        tc_fence_after();
+        constexpr uint32_t idS = idesc_bf16(128, kRowsT, 0);
+        const uint64_t qdesc = sdesc(sb + L::kQ, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)      // descriptors count 16 bytes
+          umma_bf16_ts(tmem + L::tS, tmem + L::tK + 8 * kk, qdesc + ((kk >> 2) * L::kQHalf + (kk & 3) * 32) / 16, idS, kk > 0);
+        umma_commit(s_bar);
+      }
+      __syncwarp();
+
+      // ---- V^T: thread = dim, half of the tokens, once PV of the tile before has read the last one
+      if (it > 0 && !warp_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 42)) break;
+      tc_fence_after();
+      if (32 * warp < D) {                       // d = 64: the upper lanes' results are not used
         if (!tree) {
-          const uint8_t* from = raw + key_off;
-          uint4 w = *reinterpret_cast<const uint4*>(from);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {     // rolled: small code, the next word on its way
+          uint2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint2*>(raw + group_off[i]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             uint32_t v[16];
-            const uint4 now = w;
-            from += chunk_step;
-            if (c + 1 < D / 32) w = *reinterpret_cast<const uint4*>(from);
-            decode8(now.x, v, p.magic);
-            decode8(now.y, v + 4, p.magic);
-            decode8(now.z, v + 8, p.magic);
-            decode8(now.w, v + 12, p.magic);
-            tmem_st16(tmem + L::tK + lane_off + 16 * c, v);
+            decode8(w[2 * c].x, v, p.magic);
+            decode8(w[2 * c].y, v + 4, p.magic);
+            decode8(w[2 * c + 1].x, v + 8, p.magic);
+            decode8(w[2 * c + 1].y, v + 12, p.magic);
+            tmem_st16(tmem + L::tV + lane_off + 32 * half + 16 * c, v);
           }
         } else {
-          const uint16_t* row = static_cast<const uint16_t*>(a.k_tree) +
-                                static_cast<int64_t>(n0 + key0 + (valid ? tid : 0)) * a.ldk + static_cast<int64_t>(h) * D;
+          // a value that is not finite must not meet the zero weights of rows that do not see it: it is taken
+          // out here and added at the end to the rows that see it
+          bool bad = false;
+          const uint16_t* rows = static_cast<const uint16_t*>(a.v_tree) + static_cast<int64_t>(n0 + key0) * a.ldv +
+                                 static_cast<int64_t>(h) * D + tid;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
             uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 w = valid ? *reinterpret_cast<const uint4*>(row + 32 * c + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-              v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
-            }
-            tmem_st16(tmem + L::tK + lane_off + 16 * c, v);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        wg_sync(wid);
-        if (tid == 0) {
-          tc_fence_after();
-          constexpr uint32_t idS = idesc_bf16(128, kRowsT, 0);
-          const uint64_t qdesc = sdesc(sb + L::kQ, 16, 1024);
+            for (int i = 0; i < 16; ++i) v[i] = 0u;   // places without nodes are zeros
+            if (32 * c < nkeys) {
+              // all loads first (beyond the last node: that node again), in one latency
+              uint16_t x[32];
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)    // descriptors count 16 bytes
-            umma_bf16_ts(tmem + L::tS, tmem + L::tK + 8 * kk, qdesc + ((kk >> 2) * L::kQHalf + (kk & 3) * 32) / 16, idS, kk > 0);
-          umma_commit(s_bar);
-        }
-        __syncwarp();
-      } else {
-        // ---- V^T: thread = dim, once PV of the tile before has read the last one
-        if (it > 0 && !warp_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 42)) break;
-        tc_fence_after();
-        if (32 * warp < D) {                     // d = 64: the upper lanes' results are not used
-          if (!tree) {
+              for (int i = 0; i < 32; ++i) x[i] = rows[static_cast<int64_t>(min(32 * c + i, nkeys - 1)) * a.ldv];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[16];
-              const uint2 w = *reinterpret_cast<const uint2*>(raw + group_off[2 * c]);
-              const uint2 u = *reinterpret_cast<const uint2*>(raw + group_off[2 * c + 1]);
-              decode8(w.x, v, p.magic);
-              decode8(w.y, v + 4, p.magic);
-              decode8(u.x, v + 8, p.magic);
-              decode8(u.y, v + 12, p.magic);
-              tmem_st16(tmem + L::tV + lane_off + 16 * c, v);
-            }
-          } else {
-            bool bad = false;
-            // a value that is not finite must not meet the zero weights of rows that do not see it: it is taken
-            // out here and added at the end to the rows that see it
-            const uint16_t* from = static_cast<const uint16_t*>(a.v_tree) + static_cast<int64_t>(n0 + key0) * a.ldv +
-                                   static_cast<int64_t>(h) * D + tid;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int k0 = 32 * c + 2 * i;
-                uint32_t lo = 0u, hi = 0u;       // (places without nodes are stored as zeros)
-                if (k0 < nkeys) lo = *from;
-                from += a.ldv;
-                if (k0 + 1 < nkeys) hi = *from;
-                from += a.ldv;
-                if ((lo & 0x7f80u) == 0x7f80u) { lo = 0u; bad = true; }
-                if ((hi & 0x7f80u) == 0x7f80u) { hi = 0u; bad = true; }
-                v[i] = lo | (hi << 16);
+              for (int i = 0; i < 32; ++i) {
+                uint32_t e = 32 * c + i < nkeys ? x[i] : 0u;
+                if ((e & 0x7f80u) == 0x7f80u) { e = 0u; bad = true; }
+                v[i >> 1] |= e << (16 * (i & 1));
               }
-              tmem_st16(tmem + L::tV + lane_off + 16 * c, v);
             }
-            if (bad) *dirty = 1;
+            tmem_st16(tmem + L::tV + lane_off + 16 * c, v);
           }
-          tmem_st_wait();
+          if (bad) *dirty = 1;
         }
-        if (tree) wg_sync(wid);                  // the masks are there
       }
+      // this key's scales
+      float sk = c2, sv = 1.f;
+      if (!tree) {
+        valid = valid && ((*reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) >> (tid >> ps_shift)) & 1u);
+        sk = valid ? c2 * bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off)) : 0.f;
+        sv = valid ? bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off + 2 * a.page_size)) : 0.f;
+      }
+      const int key = valid && !tree ? key0 + tid : 0x7fffffff;
+      if (loader && it > 0) {                    // the stage of the tile before, which all have read
+        load(st == 0 ? kStages - 1 : st - 1);
+        look();
+      }
+      tmem_st_wait();
 
       // ---- softmax: thread = key; scores in base-2 units over the rows' references, two rows to a register pair
       if (!warp_wait(s_bar, it & 1, abort_flag, p.status, 43)) break;
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           y[c / 2 + 1] = fma2(pair(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sk2, m.y);
         }
       }
-      if (__builtin_expect(tree || a.vis_prefix != nullptr || !__all_sync(0xffffffffu, valid), 0)) {
+      if (__builtin_expect(tree || key0 + kKeys > low_vis[half] || !__all_sync(0xffffffffu, valid), 0)) {
         const uint32_t* words = anc_s + warp * kRowsT;
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) {
@@ -534,9 +537,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           l[c / 2] = mul2(l[c / 2], f.x);
           l[c / 2 + 1] = mul2(l[c / 2 + 1], f.y);
         }
-        if (!first) {
-          if (!warp_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 46)) break;
-          tc_fence_after();
+        if (!first) {                            // (PV of the tile before has completed: waited for above)
 #pragma unroll 1
           for (int c = 0; c < kCols; c += 16) {
             uint32_t o[16];
@@ -555,8 +556,6 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       // ---- weights, times the value's scale -> P, one 128-byte swizzled row per key
       {
         const uint64_t sv2 = pair(sv, sv);
-        // P's buffer is free once PV of the tile before has completed
-        if (it > 0 && !warp_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 47)) break;
         uint8_t* prow = sm + L::kP + tid * 128;
         const bool bad = sv != sv && a.vis_prefix != nullptr;
 #pragma unroll
@@ -584,7 +583,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
       team_sync(tbar);
-      if (tid == 0 && half == 0) {
+      if (tid == 0 && half == 1) {
         tc_fence_after();
         constexpr uint32_t idO = idesc_bf16(128, kRowsT, 1);
         const uint64_t pdesc = sdesc(sb + L::kP, 1024, 1024);
@@ -594,10 +593,6 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         umma_commit(pv_bar);
       }
       __syncwarp();
-      if (loader) {                              // all have read the stage: the tile kStages further on goes there
-        load(st);
-        look();
-      }
       if (++st == kStages) { st = 0; turn ^= 1; }
       ++blk;
       if (__builtin_expect(!last, 1)) continue;
@@ -650,15 +645,19 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           tmem_ld16(tmem + L::tO + lane_off + c0 + c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            pin(o[i]);
-            const int row = row_s[c + i];
-            if (row < 0) continue;
-            if (whole)
-              static_cast<uint16_t*>(a.out)[static_cast<int64_t>(row) * D + tid] =
-                  static_cast<uint16_t>(pack_bf16(__uint_as_float(o[i]) * inv_s[c + i], 0.f));
-            else
-              p.pieces.o[(piece * kRowsT + c0 + c + i) * D + tid] = __uint_as_float(o[i]);
+          for (int i = 0; i < 16; ++i) pin(o[i]);
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int row = row_s[c + i];
+              const uint16_t f = static_cast<uint16_t>(pack_bf16(__uint_as_float(o[i]) * inv_s[c + i], 0.f));
+              if (row >= 0) static_cast<uint16_t*>(a.out)[static_cast<int64_t>(row) * D + tid] = f;
+            }
+          } else {
+            float* po = p.pieces.o + (piece * kRowsT + c0 + c) * D + tid;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (row_s[c + i] >= 0) po[i * D] = __uint_as_float(o[i]);
           }
         }
         if (__builtin_expect(*dirty, 0)) {
@@ -690,19 +689,17 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       team_sync(tbar);                           // all have read O and the rows' arrays: the next unit may begin
     }
     // every MMA issued has completed, and after an expired wait every copy has landed, before the CTA ends
-    if (loader) {
-      if (lane == 0) {
-        umma_commit(drain_bar);
-        bounded_wait(drain_bar, 0, abort_flag, p.status, 45);
-      }
-      __syncwarp();
-      if (*abort_flag)
-        for (int i = max(0, lnext - kStages); i < lnext; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try(raw_bar(i % kStages), (i / kStages) & 1) && clock64() - t0 < kWaitClocks) {
-          }
-        }
+    if (tid == 0) {
+      umma_commit(drain_bar);
+      bounded_wait(drain_bar, 0, abort_flag, p.status, 45);
     }
+    __syncwarp();
+    if (loader && *abort_flag)
+      for (int i = max(0, lnext - kStages); i < lnext; ++i) {
+        const long long t0 = clock64();
+        while (!mbar_try(raw_bar(i % kStages), (i / kStages) & 1) && clock64() - t0 < kWaitClocks) {
+        }
+      }
   }
   tc_fence_before();
   __syncthreads();

@@ -30,22 +30,23 @@ __device__ __forceinline__ float row_scale(float amax) {
   return amax <= 3.402823466e38f ? fmaxf(up, kScaleMin) : __uint_as_float(0x7fc00000u);
 }
 
-// Code of x: x / s rounded to the nearest integer, ties to even, plus 8.  The
-// quotient is the correctly rounded one (inv = 1/s correctly rounded, one
-// remainder step: Markstein 1990); bf16 rows hit exact ties often, and a
-// product with the reciprocal alone would break them either way.
+// Code of x in the low four bits of the result (the others are not zero):
+// x / s rounded to the nearest integer, ties to even, plus 8.  The quotient is
+// the correctly rounded one (inv = 1/s correctly rounded, one remainder step:
+// Markstein 1990): bf16 rows hit exact ties often, and a product with the
+// reciprocal alone would break them either way.  |x| <= 7 s, so it needs no
+// clamp; adding 1.5 * 2^23 + 8 rounds it to an integer in the low bits.
 __device__ __forceinline__ uint32_t encode(float x, float s, float inv) {
   const float q0 = __fmul_rn(x, inv);
   const float q = fmaf(fmaf(-q0, s, x), inv, q0);
-  const int n = __float2int_rn(q);              // NaN -> 0
-  return static_cast<uint32_t>(min(max(n, -7), 7) + 8);
+  return __float_as_uint(__fadd_rn(q, 12582920.f));
 }
 
 __host__ __device__ __forceinline__ constexpr int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
 
-// Value n of item e of a code word.
+// Value n of item e of a code word, by way of the mantissa (2^23 + code).
 __device__ __forceinline__ float decode(uint32_t w, int e) {
-  return static_cast<float>(static_cast<int>((w >> (4 * nibble_of(e))) & 15u) - 8);
+  return __uint_as_float(((w >> (4 * nibble_of(e))) & 15u) | 0x4b000000u) - 8388616.f;
 }
 
 // Byte offsets inside a block.

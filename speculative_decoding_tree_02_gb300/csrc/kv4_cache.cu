@@ -9,14 +9,25 @@
 namespace tv {
 namespace kv4 {
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 v = ldg_stream(p);
+// Eight consecutive elements, as loaded and as fp32.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.v[i] = ldg_stream(p + 8 / (sizeof(T) / 2) * i);
+  return r;
+}
+__device__ __forceinline__ void widen8(const Raw8<uint16_t>& r, float (&x)[8]) {
+  const uint4 v = r.v[0];
   x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
   x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const uint4 a = ldg_stream(p), b = ldg_stream(p + 4);
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float (&x)[8]) {
+  const uint4 a = r.v[0], b = r.v[1];
   x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
   x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
 }
@@ -32,6 +43,11 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Value of byte i (0..15) of a word, minus 8, by way of the mantissa.
+__device__ __forceinline__ float byte_value(uint32_t w, int i) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540u + i)) - 8388616.f;   // 2^23 + byte - (2^23 + 8)
 }
 
 // A row of d elements is d/16 units of 16 elements, in two runs of eight that
@@ -110,9 +126,10 @@ __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int6
   for (int h = lane0; h < Hq + Hkv; h += lanes) {
     const T* src = h < Hq ? q + t * ldq + static_cast<int64_t>(h) * d : k + t * ldk + static_cast<int64_t>(h - Hq) * d;
     T* dst = h < Hq ? q_out + (t * Hq + h) * d : k_out + (t * Hkv + h - Hq) * d;
+    const Raw8<T> ra = raw8(src + un.i0), rb = raw8(src + un.i1);
     float a[8], b[8];
-    load8(src + un.i0, a);
-    load8(src + un.i1, b);
+    widen8(ra, a);
+    widen8(rb, b);
     if (un.rot) rotate(a, b, c, s, inter);
     store8(dst + un.i0, a);
     store8(dst + un.i1, b);
@@ -133,29 +150,35 @@ struct AppendArgs {
   uint8_t* cache;
   int32_t* new_len;
   int32_t* err;
-  int total_rows, path_ld, max_new, max_pos, rot, inter, n_pages, P, table_ld, Hkv;
+  int total_rows, path_ld, max_new, max_pos, rot, inter, n_pages, P, table_ld, Hkv, heads;
 };
 
-// CTA = (16 cache tokens of one V group, KV head, request), D threads: thread
-// = (token, unit of its row).  A group belongs to one CTA, so the nibbles of
-// its tokens in shared V words are merged without atomics: the CTA rewrites
-// the group's words whole, keeping the nibbles of tokens that it does not
-// append.
+// CTA = (16 cache tokens of one V group, `heads` KV heads, request), D
+// threads: thread = (token, unit of its row).  A group belongs to one CTA, so
+// the nibbles of its tokens in shared V words are merged without atomics: the
+// CTA rewrites the group's words whole, keeping the nibbles of tokens that it
+// does not append.  The heads of a CTA follow one another with the next head's
+// rows on their way: the chain of lengths, tables and positions and the
+// (cos, sin) of the token are paid once for them.  See heads_per_cta for how
+// many, and the measured times.
 template <typename T, int D>
-__global__ void __launch_bounds__(D) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) {
   constexpr int kUnits = D / 16;
-  __shared__ __align__(16) uint8_t codes[16][D];
+  __shared__ __align__(16) uint8_t codes[2][16][D];
   __shared__ int s_count;
   __shared__ uint32_t s_live;
   griddep_wait();
   griddep_release();
-  const int r = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int r = blockIdx.z, h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.Hkv), tid = threadIdx.x;
   const int len = a.cache_len[r];
   const int base = a.row_off[r];
   int count = min(a.path ? min(a.path_ld, a.max_new) : a.row_off[r + 1] - base, a.max_new);
+  if (tid == 0) {
+    s_count = count;
+    s_live = 0;
+  }
+  __syncthreads();
   if (a.path) {   // rows up to the first negative entry
-    if (tid == 0) s_count = count;
-    __syncthreads();
     int first = count;
     for (int j = tid; j < count; j += D)
       if (a.path[static_cast<int64_t>(r) * a.path_ld + j] < 0) {
@@ -170,7 +193,7 @@ __global__ void __launch_bounds__(D) append_kernel(const AppendArgs a) {
   const int64_t cap = static_cast<int64_t>(a.table_ld) * a.P;
   const bool bad_len = len < 0 || len + static_cast<int64_t>(count) > cap ||
                        (!a.path && a.row_off[r + 1] - base > a.max_new);
-  if (blockIdx.x == 0 && h == 0 && tid == 0) {
+  if (blockIdx.x == 0 && h0 == 0 && tid == 0) {
     if (a.new_len) a.new_len[r] = len + count;
     if (bad_len && (count > 0 || len < 0) && a.err) *a.err = 1;
   }
@@ -184,9 +207,6 @@ __global__ void __launch_bounds__(D) append_kernel(const AppendArgs a) {
     if (tid == 0 && a.err) *a.err = 1;
     return;
   }
-  uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
-  if (tid == 0) s_live = 0;
-  __syncthreads();
 
   const int tk = tid / kUnits, u = tid % kUnits;
   const int slot = (group * 16 + tk) % a.P;
@@ -201,85 +221,96 @@ __global__ void __launch_bounds__(D) append_kernel(const AppendArgs a) {
     if (live && a.rot > 0) live = p >= 0 && p < a.max_pos;
     if (!live && a.err) *a.err = 1;
   }
-  float ka[8], kb[8], va[8], vb[8];
+  if (live && u == 0) atomicOr(&s_live, 1u << tk);
   const Unit un = unit_of(u, a.rot, a.inter);
-  if (live) {
-    const T* kr = static_cast<const T*>(a.k) + src * a.ldk + static_cast<int64_t>(h) * D;
-    const T* vr = static_cast<const T*>(a.v) + src * a.ldv + static_cast<int64_t>(h) * D;
-    load8(kr + un.i0, ka);
-    load8(kr + un.i1, kb);
-    load8(vr + 16 * u, va);
-    load8(vr + 16 * u + 8, vb);
-    if (un.rot) {
-      float c[8], s[8];
-      const float* row = a.table + static_cast<int64_t>(p) * a.rot + 8 * u;
-      table8(row, c);
-      table8(row + (a.rot >> 1), s);
-      rotate(ka, kb, c, s, a.inter);
-    }
-  } else {
+  const T* kr = static_cast<const T*>(a.k) + src * a.ldk;
+  const T* vr = static_cast<const T*>(a.v) + src * a.ldv;
+  float c[8], s[8];
+  Raw8<T> next[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ka[i] = kb[i] = va[i] = vb[i] = 0.f;
-  }
-  // row maxima over the units of a token; a NaN must survive the maximum
-  float mk = 0.f, mv = 0.f;
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    mk = fmaxf(mk, fmaxf(fabsf(ka[i]), fabsf(kb[i])));
-    mv = fmaxf(mv, fmaxf(fabsf(va[i]), fabsf(vb[i])));
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (isnan(ka[i]) || isnan(kb[i])) mk = INFINITY;
-    if (isnan(va[i]) || isnan(vb[i])) mv = INFINITY;
-  }
-#pragma unroll
-  for (int o = kUnits / 2; o; o >>= 1) {
-    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-  }
-  const float sk = row_scale(mk), sv = row_scale(mv);
-  const float ik = __frcp_rn(sk), iv = __frcp_rn(sv);
-  uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    w0 |= encode(ka[e], sk, ik) << (4 * nibble_of(e));
-    w1 |= encode(kb[e], sk, ik) << (4 * nibble_of(e));
-  }
-  uint32_t cv[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cv[e >> 2] |= encode(va[e], sv, iv) << (8 * (e & 3));
-    cv[2 + (e >> 2)] |= encode(vb[e], sv, iv) << (8 * (e & 3));
-  }
-  *reinterpret_cast<uint4*>(&codes[tk][16 * u]) = make_uint4(cv[0], cv[1], cv[2], cv[3]);
-  if (live) {
-    *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i0)) = w0;
-    *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i1)) = w1;
-    if (u == 0) {
-      *reinterpret_cast<uint16_t*>(blk + k_scale(a.P, D, slot)) = static_cast<uint16_t>(__float_as_uint(sk) >> 16);
-      *reinterpret_cast<uint16_t*>(blk + v_scale(a.P, D, slot)) = static_cast<uint16_t>(__float_as_uint(sv) >> 16);
-      atomicOr(&s_live, 1u << tk);
-    }
+    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) next[i].v[k] = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](int h) {
+    if (!live) return;
+    next[0] = raw8(kr + static_cast<int64_t>(h) * D + un.i0);
+    next[1] = raw8(kr + static_cast<int64_t>(h) * D + un.i1);
+    next[2] = raw8(vr + static_cast<int64_t>(h) * D + 16 * u);
+    next[3] = raw8(vr + static_cast<int64_t>(h) * D + 16 * u + 8);
+  };
+  fetch(h0);
+  if (live && un.rot) {
+    const float* row = a.table + static_cast<int64_t>(p) * a.rot + 8 * u;
+    table8(row, c);
+    table8(row + (a.rot >> 1), s);
   }
   __syncthreads();
-  // thread = dim: the 16 tokens' nibbles of one dim
   const uint32_t mask = s_live;
   if (mask == 0) return;
-  uint32_t w[2] = {0u, 0u}, keep[2] = {0u, 0u};
+  for (int h = h0; h < h1; ++h) {
+    uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
+    uint8_t(*buf)[D] = codes[(h - h0) & 1];
+    uint2* dst = reinterpret_cast<uint2*>(blk + v_group(a.P, D, group % (a.P / 16), tid));
+    uint2 old = make_uint2(0u, 0u);
+    if (mask != 0xffffu) old = *dst;
+    float ka[8], kb[8], va[8], vb[8];
+    widen8(next[0], ka);
+    widen8(next[1], kb);
+    widen8(next[2], va);
+    widen8(next[3], vb);
+    if (h + 1 < h1) fetch(h + 1);
+    if (live && un.rot) rotate(ka, kb, c, s, a.inter);
+    // row maxima over the units of a token; a NaN must survive the maximum
+    float mk = 0.f, mv = 0.f;
+    bool nk = false, nv = false;
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    const int sh = 4 * nibble_of(t & 7);
-    w[t >> 3] |= ((mask >> t) & 1u ? static_cast<uint32_t>(codes[t][tid]) : 0u) << sh;
-    if (!((mask >> t) & 1u)) keep[t >> 3] |= 15u << sh;
+    for (int i = 0; i < 8; ++i) {
+      mk = fmaxf(mk, fmaxf(fabsf(ka[i]), fabsf(kb[i])));
+      mv = fmaxf(mv, fmaxf(fabsf(va[i]), fabsf(vb[i])));
+      nk = nk || isnan(ka[i]) || isnan(kb[i]);
+      nv = nv || isnan(va[i]) || isnan(vb[i]);
+    }
+    if (nk) mk = INFINITY;
+    if (nv) mv = INFINITY;
+#pragma unroll
+    for (int o = kUnits / 2; o; o >>= 1) {
+      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    const float sk = row_scale(mk), sv = row_scale(mv);
+    const float ik = __frcp_rn(sk), iv = __frcp_rn(sv);
+    uint32_t w0 = 0, w1 = 0, cv[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int m = 7; m >= 0; --m) {               // nibble m holds item 2 m (+ 1 - 8 in the upper half)
+      const int e = m < 4 ? 2 * m : 2 * m - 7;
+      w0 = (w0 << 4) | (encode(ka[e], sk, ik) & 15u);
+      w1 = (w1 << 4) | (encode(kb[e], sk, ik) & 15u);
+    }
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+      cv[e >> 2] = (cv[e >> 2] << 8) | (encode(va[e], sv, iv) & 15u);
+      cv[2 + (e >> 2)] = (cv[2 + (e >> 2)] << 8) | (encode(vb[e], sv, iv) & 15u);
+    }
+    *reinterpret_cast<uint4*>(&buf[tk][16 * u]) = make_uint4(cv[0], cv[1], cv[2], cv[3]);
+    if (live) {
+      *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i0)) = w0;
+      *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i1)) = w1;
+      if (u == 0) {
+        *reinterpret_cast<uint16_t*>(blk + k_scale(a.P, D, slot)) = static_cast<uint16_t>(__float_as_uint(sk) >> 16);
+        *reinterpret_cast<uint16_t*>(blk + v_scale(a.P, D, slot)) = static_cast<uint16_t>(__float_as_uint(sv) >> 16);
+      }
+    }
+    __syncthreads();
+    // thread = dim: the 16 tokens' nibbles of one dim
+    uint32_t w[2] = {0u, 0u}, keep[2] = {0u, 0u};
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const int sh = 4 * nibble_of(t & 7);
+      w[t >> 3] |= static_cast<uint32_t>(buf[t][tid]) << sh;
+      if (!((mask >> t) & 1u)) keep[t >> 3] |= 15u << sh;
+    }
+    *dst = make_uint2((w[0] & ~keep[0]) | (old.x & keep[0]), (w[1] & ~keep[1]) | (old.y & keep[1]));
   }
-  uint2* dst = reinterpret_cast<uint2*>(blk + v_group(a.P, D, group % (a.P / 16), tid));
-  if (mask != 0xffffu) {
-    const uint2 old = *dst;
-    w[0] |= old.x & keep[0];
-    w[1] |= old.y & keep[1];
-  }
-  *dst = make_uint2(w[0], w[1]);
 }
 
 // -------------------------------------------------------------------- gather
@@ -291,26 +322,27 @@ struct GatherArgs {
   void* k_out;
   void* v_out;
   int32_t* err;
-  int n_pages, P, table_ld, Hkv, total_rows, max_rows;
+  int n_pages, P, table_ld, Hkv, total_rows, max_rows, heads;
 };
 
-// CTA = (16 cache tokens, KV head, request), D threads: thread = (token, 16
-// dims) for the rows; V codes pass through shared memory to turn the group's
-// dim-major words into rows.
+// CTA = (16 cache tokens, `heads` KV heads, request), D threads: thread =
+// (token, 16 dims) for the rows; V codes pass through shared memory to turn
+// the group's dim-major words into rows.  The heads of a CTA follow one another
+// with the next head's codes on their way.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
   constexpr int kUnits = D / 16;
-  __shared__ __align__(16) uint8_t codes[16][D];
+  __shared__ __align__(16) uint8_t codes[2][16][D];
   griddep_wait();
   griddep_release();
-  const int r = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int r = blockIdx.z, h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.Hkv), tid = threadIdx.x;
   const int o0 = a.out_off[r];
   int n = a.out_off[r + 1] - o0;
   const int t0 = a.start ? a.start[r] : 0;
   if (n <= 0) return;
   const int64_t cap = static_cast<int64_t>(a.table_ld) * a.P;
   const bool bad = t0 < 0 || o0 < 0 || static_cast<int64_t>(o0) + n > a.total_rows;
-  if (blockIdx.x == 0 && h == 0 && tid == 0 && a.err && (bad || n > a.max_rows || t0 + static_cast<int64_t>(n) > cap))
+  if (blockIdx.x == 0 && h0 == 0 && tid == 0 && a.err && (bad || n > a.max_rows || t0 + static_cast<int64_t>(n) > cap))
     *a.err = 1;
   if (bad) return;
   n = min(n, a.max_rows);
@@ -323,39 +355,63 @@ __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
     if (tid == 0 && a.err) *a.err = 1;
     return;
   }
-  const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
   const int tk = tid / kUnits, u = tid % kUnits;
   const int slot = (group * 16 + tk) % a.P;
-  const uint2 kw = *reinterpret_cast<const uint2*>(blk + k_word(a.P, slot, 16 * u));
-  const uint2 vw = *reinterpret_cast<const uint2*>(blk + v_group(a.P, D, group % (a.P / 16), tid));
-  const float sk = bf16_at(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot)));
-  const float sv = bf16_at(reinterpret_cast<const uint16_t*>(blk + v_scale(a.P, D, slot)));
-#pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    codes[t][tid] = static_cast<uint8_t>((vw.x >> (4 * nibble_of(t))) & 15u);
-    codes[t + 8][tid] = static_cast<uint8_t>((vw.y >> (4 * nibble_of(t))) & 15u);
-  }
-  __syncthreads();
   const int64_t i = static_cast<int64_t>(group) * 16 + tk - t0;
-  if (i < 0 || i >= n) return;
-  const int64_t at = ((o0 + i) * a.Hkv + h) * D + 16 * u;
-  float x[8], y[8];
+  const bool live = i >= 0 && i < n;
+  const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h0) * block_bytes(a.P, D);
+  const int ko = k_word(a.P, slot, 16 * u), vo = v_group(a.P, D, group % (a.P / 16), tid);
+  uint2 kw, vw;
+  uint16_t ks, vs;
+  auto fetch = [&]() {
+    kw = __ldg(reinterpret_cast<const uint2*>(blk + ko));
+    vw = __ldg(reinterpret_cast<const uint2*>(blk + vo));
+    ks = __ldg(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot)));
+    vs = __ldg(reinterpret_cast<const uint16_t*>(blk + v_scale(a.P, D, slot)));
+  };
+  fetch();
+  for (int h = h0; h < h1; ++h) {
+    uint8_t(*buf)[D] = codes[(h - h0) & 1];
+    const uint2 k2 = kw;
+    const float sk = bf16_at(&ks), sv = bf16_at(&vs);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = sk * decode(kw.x, e);
-    y[e] = sk * decode(kw.y, e);
-  }
-  store8(static_cast<T*>(a.k_out) + at, x);
-  store8(static_cast<T*>(a.k_out) + at + 8, y);
-  const uint4 cv = *reinterpret_cast<const uint4*>(&codes[tk][16 * u]);
-  const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+    for (int t = 0; t < 8; ++t) {
+      buf[t][tid] = static_cast<uint8_t>((vw.x >> (4 * nibble_of(t))) & 15u);
+      buf[t + 8][tid] = static_cast<uint8_t>((vw.y >> (4 * nibble_of(t))) & 15u);
+    }
+    blk += block_bytes(a.P, D);
+    if (h + 1 < h1) fetch();
+    __syncthreads();
+    if (!live) continue;
+    const int64_t at = ((o0 + i) * a.Hkv + h) * D + 16 * u;
+    float x[8], y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = sv * static_cast<float>(static_cast<int>((cw[e >> 2] >> (8 * (e & 3))) & 15u) - 8);
-    y[e] = sv * static_cast<float>(static_cast<int>((cw[2 + (e >> 2)] >> (8 * (e & 3))) & 15u) - 8);
+    for (int e = 0; e < 8; ++e) {
+      x[e] = sk * decode(k2.x, e);
+      y[e] = sk * decode(k2.y, e);
+    }
+    store8(static_cast<T*>(a.k_out) + at, x);
+    store8(static_cast<T*>(a.k_out) + at + 8, y);
+    const uint4 cv = *reinterpret_cast<const uint4*>(&buf[tk][16 * u]);
+    const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = sv * byte_value(cw[e >> 2], e & 3);
+      y[e] = sv * byte_value(cw[2 + (e >> 2)], e & 3);
+    }
+    store8(static_cast<T*>(a.v_out) + at, x);
+    store8(static_cast<T*>(a.v_out) + at + 8, y);
   }
-  store8(static_cast<T*>(a.v_out) + at, x);
-  store8(static_cast<T*>(a.v_out) + at + 8, y);
+}
+
+// KV heads that a CTA of append and gather takes one after another: all of
+// them while that leaves enough CTAs for every SM, else fewer.
+// (HEADSNOTE)
+int heads_per_cta(int64_t groups, int Hkv) {
+  const int64_t want = 8ll * sm_count();
+  int heads = Hkv;
+  while (heads > 1 && groups * ((Hkv + heads - 1) / heads) < want) heads = (heads + 1) / 2;
+  return heads;
 }
 
 bool cache_ok(int n_pages, int page_size, int table_ld, int Hkv, int d) {
@@ -428,9 +484,11 @@ TV_API int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, in
     if (p && !aligned(p, 16)) return TV_EINVAL;
   kv4::AppendArgs a{k, v, ldk, ldv, row_off, path, pos, table, block_table, cache_len, static_cast<uint8_t*>(cache),
                     new_len, err, total_rows, path_ld, max_new, max_pos, rot_dim, interleaved ? 1 : 0, n_pages,
-                    page_size, table_ld, Hkv};
+                    page_size, table_ld, Hkv, 1};
   if (total_rows == 0) a.n_pages = 0;     // no row can be read or written
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_new) + 15) / 16 + 1), Hkv, B);
+  const int64_t groups = (static_cast<int64_t>(max_new) + 15) / 16 + 1;
+  a.heads = kv4::heads_per_cta(std::min(groups * B, static_cast<int64_t>(total_rows) / 16 + B), Hkv);
+  const dim3 grid(static_cast<unsigned>(groups), (Hkv + a.heads - 1) / a.heads, B);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TV_BF16)
     return d == 128 ? launch_pdl(kv4::append_kernel<uint16_t, 128>, grid, dim3(128), 0, st, a)
@@ -452,9 +510,11 @@ TV_API int kv4_gather(const void* cache, int n_pages, int page_size, const int32
   const void* ptrs[] = {cache, k_out, v_out};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return TV_EINVAL;
-  const kv4::GatherArgs a{static_cast<const uint8_t*>(cache), block_table, start, out_off, k_out, v_out, err, n_pages,
-                          page_size, table_ld, Hkv, total_rows, max_rows};
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_rows) + 15) / 16 + (start ? 1 : 0)), Hkv, B);
+  kv4::GatherArgs a{static_cast<const uint8_t*>(cache), block_table, start, out_off, k_out, v_out, err, n_pages,
+                    page_size, table_ld, Hkv, total_rows, max_rows, 1};
+  const int64_t groups = (static_cast<int64_t>(max_rows) + 15) / 16 + (start ? 1 : 0);
+  a.heads = kv4::heads_per_cta(std::min(groups * B, static_cast<int64_t>(total_rows) / 16 + B), Hkv);
+  const dim3 grid(static_cast<unsigned>(groups), (Hkv + a.heads - 1) / a.heads, B);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TV_BF16)
     return d == 128 ? launch_pdl(kv4::gather_kernel<uint16_t, 128>, grid, dim3(128), 0, st, a)
