@@ -51,22 +51,19 @@ __device__ __forceinline__ float byte_value(uint32_t w, int i) {
 }
 
 // A row of d elements is d/16 units of 16 elements, in two runs of eight that
-// start at i0 and i1.  In the rotated part a unit holds the eight pairs
-// 8u .. 8u+7: (i, i + rot/2) or, interleaved, (2i, 2i + 1).
+// start at i0 and i1: run u of the first and of the second half of the rotated
+// part (or of what follows it), so that neighbouring threads touch neighbouring
+// 16 bytes.  In halves the two runs are the pairs' first and second elements,
+// interleaved each run is four pairs.
 struct Unit {
   int i0, i1;
   bool rot;
 };
-__device__ __forceinline__ Unit unit_of(int u, int rot, bool inter) {
+__device__ __forceinline__ Unit unit_of(int u, int d, int rot) {
   Unit r;
   r.rot = 16 * u < rot;
-  if (r.rot && !inter) {
-    r.i0 = 8 * u;
-    r.i1 = (rot >> 1) + 8 * u;
-  } else {
-    r.i0 = 16 * u;
-    r.i1 = 16 * u + 8;
-  }
+  r.i0 = r.rot ? 8 * u : rot + 8 * (u - (rot >> 4));
+  r.i1 = r.i0 + (r.rot ? rot : d - rot) / 2;
   return r;
 }
 // Rotates a unit in place.  Every product and sum is rounded by itself (no
@@ -92,9 +89,18 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
     }
   }
 }
-__device__ __forceinline__ void table8(const float* p, float (&x)[8]) {   // table rows are reused: cached loads
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// The (cos, sin) of unit u from a table row; rows are reused: cached loads.
+__device__ __forceinline__ void table_unit(const float* row, int u, int rot, bool inter, float (&c)[8], float (&s)[8]) {
+  const float* at = row + (inter ? 4 : 8) * u;
+  const int step = inter ? rot >> 2 : 4, half = rot >> 1;
+  const float4 v[4] = {__ldg(reinterpret_cast<const float4*>(at)), __ldg(reinterpret_cast<const float4*>(at + step)),
+                       __ldg(reinterpret_cast<const float4*>(at + half)),
+                       __ldg(reinterpret_cast<const float4*>(at + half + step))};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    c[4 * i] = v[i].x; c[4 * i + 1] = v[i].y; c[4 * i + 2] = v[i].z; c[4 * i + 3] = v[i].w;
+    s[4 * i] = v[2 + i].x; s[4 * i + 1] = v[2 + i].y; s[4 * i + 2] = v[2 + i].z; s[4 * i + 3] = v[2 + i].w;
+  }
 }
 
 // ------------------------------------------------------------------ rotation
@@ -116,13 +122,9 @@ __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int6
     if (threadIdx.x == 0 && err) *err = 1;
     return;
   }
-  const Unit un = unit_of(u, rot, inter);
+  const Unit un = unit_of(u, d, rot);
   float c[8], s[8];
-  if (un.rot) {
-    const float* row = table + static_cast<int64_t>(p) * rot + 8 * u;
-    table8(row, c);
-    table8(row + (rot >> 1), s);
-  }
+  if (un.rot) table_unit(table + static_cast<int64_t>(p) * rot, u, rot, inter, c, s);
   for (int h = lane0; h < Hq + Hkv; h += lanes) {
     const T* src = h < Hq ? q + t * ldq + static_cast<int64_t>(h) * d : k + t * ldk + static_cast<int64_t>(h - Hq) * d;
     T* dst = h < Hq ? q_out + (t * Hq + h) * d : k_out + (t * Hkv + h - Hq) * d;
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
     if (!live && a.err) *a.err = 1;
   }
   if (live && u == 0) atomicOr(&s_live, 1u << tk);
-  const Unit un = unit_of(u, a.rot, a.inter);
+  const Unit un = unit_of(u, D, a.rot);
   const T* kr = static_cast<const T*>(a.k) + src * a.ldk;
   const T* vr = static_cast<const T*>(a.v) + src * a.ldv;
   float c[8], s[8];
@@ -235,15 +237,11 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
     if (!live) return;
     next[0] = raw8(kr + static_cast<int64_t>(h) * D + un.i0);
     next[1] = raw8(kr + static_cast<int64_t>(h) * D + un.i1);
-    next[2] = raw8(vr + static_cast<int64_t>(h) * D + 16 * u);
-    next[3] = raw8(vr + static_cast<int64_t>(h) * D + 16 * u + 8);
+    next[2] = raw8(vr + static_cast<int64_t>(h) * D + 8 * u);
+    next[3] = raw8(vr + static_cast<int64_t>(h) * D + D / 2 + 8 * u);
   };
   fetch(h0);
-  if (live && un.rot) {
-    const float* row = a.table + static_cast<int64_t>(p) * a.rot + 8 * u;
-    table8(row, c);
-    table8(row + (a.rot >> 1), s);
-  }
+  if (live && un.rot) table_unit(a.table + static_cast<int64_t>(p) * a.rot, u, a.rot, a.inter, c, s);
   __syncthreads();
   const uint32_t mask = s_live;
   if (mask == 0) return;
@@ -291,7 +289,8 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
       cv[e >> 2] = (cv[e >> 2] << 8) | (encode(va[e], sv, iv) & 15u);
       cv[2 + (e >> 2)] = (cv[2 + (e >> 2)] << 8) | (encode(vb[e], sv, iv) & 15u);
     }
-    *reinterpret_cast<uint4*>(&buf[tk][16 * u]) = make_uint4(cv[0], cv[1], cv[2], cv[3]);
+    *reinterpret_cast<uint2*>(&buf[tk][8 * u]) = make_uint2(cv[0], cv[1]);
+    *reinterpret_cast<uint2*>(&buf[tk][D / 2 + 8 * u]) = make_uint2(cv[2], cv[3]);
     if (live) {
       *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i0)) = w0;
       *reinterpret_cast<uint32_t*>(blk + k_word(a.P, slot, un.i1)) = w1;
@@ -326,12 +325,13 @@ struct GatherArgs {
 };
 
 // CTA = (16 cache tokens, `heads` KV heads, request), D threads: thread =
-// (token, 16 dims) for the rows; V codes pass through shared memory to turn
+// (tokens tk and tk + 8, 8 dims) for the rows, so that a warp's store is whole
+// rows; V codes pass through shared memory to turn
 // the group's dim-major words into rows.  The heads of a CTA follow one another
 // with the next head's codes on their way.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
-  constexpr int kUnits = D / 16;
+  constexpr int kUnits = D / 8;
   __shared__ __align__(16) uint8_t codes[2][16][D];
   griddep_wait();
   griddep_release();
@@ -356,24 +356,27 @@ __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
     return;
   }
   const int tk = tid / kUnits, u = tid % kUnits;
-  const int slot = (group * 16 + tk) % a.P;
-  const int64_t i = static_cast<int64_t>(group) * 16 + tk - t0;
-  const bool live = i >= 0 && i < n;
+  const int slot = (group * 16) % a.P + tk;
+  const int64_t i0 = static_cast<int64_t>(group) * 16 + tk - t0;
   const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h0) * block_bytes(a.P, D);
-  const int ko = k_word(a.P, slot, 16 * u), vo = v_group(a.P, D, group % (a.P / 16), tid);
-  uint2 kw, vw;
-  uint16_t ks, vs;
+  const int ko = k_word(a.P, slot, 8 * u), vo = v_group(a.P, D, group % (a.P / 16), tid);
+  uint32_t kw[2];
+  uint2 vw;
+  uint16_t ks[2], vs[2];
   auto fetch = [&]() {
-    kw = __ldg(reinterpret_cast<const uint2*>(blk + ko));
     vw = __ldg(reinterpret_cast<const uint2*>(blk + vo));
-    ks = __ldg(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot)));
-    vs = __ldg(reinterpret_cast<const uint16_t*>(blk + v_scale(a.P, D, slot)));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      kw[t] = __ldg(reinterpret_cast<const uint32_t*>(blk + ko + 128 * t));
+      ks[t] = __ldg(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot + 8 * t)));
+      vs[t] = __ldg(reinterpret_cast<const uint16_t*>(blk + v_scale(a.P, D, slot + 8 * t)));
+    }
   };
   fetch();
   for (int h = h0; h < h1; ++h) {
     uint8_t(*buf)[D] = codes[(h - h0) & 1];
-    const uint2 k2 = kw;
-    const float sk = bf16_at(&ks), sv = bf16_at(&vs);
+    const uint32_t k2[2] = {kw[0], kw[1]};
+    const float sk[2] = {bf16_at(&ks[0]), bf16_at(&ks[1])}, sv[2] = {bf16_at(&vs[0]), bf16_at(&vs[1])};
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       buf[t][tid] = static_cast<uint8_t>((vw.x >> (4 * nibble_of(t))) & 15u);
@@ -382,25 +385,20 @@ __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
     blk += block_bytes(a.P, D);
     if (h + 1 < h1) fetch();
     __syncthreads();
-    if (!live) continue;
-    const int64_t at = ((o0 + i) * a.Hkv + h) * D + 16 * u;
-    float x[8], y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = sk * decode(k2.x, e);
-      y[e] = sk * decode(k2.y, e);
-    }
-    store8(static_cast<T*>(a.k_out) + at, x);
-    store8(static_cast<T*>(a.k_out) + at + 8, y);
-    const uint4 cv = *reinterpret_cast<const uint4*>(&buf[tk][16 * u]);
-    const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+    for (int t = 0; t < 2; ++t) {
+      const int64_t i = i0 + 8 * t;
+      if (i < 0 || i >= n) continue;
+      const int64_t at = ((o0 + i) * a.Hkv + h) * D + 8 * u;
+      float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = sv * byte_value(cw[e >> 2], e & 3);
-      y[e] = sv * byte_value(cw[2 + (e >> 2)], e & 3);
+      for (int e = 0; e < 8; ++e) x[e] = sk[t] * decode(k2[t], e);
+      store8(static_cast<T*>(a.k_out) + at, x);
+      const uint2 cv = *reinterpret_cast<const uint2*>(&buf[tk + 8 * t][8 * u]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = sv[t] * byte_value(e < 4 ? cv.x : cv.y, e & 3);
+      store8(static_cast<T*>(a.v_out) + at, x);
     }
-    store8(static_cast<T*>(a.v_out) + at, x);
-    store8(static_cast<T*>(a.v_out) + at + 8, y);
   }
 }
 
