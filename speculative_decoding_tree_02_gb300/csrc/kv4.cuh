@@ -23,11 +23,34 @@ namespace kv4 {
 constexpr float kScaleMin = 7.888609052210118e-31f;   // 2^-100: keeps 1/s finite
 
 // Scale of a row: max|x| / 7 rounded up to bf16, at least 2^-100; NaN for a
-// row with a non-finite entry, so that the whole row reads back as NaN.
+// row with a non-finite entry (amax NaN or infinite), so that the whole row
+// reads back as NaN.  The quotient is correctly rounded: 1/7 correctly rounded
+// and one remainder step (Markstein 1990).
 __device__ __forceinline__ float row_scale(float amax) {
-  const float a = __fdiv_rn(amax, 7.f);
+  const float q0 = __fmul_rn(amax, 1.f / 7.f);
+  const float a = fmaf(fmaf(-q0, 7.f, amax), 1.f / 7.f, q0);
   const float up = __uint_as_float((__float_as_uint(a) + 0xffffu) & 0xffff0000u);
   return amax <= 3.402823466e38f ? fmaxf(up, kScaleMin) : __uint_as_float(0x7fc00000u);
+}
+// 1/s correctly rounded, s a row's scale: one Newton step on the hardware's
+// approximation.  For each of the 128 significands of a bf16 number the step
+// gives the correctly rounded reciprocal from anything within 4 units in the
+// last place of it (enumerated), and 2^-100 <= s < 2^126 keeps both normal.
+__device__ __forceinline__ float row_inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(r, fmaf(-s, r, 1.f), r);
+}
+// max(m, |x|, |y|); a NaN stays.
+__device__ __forceinline__ float max_abs(float m, float x, float y) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(x)), "f"(fabsf(y)));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+  return d;
 }
 
 // Code of x in the low four bits of the result (the others are not zero):

@@ -68,9 +68,9 @@ __device__ __forceinline__ Unit unit_of(int u, int d, int rot) {
 }
 // Rotates a unit in place.  Every product and sum is rounded by itself (no
 // fused multiply-add), so the result is the same wherever it is computed.
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8],
-                                       bool inter) {
-  if (inter) {
+template <bool kInter>
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8]) {
+  if constexpr (kInter) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float x = a[2 * j], y = a[2 * j + 1];
@@ -90,9 +90,10 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
   }
 }
 // The (cos, sin) of unit u from a table row; rows are reused: cached loads.
-__device__ __forceinline__ void table_unit(const float* row, int u, int rot, bool inter, float (&c)[8], float (&s)[8]) {
-  const float* at = row + (inter ? 4 : 8) * u;
-  const int step = inter ? rot >> 2 : 4, half = rot >> 1;
+template <bool kInter>
+__device__ __forceinline__ void table_unit(const float* row, int u, int rot, float (&c)[8], float (&s)[8]) {
+  const float* at = row + (kInter ? 4 : 8) * u;
+  const int step = kInter ? rot >> 2 : 4, half = rot >> 1;
   const float4 v[4] = {__ldg(reinterpret_cast<const float4*>(at)), __ldg(reinterpret_cast<const float4*>(at + step)),
                        __ldg(reinterpret_cast<const float4*>(at + half)),
                        __ldg(reinterpret_cast<const float4*>(at + half + step))};
@@ -106,11 +107,11 @@ __device__ __forceinline__ void table_unit(const float* row, int u, int rot, boo
 // ------------------------------------------------------------------ rotation
 // CTA = one token; thread = (unit of the row, head lane), so a thread reads
 // its eight (cos, sin) once for all of its heads.
-template <typename T>
+template <typename T, bool kInter>
 __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int64_t ldq, const T* __restrict__ k,
                                                    int64_t ldk, int Hq, int Hkv, int d,
                                                    const int32_t* __restrict__ pos, const float* __restrict__ table,
-                                                   int max_pos, int rot, int inter, T* __restrict__ q_out,
+                                                   int max_pos, int rot, T* __restrict__ q_out,
                                                    T* __restrict__ k_out, int32_t* err) {
   griddep_wait();
   griddep_release();
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int6
   }
   const Unit un = unit_of(u, d, rot);
   float c[8], s[8];
-  if (un.rot) table_unit(table + static_cast<int64_t>(p) * rot, u, rot, inter, c, s);
+  if (un.rot) table_unit<kInter>(table + static_cast<int64_t>(p) * rot, u, rot, c, s);
   for (int h = lane0; h < Hq + Hkv; h += lanes) {
     const T* src = h < Hq ? q + t * ldq + static_cast<int64_t>(h) * d : k + t * ldk + static_cast<int64_t>(h - Hq) * d;
     T* dst = h < Hq ? q_out + (t * Hq + h) * d : k_out + (t * Hkv + h - Hq) * d;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int6
     float a[8], b[8];
     widen8(ra, a);
     widen8(rb, b);
-    if (un.rot) rotate(a, b, c, s, inter);
+    if (un.rot) rotate<kInter>(a, b, c, s);
     store8(dst + un.i0, a);
     store8(dst + un.i1, b);
   }
@@ -152,7 +153,7 @@ struct AppendArgs {
   uint8_t* cache;
   int32_t* new_len;
   int32_t* err;
-  int total_rows, path_ld, max_new, max_pos, rot, inter, n_pages, P, table_ld, Hkv, heads;
+  int total_rows, path_ld, max_new, max_pos, rot, n_pages, P, table_ld, Hkv, heads;
 };
 
 // CTA = (16 cache tokens of one V group, `heads` KV heads, request), D
@@ -163,7 +164,7 @@ struct AppendArgs {
 // rows on their way: the chain of lengths, tables and positions and the
 // (cos, sin) of the token are paid once for them.  See heads_per_cta for how
 // many, and the measured times.
-template <typename T, int D>
+template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) {
   constexpr int kUnits = D / 16;
   __shared__ __align__(16) uint8_t codes[2][16][D];
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
     next[3] = raw8(vr + static_cast<int64_t>(h) * D + D / 2 + 8 * u);
   };
   fetch(h0);
-  if (live && un.rot) table_unit(a.table + static_cast<int64_t>(p) * a.rot, u, a.rot, a.inter, c, s);
+  if (live && un.rot) table_unit<kInter>(a.table + static_cast<int64_t>(p) * a.rot, u, a.rot, c, s);
   __syncthreads();
   const uint32_t mask = s_live;
   if (mask == 0) return;
@@ -257,26 +258,21 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
     widen8(next[2], va);
     widen8(next[3], vb);
     if (h + 1 < h1) fetch(h + 1);
-    if (live && un.rot) rotate(ka, kb, c, s, a.inter);
-    // row maxima over the units of a token; a NaN must survive the maximum
+    if (live && un.rot) rotate<kInter>(ka, kb, c, s);
+    // row maxima over the units of a token
     float mk = 0.f, mv = 0.f;
-    bool nk = false, nv = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      mk = fmaxf(mk, fmaxf(fabsf(ka[i]), fabsf(kb[i])));
-      mv = fmaxf(mv, fmaxf(fabsf(va[i]), fabsf(vb[i])));
-      nk = nk || isnan(ka[i]) || isnan(kb[i]);
-      nv = nv || isnan(va[i]) || isnan(vb[i]);
+      mk = max_abs(mk, ka[i], kb[i]);
+      mv = max_abs(mv, va[i], vb[i]);
     }
-    if (nk) mk = INFINITY;
-    if (nv) mv = INFINITY;
 #pragma unroll
     for (int o = kUnits / 2; o; o >>= 1) {
-      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+      mk = max_nan(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+      mv = max_nan(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
     const float sk = row_scale(mk), sv = row_scale(mv);
-    const float ik = __frcp_rn(sk), iv = __frcp_rn(sv);
+    const float ik = row_inverse(sk), iv = row_inverse(sv);
     uint32_t w0 = 0, w1 = 0, cv[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int m = 7; m >= 0; --m) {               // nibble m holds item 2 m (+ 1 - 8 in the upper half)
@@ -449,13 +445,15 @@ TV_API int tv_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int d
   const int iters = (H + lanes - 1) / lanes;
   lanes = (H + iters - 1) / iters;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto tag) {
+  auto go = [&](auto tag, auto kernel) {
     using T = decltype(tag);
-    return launch_pdl(kv4::rope_kernel<T>, dim3(n), dim3(units * lanes), 0, st, static_cast<const T*>(q), ldq,
-                      static_cast<const T*>(k), ldk, Hq, Hkv, d, pos, table, max_pos, rot_dim, interleaved ? 1 : 0,
-                      static_cast<T*>(q_out), static_cast<T*>(k_out), err);
+    return launch_pdl(kernel, dim3(n), dim3(units * lanes), 0, st, static_cast<const T*>(q), ldq,
+                      static_cast<const T*>(k), ldk, Hq, Hkv, d, pos, table, max_pos, rot_dim, static_cast<T*>(q_out),
+                      static_cast<T*>(k_out), err);
   };
-  return dtype == TV_BF16 ? go(uint16_t{}) : go(float{});
+  if (dtype == TV_BF16)
+    return interleaved ? go(uint16_t{}, kv4::rope_kernel<uint16_t, true>) : go(uint16_t{}, kv4::rope_kernel<uint16_t, false>);
+  return interleaved ? go(float{}, kv4::rope_kernel<float, true>) : go(float{}, kv4::rope_kernel<float, false>);
 }
 
 TV_API int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype, int total_rows,
@@ -481,18 +479,21 @@ TV_API int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, in
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return TV_EINVAL;
   kv4::AppendArgs a{k, v, ldk, ldv, row_off, path, pos, table, block_table, cache_len, static_cast<uint8_t*>(cache),
-                    new_len, err, total_rows, path_ld, max_new, max_pos, rot_dim, interleaved ? 1 : 0, n_pages,
+                    new_len, err, total_rows, path_ld, max_new, max_pos, rot_dim, n_pages,
                     page_size, table_ld, Hkv, 1};
   if (total_rows == 0) a.n_pages = 0;     // no row can be read or written
   const int64_t groups = (static_cast<int64_t>(max_new) + 15) / 16 + 1;
   a.heads = kv4::heads_per_cta(std::min(groups * B, static_cast<int64_t>(total_rows) / 16 + B), Hkv);
   const dim3 grid(static_cast<unsigned>(groups), (Hkv + a.heads - 1) / a.heads, B);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto k128, auto k64) {
+    return d == 128 ? launch_pdl(k128, grid, dim3(128), 0, st, a) : launch_pdl(k64, grid, dim3(64), 0, st, a);
+  };
   if (dtype == TV_BF16)
-    return d == 128 ? launch_pdl(kv4::append_kernel<uint16_t, 128>, grid, dim3(128), 0, st, a)
-                    : launch_pdl(kv4::append_kernel<uint16_t, 64>, grid, dim3(64), 0, st, a);
-  return d == 128 ? launch_pdl(kv4::append_kernel<float, 128>, grid, dim3(128), 0, st, a)
-                  : launch_pdl(kv4::append_kernel<float, 64>, grid, dim3(64), 0, st, a);
+    return interleaved ? go(kv4::append_kernel<uint16_t, 128, true>, kv4::append_kernel<uint16_t, 64, true>)
+                       : go(kv4::append_kernel<uint16_t, 128, false>, kv4::append_kernel<uint16_t, 64, false>);
+  return interleaved ? go(kv4::append_kernel<float, 128, true>, kv4::append_kernel<float, 64, true>)
+                     : go(kv4::append_kernel<float, 128, false>, kv4::append_kernel<float, 64, false>);
 }
 
 TV_API int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
