@@ -42,7 +42,7 @@ TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, i
   const int64_t lds[] = {ldq, ldk, ldv};
   const int heads[] = {Hq, Hkv, Hkv};
   for (int i = 0; i < 3; ++i)
-    if (lds[i] < static_cast<int64_t>(heads[i]) * d || lds[i] % vec) return TV_EINVAL;
+    if (lds[i] < static_cast<int64_t>(heads[i]) * d || lds[i] % vec || lds[i] > 0x7fffffffll) return TV_EINVAL;
   const void* ptrs[] = {q, k_tree, v_tree, out, cache};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return TV_EINVAL;

@@ -237,8 +237,20 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       if (lblk < lx.np && lane < per_tile && key < lx.len)
         lpage = a.block_table[static_cast<int64_t>(lr) * a.table_ld + (key >> ps_shift)];
     };
+    // What the start of a unit and its tile of nodes read, on its way into L1 some tiles ahead.
+    auto announce = [&]() {
+      const Span sp = node_span(a, lr);
+      const int node0 = lt * p.nq, nodes = min(p.nq, sp.cnt - node0);
+      for (int i = lane; i < nodes * g; i += 32) {
+        const uint16_t* row = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(sp.n0 + node0 + i / g) * a.ldq +
+                              static_cast<int64_t>(lh * g + i % g) * D;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+        if (D == 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + 64));
+      }
+    };
     auto load = [&](int st) {
       if (lnext >= n) return;
+      if (lblk == 0 && lnext > 0) announce();
       const bool wanted = lblk < lx.np && lane < per_tile && lblk * kKeys + (lane << ps_shift) < lx.len;
       const bool ok = wanted && lpage >= 0 && lpage < a.n_pages;
       if (wanted && !ok && a.err) *a.err = 1;
@@ -360,29 +372,32 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           tmem_st16(tmem + L::tK + lane_off + half * (D / 4) + 16 * c, v);
         }
       } else {
-        if (tid < kCols) {                       // the rows' masks over the tile's nodes
-          const int row = row_s[tid];
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int word = (key0 >> 6) + w;
-            const uint64_t v =
-                row >= 0 && word < a.anc_words ? a.anc[static_cast<int64_t>(row / a.Hq) * a.anc_words + word] : 0ull;
-            anc_s[(2 * w) * kRowsT + tid] = static_cast<uint32_t>(v);
-            anc_s[(2 * w + 1) * kRowsT + tid] = static_cast<uint32_t>(v >> 32);
-          }
-        }
         const uint16_t* row = static_cast<const uint16_t*>(a.k_tree) +
                               static_cast<int64_t>(n0 + key0 + min(tid, nkeys - 1)) * a.ldk + static_cast<int64_t>(h) * D +
                               half * (D / 2);   // (places without nodes: the last one, masked below)
+        uint32_t v[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + 8 * i);
+          v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
+        }
+        if (tid < kCols) {                       // the rows' masks over the tile's nodes
+          const int at = row_s[tid];
+          uint64_t m[2];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int word = (key0 >> 6) + w;
+            m[w] = at >= 0 && word < a.anc_words ? a.anc[static_cast<int64_t>(at / a.Hq) * a.anc_words + word] : 0ull;
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) anc_s[w * kRowsT + tid] = static_cast<uint32_t>(m[w >> 1] >> (32 * (w & 1)));
+        }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          uint32_t v[16];
+          uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(row + 32 * c + 8 * i);
-            v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
-          }
-          tmem_st16(tmem + L::tK + lane_off + half * (D / 4) + 16 * c, v);
+          for (int i = 0; i < 16; ++i) u[i] = v[16 * c + i];
+          tmem_st16(tmem + L::tK + lane_off + half * (D / 4) + 16 * c, u);
         }
       }
       tmem_st_wait();
@@ -420,8 +435,10 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           // a value that is not finite must not meet the zero weights of rows that do not see it: it is taken
           // out here and added at the end to the rows that see it
           bool bad = false;
+          // lanes 2j, 2j + 1 read dims 2j, 2j + 1 of an even and of the next token and swap a half
           const uint16_t* rows = static_cast<const uint16_t*>(a.v_tree) + static_cast<int64_t>(n0 + key0) * a.ldv +
-                                 static_cast<int64_t>(h) * D + tid;
+                                 static_cast<int64_t>(h) * D + (tid & ~1);
+          const int ldv = static_cast<int>(a.ldv);
 #pragma unroll 1
           for (int c = 2 * half; c < 2 * half + 2; ++c) {
             uint32_t v[16];
@@ -429,14 +446,17 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
             for (int i = 0; i < 16; ++i) v[i] = 0u;   // places without nodes are zeros
             if (32 * c < nkeys) {
               // all loads first (beyond the last node: that node again), in one latency
-              uint16_t x[32];
+              const int k0 = 32 * c + (tid & 1);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = rows[static_cast<int64_t>(min(32 * c + i, nkeys - 1)) * a.ldv];
+              for (int i = 0; i < 16; ++i)
+                v[i] = *reinterpret_cast<const uint32_t*>(rows + static_cast<int64_t>(min(k0 + 2 * i, nkeys - 1)) * ldv);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                uint32_t e = 32 * c + i < nkeys ? x[i] : 0u;
-                if ((e & 0x7f80u) == 0x7f80u) { e = 0u; bad = true; }
-                v[i >> 1] |= e << (16 * (i & 1));
+              for (int i = 0; i < 16; ++i) {
+                uint32_t e = k0 + 2 * i < nkeys ? v[i] : 0u;
+                if ((e & 0x7f80u) == 0x7f80u) { e &= 0xffff0000u; bad = true; }
+                if ((e & 0x7f800000u) == 0x7f800000u) { e &= 0x0000ffffu; bad = true; }
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, e, 1);
+                v[i] = tid & 1 ? __byte_perm(other, e, 0x7632) : __byte_perm(e, other, 0x5410);
               }
             }
             tmem_st16(tmem + L::tV + lane_off + 16 * c, v);
@@ -476,16 +496,27 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           y[c / 2 + 1] = fma2(pair(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sk2, m.y);
         }
       }
-      if (__builtin_expect(tree || key0 + kKeys > low_vis[half] || !__all_sync(0xffffffffu, valid), 0)) {
+      if (__builtin_expect(tree || low_vis[half] < min(key0 + kKeys, x.len), 0)) {
         const uint32_t* words = anc_s + warp * kRowsT;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          float lo, hi;
-          split(y[c / 2], lo, hi);
-          const bool s0 = tree ? valid && ((words[c] >> lane) & 1u) : key < vis_s[c];
-          const bool s1 = tree ? valid && ((words[c + 1] >> lane) & 1u) : key < vis_s[c + 1];
-          y[c / 2] = pair(s0 ? lo : -INFINITY, s1 ? hi : -INFINITY);
+        for (int c = 0; c < kCols; c += 4) {
+          const uint4 m = *reinterpret_cast<const uint4*>(words + c);
+          const int4 q = *reinterpret_cast<const int4*>(vis_s + c);
+          const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+          const int vis[4] = {q.x, q.y, q.z, q.w};
+          float v[4];
+          split(y[c / 2], v[0], v[1]);
+          split(y[c / 2 + 1], v[2], v[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(tree ? valid && ((w[i] >> lane) & 1u) : key < vis[i])) v[i] = -INFINITY;
+          y[c / 2] = pair(v[0], v[1]);
+          y[c / 2 + 1] = pair(v[2], v[3]);
         }
+      } else if (!__all_sync(0xffffffffu, valid)) {   // every row sees every valid key
+        const uint64_t none = pair(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) y[c] = valid ? y[c] : none;
       }
       bool slow = first || force;
       if (!slow) {
