@@ -9,7 +9,11 @@ namespace {
 bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
   return B >= 0 && max_nodes >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && (d == 64 || d == 128);
 }
-bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 32; }
+// Which bf16 kernel: up to 16 rows per KV head the warps' own mma.sync (a
+// single token of 64 requests over 512..4096 tokens 52 us; the tcgen05 tile of
+// 64 rows would cost 155), above it tcgen05 (8 nodes x 4 heads: mma.sync 152
+// us, and 36 for one request, against 150 and 21).
+bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 16; }
 }  // namespace
 
 TV_API size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype) {

@@ -1,4 +1,4 @@
-// tree_verify_attn_kv4 for few query rows (bf16; at most 32 rows = nodes x
+// tree_verify_attn_kv4 for few query rows (bf16; at most 16 rows = nodes x
 // heads of one KV head: single tokens, short drafts), d = 64 or 128.
 //
 // Every warp works by itself: it walks its own run of 64-token chunks, with
@@ -86,8 +86,7 @@ template <int D, int NB>
 __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const __grid_constant__ MmaArgs p) {
   using L = Lay<D, NB>;
   constexpr int kC = D / 32, kDm = D / 16, R = 8 * NB;
-  constexpr int M = NB == 4 ? 2 : 4;             // blocks of 16 keys taken together (registers)
-  constexpr int kTreeM = NB == 4 ? 2 : 1;        // blocks of 16 nodes: there are no more nodes than rows
+  constexpr int M = kChunk / 16;                 // blocks of 16 keys; the nodes fit in one, being no more than the rows
   extern __shared__ __align__(128) uint8_t sm[];
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
@@ -257,13 +256,17 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
       const int rows = cnt * g;
       __syncwarp();
 #pragma unroll 1
-      for (int i = 0; i < NB * kC; ++i) {
-        const int r = 8 * (i / kC) + gq, c = i % kC;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows)
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(n0 + r / g) * a.ldq +
-                                              static_cast<int64_t>(h * g + r % g) * D + 32 * c + 8 * tq);
-        *reinterpret_cast<uint4*>(mine + L::kQ + i * 512 + lane * 16) = v;
+      for (int nb = 0; nb < NB; ++nb) {          // eight rows' loads in one latency
+        const int r = 8 * nb + gq;
+        const uint16_t* row = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(n0 + min(r, rows - 1) / g) * a.ldq +
+                              static_cast<int64_t>(h * g + min(r, rows - 1) % g) * D + 8 * tq;
+        uint4 v[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) v[c] = *reinterpret_cast<const uint4*>(row + 32 * c);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          *reinterpret_cast<uint4*>(mine + L::kQ + (nb * kC + c) * 512 + lane * 16) =
+              r < rows ? v[c] : make_uint4(0u, 0u, 0u, 0u);
       }
       live = 0;
       low_vis = 0x7fffffff;
@@ -299,8 +302,6 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     const int key0 = blk * kChunk, nkeys = tree ? cnt : min(kChunk, u.len - key0);
     const unsigned pages = (good >> (8 * st)) & 0xffu;
 
-#pragma unroll 1
-    for (int kb = 0; kb < (tree ? 32 : kChunk); kb += 16 * M) {   // keys kb .. kb + 16 M - 1 of the chunk
     // ---- S^T = K Q^T
     float s[M][NB][4];
 #pragma unroll
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
       const uint8_t* kp[M];
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        kp[m] = stage + (kb ? pg[m + 4 - M] + 16 * sl[m + 4 - M] : pg[m] + 16 * sl[m]) + gq * 16 + tq * 4;
+        kp[m] = stage + pg[m] + 16 * sl[m] + gq * 16 + tq * 4;
       }
 #pragma unroll 1
       for (int c = 0; c < kC; ++c) {
@@ -335,36 +336,32 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
         }
       }
     } else {
-      // the nodes' own keys, at most 32
-#pragma unroll 1
-      for (int c = 0; c < kC; ++c) {
-        uint4 q[NB];
+      // the nodes' own keys, at most 16 (beyond the last: that one again, masked below)
+      {
+        uint4 x[2][kC];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) q[i] = *reinterpret_cast<const uint4*>(mine + L::kQ + (i * kC + c) * 512 + lane * 16);
+        for (int b = 0; b < 2; ++b) {
+          const uint16_t* row = static_cast<const uint16_t*>(a.k_tree) +
+                                static_cast<int64_t>(n0 + min(gq + 8 * b, cnt - 1)) * a.ldk +
+                                static_cast<int64_t>(h) * D + 8 * tq;
 #pragma unroll
-        for (int m = 0; m < kTreeM; ++m) {
-          if (16 * m >= cnt) break;          // (nodes: kb is 0)
-          uint4 x[2];
+          for (int c = 0; c < kC; ++c) x[b][c] = *reinterpret_cast<const uint4*>(row + 32 * c);
+        }
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int j = 16 * m + gq + 8 * b;
-            x[b] = make_uint4(0u, 0u, 0u, 0u);
-            if (j < cnt)
-              x[b] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_tree) +
-                                                     static_cast<int64_t>(n0 + j) * a.ldk + static_cast<int64_t>(h) * D +
-                                                     32 * c + 8 * tq);
-          }
-          const uint32_t f0[4] = {x[0].x, x[1].x, x[0].y, x[1].y}, f1[4] = {x[0].z, x[1].z, x[0].w, x[1].w};
+        for (int c = 0; c < kC; ++c) {
+          const uint32_t f0[4] = {x[0][c].x, x[1][c].x, x[0][c].y, x[1][c].y};
+          const uint32_t f1[4] = {x[0][c].z, x[1][c].z, x[0][c].w, x[1][c].w};
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            mma16816(s[m][i], f0, q[i].x, q[i].y);
-            mma16816(s[m][i], f1, q[i].z, q[i].w);
+            const uint4 q = *reinterpret_cast<const uint4*>(mine + L::kQ + (i * kC + c) * 512 + lane * 16);
+            mma16816(s[0][i], f0, q.x, q.y);
+            mma16816(s[0][i], f1, q.z, q.w);
           }
         }
       }
     }
 
-    // ---- scores in base-2 units over the references: keys kb + 16 m + g, + 8, rows 2t, 2t + 1
+    // ---- scores in base-2 units over the references: keys 16 m + g, + 8, rows 2t, 2t + 1
     uint64_t y[M][NB][2];
     float sv[M][2];
     const bool full = !tree && nkeys == kChunk && key0 + kChunk <= low_vis &&
@@ -378,7 +375,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
           float sk = c2;
           sv[m][b] = 1.f;
           if (!tree) {
-            const uint8_t* at = stage + (kb ? pg[m + 4 - M] + 2 * sl[m + 4 - M] : pg[m] + 2 * sl[m]) + Pe * D + 2 * gq + 16 * b;
+            const uint8_t* at = stage + pg[m] + 2 * sl[m] + Pe * D + 2 * gq + 16 * b;
             sk = c2 * bf16_at(reinterpret_cast<const uint16_t*>(at));
             sv[m][b] = bf16_at(reinterpret_cast<const uint16_t*>(at + 2 * Pe));
           }
@@ -400,7 +397,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
         for (int m = 0; m < M; ++m)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const int k = kb + 16 * m + gq + 8 * b;
+            const int k = 16 * m + gq + 8 * b;
             const bool there = k < nkeys && (tree || (P > kChunk ? pages != 0 : (pages >> (k >> shift)) & 1u));
             if (!there) sv[m][b] = 0.f;
 #pragma unroll
@@ -515,7 +512,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     if (!tree) {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const uint8_t* vg = stage + (kb ? pg[m + 4 - M] + sl[m + 4 - M] * (D / 2) : pg[m] + sl[m] * (D / 2)) + Pe * (D / 2) +
+        const uint8_t* vg = stage + pg[m] + sl[m] * (D / 2) + Pe * (D / 2) +
                             gq * 16;
 #pragma unroll
         for (int d = 0; d < kDm; ++d) {
@@ -529,30 +526,36 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     } else {
       // the nodes' own values; one that is not finite must not meet the zero weights of rows that do not see it:
       // it is taken out here and added at the end to the rows that see it
+      {
+        const uint16_t* rows[4];
 #pragma unroll
-      for (int m = 0; m < kTreeM; ++m) {
-        if (16 * m >= cnt) break;
+        for (int k = 0; k < 4; ++k)
+          rows[k] = static_cast<const uint16_t*>(a.v_tree) +
+                    static_cast<int64_t>(n0 + min(2 * tq + (k & 1) + 8 * (k >> 1), cnt - 1)) * a.ldv +
+                    static_cast<int64_t>(h) * D + 2 * gq;
 #pragma unroll
-        for (int d = 0; d < kDm; ++d) {
-          uint32_t w[4];
+        for (int d0 = 0; d0 < kDm; d0 += 4) {    // four blocks' loads in one latency
+          uint32_t w[4][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = 16 * m + 2 * tq + (k & 1) + 8 * (k >> 1);
-            w[k] = 0u;
-            if (j < cnt)
-              w[k] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.v_tree) +
-                                                        static_cast<int64_t>(n0 + j) * a.ldv +
-                                                        static_cast<int64_t>(h) * D + 16 * d + 2 * gq);
-            if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; dirty = true; }
-            if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0x0000ffffu; dirty = true; }
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[d][k] = *reinterpret_cast<const uint32_t*>(rows[k] + 16 * (d0 + d));
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t& e = w[d][k];
+              if (2 * tq + (k & 1) + 8 * (k >> 1) >= cnt) e = 0u;
+              if ((e & 0x7f80u) == 0x7f80u) { e &= 0xffff0000u; dirty = true; }
+              if ((e & 0x7f800000u) == 0x7f800000u) { e &= 0x0000ffffu; dirty = true; }
+            }
+            const uint32_t f[4] = {__byte_perm(w[d][0], w[d][1], 0x5410), __byte_perm(w[d][0], w[d][1], 0x7632),
+                                   __byte_perm(w[d][2], w[d][3], 0x5410), __byte_perm(w[d][2], w[d][3], 0x7632)};
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mma16816(o[d0 + d][i], f, pb[0][i][0], pb[0][i][1]);
           }
-          const uint32_t f[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                                 __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
-#pragma unroll
-          for (int i = 0; i < NB; ++i) mma16816(o[d][i], f, pb[m][i][0], pb[m][i][1]);
         }
       }
-    }
     }
 
     __syncwarp();                                // the stage was read
@@ -633,9 +636,9 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
 
 int blocks_of(int max_nodes, int g) {            // blocks of eight rows
   const int rows = max_nodes * g;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return rows <= 8 ? 1 : 2;
 }
-int warps_of(int nb) { return nb == 1 ? Lay<128, 1>::kWarps : Lay<128, 4>::kWarps; }
+int warps_of(int nb) { return nb == 1 ? Lay<128, 1>::kWarps : Lay<128, 2>::kWarps; }
 
 template <int D, int NB>
 int launch(const MmaArgs& p, cudaStream_t st) {
@@ -669,8 +672,8 @@ int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st) {
     if (rc != TV_OK) return rc;
     p.extents = extents;
   }
-  if (a.d == 128) return nb == 1 ? launch<128, 1>(p, st) : nb == 2 ? launch<128, 2>(p, st) : launch<128, 4>(p, st);
-  return nb == 1 ? launch<64, 1>(p, st) : nb == 2 ? launch<64, 2>(p, st) : launch<64, 4>(p, st);
+  if (a.d == 128) return nb == 1 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
+  return nb == 1 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
 }
 
 }  // namespace kv4

@@ -125,7 +125,7 @@ __device__ __forceinline__ int prefix_len(const AttnArgs& a, int r) {
 }
 
 int attn_simt(const AttnArgs& a, cudaStream_t st);            // fp32 rows
-int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st);   // bf16, at most 32 rows per KV head
+int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st);   // bf16, at most 16 rows per KV head
 int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st);    // bf16
 size_t attn_mma_workspace(int B, int max_nodes, int Hq, int Hkv, int d);
 size_t attn_tc_workspace(int B, int max_nodes, int Hq, int Hkv, int d);

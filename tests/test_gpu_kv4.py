@@ -322,6 +322,16 @@ ATTN = [
     ([150], [140], 2, 2, 128, 32, "chain", True),
     ([5], [260], 64, 1, 128, 16, "roots", False),
     ([4, 4], [96, 17], 48, 1, 64, 32, "chain", False),
+    # few rows per KV head: 3 to 16, one and two blocks of eight
+    ([3, 1, 2], [64, 200, 65], 8, 2, 128, 16, "chain", True),
+    ([2], [1000], 16, 4, 64, 128, "roots", False),
+    ([4, 3, 1], [300, 1, 63], 32, 8, 128, 32, "random", False),
+    ([16, 9], [130, 128], 1, 1, 128, 128, "random", True),
+    ([1, 1], [65, 129], 16, 1, 128, 64, "chain", True),
+    ([2, 2], [40, 700], 7, 1, 64, 16, "chain", False),
+    # 17 rows and one more tile of 64
+    ([17], [127], 1, 1, 64, 64, "roots", False),
+    ([65], [100], 2, 2, 128, 64, "random", False),
 ]
 
 
@@ -335,24 +345,26 @@ def test_attention_matches_the_oracle(tv, counts, lens, Hq, Hkv, d, P, kind, vis
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-def test_attention_large_logits_and_scale(tv, bf16):
-    c = Case(7, [20, 3], [300, 140], 8, 2, 128, 64, bf16, scale=2.5)   # peaked softmax, growing maxima
+@pytest.mark.parametrize("counts", [[20, 3], [2, 1], [4, 4]])
+def test_attention_large_logits_and_scale(tv, counts, bf16):
+    c = Case(7, counts, [300, 140], 8, 2, 128, 64, bf16, scale=2.5)   # peaked softmax, growing maxima
     out, lse, _ = c.run(tv)
     c.check(out, lse)
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-def test_attention_node_cnt_leaves_other_rows(tv, bf16):
-    c = Case(8, [16, 16, 9], [100, 300, 64], 8, 2, 128, 32, bf16, "chain", node_cnt=[5, 0, 9])
+@pytest.mark.parametrize("counts,cnt", [([16, 16, 9], [5, 0, 9]), ([4, 2, 3], [1, 0, 3])])
+def test_attention_node_cnt_leaves_other_rows(tv, counts, cnt, bf16):
+    c = Case(8, counts, [100, 300, 64], 8, 2, 128, 32, bf16, "chain", node_cnt=cnt)
     n = int(c.off[-1])
     out = torch.full((n, 8, 128), 5.0, dtype=c.q.dtype, device="cuda")
     lse = torch.full((n, 8), 5.0, device="cuda")
     c.run(tv, out=out, lse=lse)
     c.check(out, lse)
-    left = [i for i in range(n) if not (i < 5 or i >= 32)]
+    left = [c.off[r] + i for r in range(3) for i in range(cnt[r], counts[r])]
     assert (out[left] == 5).all() and (lse[left] == 5).all()
     without, none, _ = c.run(tv, want_lse=False)
-    assert none is None and torch.equal(without[:5], out[:5])
+    assert none is None and torch.equal(without[:cnt[0]], out[:cnt[0]])
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -369,10 +381,25 @@ def test_attention_rows_that_see_nothing(tv, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-def test_attention_ignores_whatever_it_does_not_see(tv, bf16):
+def test_attention_few_rows_that_see_nothing_or_late(tv, bf16):
+    """Rows whose first visible key comes after many masked ones, and rows without any, among few rows."""
+    c = Case(19, [4, 2], [200, 70], 8, 2, 128, 64, bf16, "chain", vis=True)
+    c.vis[:] = [0, 200, 0, 1, 0, 70]
+    for i in (0, 4):
+        c.anc[i] = 0
+        c.see[i] = False
+    out, lse, _ = c.run(tv)
+    c.check(out, lse)
+    assert (out[[0, 4]] == 0).all() and torch.isneginf(lse[[0, 4]]).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("counts", [[24, 24, 10], [4, 4, 3]])
+def test_attention_ignores_whatever_it_does_not_see(tv, counts, bf16):
     """NaN and infinities in tree rows that a node does not see, in rows of other requests, in rows beyond node_cnt,
     and NaN scales behind the end of the cached tokens."""
-    c = Case(10, [24, 24, 10], [70, 129, 33], 8, 2, 128, 64, bf16, "random", node_cnt=[24, 12, 10])
+    half = counts[1] // 2
+    c = Case(10, counts, [70, 129, 33], 8, 2, 128, 64, bf16, "random", node_cnt=[counts[0], half, counts[2]])
     clean = c.run(tv)
     want = c.oracle()
     d, P = c.d, c.P
@@ -381,43 +408,57 @@ def test_attention_ignores_whatever_it_does_not_see(tv, bf16):
         if pg >= 0:
             c.cache[pg, :, P * d + 2 * (n % P):P * d + 2 * P] = 0xFF
             c.cache[pg, :, P * d + 2 * P + 2 * (n % P):] = 0xFF
-    poison = [24 + 12, 24 + 20, 47]            # nodes that node_cnt leaves out
-    for i, bad in zip(poison, (NAN, float("inf"), -float("inf"))):
+    gone = list(range(int(c.off[1]) + half, int(c.off[2])))    # nodes that node_cnt leaves out
+    for i, bad in zip(gone, (NAN, float("inf"), -float("inf"))):
         c.k[i], c.v[i], c.q[i] = bad, bad, bad
-    leaf = 23                                  # the last node is nobody's ancestor
+    leaf = counts[0] - 1                       # the last node is nobody's ancestor
     c.k[leaf], c.v[leaf] = NAN, NAN
     out, lse, err = c.run(tv)
     assert int(err) == 0
-    rows = [i for i in range(58) if i != leaf and not 36 <= i < 48]
+    rows = [i for i in range(sum(counts)) if i != leaf and i not in gone]
     assert torch.equal(out[rows], clean[0][rows]) and torch.equal(lse[rows], clean[1][rows])
     assert torch.isnan(out[leaf]).all() and torch.isnan(lse[leaf]).all()
     c.check(clean[0], clean[1], want)
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-def test_attention_nan_and_infinity_reach_exactly_the_rows_that_see_them(tv, bf16):
-    c = Case(11, [10, 4], [40, 40], 8, 2, 128, 16, bf16, "chain")
+@pytest.mark.parametrize("counts", [[10, 6], [4, 3]])
+def test_attention_nan_and_infinity_reach_exactly_the_rows_that_see_them(tv, counts, bf16):
+    n0, n = counts[0], sum(counts)
+    c = Case(11, counts, [40, 40], 8, 2, 128, 16, bf16, "chain")
     clean = c.run(tv)
-    c.v[4, 1, 7] = float("inf")                # node 4 of request 0, KV head 1, dim 7
-    c.v[6, 0, 3] = NAN
+    a, b = n0 // 2 - 1, n0 - 2
+    c.v[a, 1, 7] = float("inf")                # a node of request 0, KV head 1, dim 7
+    c.v[b, 0, 3] = NAN
     out, lse, _ = c.run(tv)
     exp = clean[0].clone()
-    exp[4:10, 4:, 7] = float("inf")
-    exp[6:10, :4, 3] = NAN
+    exp[a:n0, 4:, 7] = float("inf")
+    exp[b:n0, :4, 3] = NAN
     assert torch.equal(torch.isnan(out), torch.isnan(exp)) and torch.equal(torch.isinf(out), torch.isinf(exp))
     ok_ = torch.isfinite(exp)
     assert torch.equal(out[ok_], exp[ok_]) and torch.equal(lse, clean[1])
-    # a cached token whose row was not finite: every row that sees it is NaN
+    # a cached token whose key was not finite: every row that sees it is NaN, the others are as they were
+    c = Case(11, counts, [40, 40], 8, 2, 128, 16, bf16, "chain", vis=True)
+    c.vis[:] = 40
+    c.vis[n0] = 35                             # tokens 0 .. 34: token 35 is not among them
+    clean = c.run(tv)
     pg = c.table[1, 2]
     c.cache[pg, 0, c.P * 128 + 2 * 3:c.P * 128 + 2 * 3 + 2] = [0xC0, 0x7F]
     out, lse, _ = c.run(tv)
-    assert torch.isnan(out[10:, :4]).all() and torch.isnan(lse[10:, :4]).all()
-    assert torch.equal(out[10:, 4:], clean[0][10:, 4:])
+    assert torch.isnan(out[n0 + 1:, :4]).all() and torch.isnan(lse[n0 + 1:, :4]).all()
+    assert torch.equal(out[:n0 + 1], clean[0][:n0 + 1]) and torch.equal(out[n0 + 1:, 4:], clean[0][n0 + 1:, 4:])
+    # ... whose value was not: outputs are NaN, the sums are not
+    c.cache[pg, 0, c.P * 128 + 2 * 3:c.P * 128 + 2 * 3 + 2] = c.pool[0][pg, 0, c.P * 128 + 6:c.P * 128 + 8]
+    c.cache[pg, 0, c.P * 130 + 2 * 3:c.P * 130 + 2 * 3 + 2] = [0xC0, 0x7F]
+    out, lse, _ = c.run(tv)
+    assert torch.isnan(out[n0 + 1:, :4]).all() and torch.equal(lse, clean[1])
+    assert torch.equal(out[:n0 + 1], clean[0][:n0 + 1])
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-def test_attention_bad_pages_are_not_visible(tv, bf16):
-    c = Case(12, [5, 5], [200, 90], 8, 2, 128, 32, bf16)
+@pytest.mark.parametrize("counts", [[5, 5], [2, 1], [4, 4]])
+def test_attention_bad_pages_are_not_visible(tv, counts, bf16):
+    c = Case(12, counts, [200, 90], 8, 2, 128, 32, bf16)
     c.table[0, 2] = -1
     c.table[1, 1] = 10 ** 6
     c.page_ok = [np.arange(200) // 32 != 2, np.arange(90) // 32 != 1]
@@ -438,10 +479,11 @@ def test_attention_clamps_lengths(tv):
     c.check(out, lse)
 
 
-def test_attention_is_the_same_twice_on_another_stream_and_in_a_graph(tv):
-    c = Case(14, [16, 16, 1], [900, 1300, 40], 32, 8, 128, 64, True, "chain")
+@pytest.mark.parametrize("counts", [[16, 16, 1], [1, 1, 1], [3, 2, 4]])
+def test_attention_is_the_same_twice_on_another_stream_and_in_a_graph(tv, counts):
+    c = Case(14, counts, [900, 1300, 40], 32, 8, 128, 64, True, "chain")
     args, kw = c.args(), c.kwargs()
-    ws = [tv.tree_verify_attn_kv4_workspace(3, 16, 32, 8, 128) for _ in range(2)]
+    ws = [tv.tree_verify_attn_kv4_workspace(3, max(counts), 32, 8, 128) for _ in range(2)]
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     one = tv.tree_verify_attn_kv4(*args, **kw, ws=ws[0], err=err)
     torch.cuda.synchronize()
