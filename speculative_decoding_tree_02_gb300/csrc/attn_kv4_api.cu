@@ -9,10 +9,11 @@ namespace {
 bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
   return B >= 0 && max_nodes >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && (d == 64 || d == 128);
 }
-// Which bf16 kernel: up to 16 rows per KV head the warps' own mma.sync (a
-// single token of 64 requests over 512..4096 tokens 52 us; the tcgen05 tile of
-// 64 rows would cost 155), above it tcgen05 (8 nodes x 4 heads: mma.sync 152
-// us, and 36 for one request, against 150 and 21).
+// Which bf16 kernel: the warps' own mma.sync up to 16 rows per KV head, the
+// tcgen05 tiles above. 64 requests over 512..4096 tokens, 1 over 2048 and 8 over
+// 8192 of 8 KV heads of 128, mma.sync against tcgen05: 4 rows 56/17/35 against
+// 135/17/60 us, 16 rows 79/21/41 against 140/18/62, 32 rows 152/39/72 against
+// 146/19/64.
 bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 16; }
 }  // namespace
 

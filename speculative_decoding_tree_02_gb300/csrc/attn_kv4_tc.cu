@@ -95,6 +95,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r != 0;
+}
 // Barriers of a team and of a warpgroup, and the latter with an OR over its threads.
 __device__ __forceinline__ void team_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -136,8 +142,10 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   // aligned by an offset, so that the compiler still knows the pointer to be one to shared memory
   uint8_t* sm0 = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const AttnArgs& a = p.a;
-  const int team = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;   // warpgroup of the team
-  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31, c0 = kCols * half;
+  // the warp's number by a shuffle, so that the compiler knows all that follows from it to be uniform
+  const int warp16 = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int team = warp16 >> 3, half = (warp16 >> 2) & 1;   // warpgroup of the team
+  const int tid = threadIdx.x & 127, warp = warp16 & 3, lane = tid & 31, c0 = kCols * half;
   const int tbar = 1 + team, wid = 3 + 2 * team + half;
   const int g = a.Hq / a.Hkv;
   uint8_t* sm = sm0 + team * L::kTeam;
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   const int per = ((E + 15) / 16 + 31) / 32 * 32;  // entries per warp
   auto tiles_of = [&](int e, int end) { return e < end ? static_cast<long long>(extent_of(p, e).nb) * a.Hkv : 0ll; };
   {
-    const int w16 = threadIdx.x >> 5, lo = min(w16 * per, E), hi = min(lo + per, E);
+    const int w16 = warp16, lo = min(w16 * per, E), hi = min(lo + per, E);
     long long s = 0;
     for (int e = lo; e < hi; e += 32) s += tiles_of(e + lane, hi);
 #pragma unroll
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[0] + 256 * team;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0) + 256 * team;
   long long W = 0;
   for (int w = 0; w < 16; ++w) W += sums[w];
   const long long G = min(2ll * p.grid, W);
@@ -403,7 +411,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       tmem_st_wait();
       tc_fence_before();
       team_sync(tbar);
-      if (half == 0 && tid == 0) {
+      if (half == 0 && warp == 0 && elect()) {
         tc_fence_after();
         constexpr uint32_t idS = idesc_bf16(128, kRowsT, 0);
         const uint64_t qdesc = sdesc(sb + L::kQ, 16, 1024);
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
       team_sync(tbar);
-      if (tid == 0 && half == 1) {
+      if (half == 1 && warp == 0 && elect()) {
         tc_fence_after();
         constexpr uint32_t idO = idesc_bf16(128, kRowsT, 1);
         const uint64_t pdesc = sdesc(sb + L::kP, 1024, 1024);
