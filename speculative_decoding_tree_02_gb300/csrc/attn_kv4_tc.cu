@@ -101,18 +101,19 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
   return r != 0;
 }
-// Barriers of a team and of a warpgroup, and the latter with an OR over its threads.
+// Barriers of a team and of a warpgroup, and with an OR over their threads.
 __device__ __forceinline__ void team_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool wg_any(int id, bool p) {
+template <int kThreads>
+__device__ __forceinline__ bool any_of(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %2, 0;\n\t"
-      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "bar.red.or.pred q, %1, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"(id), "r"(static_cast<uint32_t>(p))
+      : "r"(id), "r"(static_cast<uint32_t>(p)), "n"(kThreads)
       : "memory");
   return r != 0;
 }
@@ -490,6 +491,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       if (!warp_wait(s_bar, it & 1, abort_flag, p.status, 43)) break;
       tc_fence_after();
       uint64_t y[kCols / 2];
+      for (bool slow = first || force;;) {
       {
         const uint64_t sk2 = pair(sk, sk);
         uint32_t v[kCols];
@@ -526,17 +528,6 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
 #pragma unroll
         for (int c = 0; c < kCols / 2; ++c) y[c] = valid ? y[c] : none;
       }
-      bool slow = first || force;
-      if (!slow) {
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) {
-          float lo, hi;
-          split(y[c], lo, hi);
-          mx[c & 1] = max3(mx[c & 1], lo, hi);
-        }
-        slow = wg_any(wid, fmaxf(mx[0], mx[1]) > 8.f);
-      }
       if (__builtin_expect(slow, 0)) {
         // new references: the rows' maxima so far
         int mine = static_cast<int>(0x80000000);
@@ -566,7 +557,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           corr_s[tid] = unset ? 0.f : ex2(-sh);
           shift_s[tid] = -sh;
         }
-        force = wg_any(wid, none);
+        force = any_of<128>(wid, none);
 #pragma unroll
         for (int c = 0; c < kCols; c += 4) {
           const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(shift_s + c);
@@ -593,6 +584,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         }
       }
       // ---- weights, times the value's scale -> P, one 128-byte swizzled row per key
+      float mx[2] = {-INFINITY, -INFINITY};
       {
         const uint64_t sv2 = pair(sv, sv);
         uint8_t* prow = sm + L::kP + tid * 128;
@@ -605,9 +597,9 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
             const int c = 4 * c8 + i;
             float lo, hi;
             split(y[c], lo, hi);
-            const uint64_t w = pair(ex2(lo), ex2(hi));
-            l[c] = add2(l[c], w);
-            split(mul2(w, sv2), lo, hi);
+            mx[i & 1] = max3(mx[i & 1], lo, hi);
+            y[c] = pair(ex2(lo), ex2(hi));
+            split(mul2(y[c], sv2), lo, hi);
             pk[i] = pack_bf16(lo, hi);
           }
           if (__builtin_expect(bad, 0)) {
@@ -621,7 +613,10 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
-      team_sync(tbar);
+      // a score beyond a reference by 2^8: the same again over new references
+      slow = any_of<256>(tbar, !slow && fmaxf(mx[0], mx[1]) > 8.f);
+      if (__builtin_expect(!slow, 1)) break;
+      }
       if (half == 1 && warp == 0 && elect()) {
         tc_fence_after();
         constexpr uint32_t idO = idesc_bf16(128, kRowsT, 1);
@@ -632,6 +627,8 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         umma_commit(pv_bar);
       }
       __syncwarp();
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c) l[c] = add2(l[c], y[c]);
       if (++st == kStages) { st = 0; turn ^= 1; }
       ++blk;
       if (__builtin_expect(!last, 1)) continue;
