@@ -68,8 +68,8 @@ struct Lay {
   static constexpr uint32_t kRow = kVis + 256;                // int [64] output row, -1: none
   static constexpr uint32_t kAnc = kRow + 256;                // u32 [4][64]
   static constexpr uint32_t kWarpMax = kAnc + 1024;           // int [4][64]
-  static constexpr uint32_t kPages = kWarpMax + 1024;         // u32 [kStages] bit i: page i of the tile is staged
-  static constexpr uint32_t kBars = kPages + 32;              // RAW [kStages], S, PV, DRAIN
+  static constexpr uint32_t kPages = kWarpMax + 1024;         // u8 [kStages][8] page i of the tile is staged; dirty, low_vis
+  static constexpr uint32_t kBars = kPages + 48;              // RAW [kStages], S, PV, DRAIN
   static constexpr uint32_t kTeam = (kBars + 64 + 1023) / 1024 * 1024;    // bytes of a team
   static constexpr uint32_t kMisc = 2 * kTeam;                // tensor memory address, abort flag, entry sums
   static constexpr uint32_t kBytes = kMisc + 192 + 1024;      // + alignment slack
@@ -156,8 +156,11 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   long long* sums = reinterpret_cast<long long*>(sm0 + L::kMisc + 16);
   auto raw_bar = [&](int st) { return sb + L::kBars + 8u * st; };
   const uint32_t s_bar = sb + L::kBars + 8 * kStages, pv_bar = s_bar + 8, drain_bar = s_bar + 16;
+  const uint32_t blk_bytes = static_cast<uint32_t>(a.page_size) * (D + 4);
+  const int ps_shift = 31 - __clz(a.page_size), per_tile = kKeys >> ps_shift;
   if (tid == 0 && half == 0) {
-    for (int i = 0; i < kStages + 3; ++i) mbar_init(sb + L::kBars + 8 * i, i == kStages + 2 ? 2 : 1);
+    for (int i = 0; i < kStages + 3; ++i)
+      mbar_init(sb + L::kBars + 8 * i, i < kStages ? per_tile : i == kStages + 2 ? 2 : 1);
     if (team == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -223,13 +226,13 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     const int skip = static_cast<int>(w0 - before);
     int h = skip / x.nb, blk = skip % x.nb;
 
-    const uint32_t blk_bytes = static_cast<uint32_t>(a.page_size) * (D + 4);
-    const int ps_shift = 31 - __clz(a.page_size), per_tile = kKeys >> ps_shift;
-    const bool loader = half == 1 && warp == 3;
-    // ---- loads (one warp): kStages tiles ahead, their page numbers one more
+    // ---- loads: page i of a tile by the team's warp 7 - i, kStages tiles ahead, its number one more
+    const int page_i = 7 - (warp16 & 7);
+    const bool loader = page_i < per_tile;
+    volatile uint8_t* staged = sm + L::kPages;
     int le = e, lh = h, lblk = blk, lnext = 0, lpage = -1, lr = e / p.tiles, lt = e % p.tiles;
     Extent lx = x;
-    auto look = [&]() {                          // this lane's page of the next tile to load
+    auto look = [&]() {                          // this warp's page of the next tile to load
       lpage = -1;
       if (lnext >= n) return;
       if (lblk == lx.nb) {
@@ -242,8 +245,8 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           } while (lx.nb == 0 && le + 1 < E);
         }
       }
-      const int key = lblk * kKeys + (lane << ps_shift);
-      if (lblk < lx.np && lane < per_tile && key < lx.len)
+      const int key = lblk * kKeys + (page_i << ps_shift);
+      if (lblk < lx.np && key < lx.len)
         lpage = a.block_table[static_cast<int64_t>(lr) * a.table_ld + (key >> ps_shift)];
     };
     // What the start of a unit and its tile of nodes read, on its way into L1 some tiles ahead.
@@ -259,20 +262,22 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     };
     auto load = [&](int st) {
       if (lnext >= n) return;
-      if (lblk == 0 && lnext > 0) announce();
-      const bool wanted = lblk < lx.np && lane < per_tile && lblk * kKeys + (lane << ps_shift) < lx.len;
-      const bool ok = wanted && lpage >= 0 && lpage < a.n_pages;
-      if (wanted && !ok && a.err) *a.err = 1;
-      const unsigned have = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) {
-        *reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) = have;
-        if (have) mbar_expect_tx(raw_bar(st), __popc(have) * blk_bytes);
-        else mbar_arrive(raw_bar(st));
+      if (page_i == 0 && lblk == 0 && lnext > 0) announce();
+      const bool wanted = lblk < lx.np && lblk * kKeys + (page_i << ps_shift) < lx.len;
+      const int page = __shfl_sync(0xffffffffu, lpage, 0);
+      const bool ok = wanted && page >= 0 && page < a.n_pages;
+      if (elect()) {
+        staged[8 * st + page_i] = ok;
+        if (ok) {
+          mbar_expect_tx(raw_bar(st), blk_bytes);
+          bulk_load(sb + L::kRaw + st * L::kStage + page_i * blk_bytes,
+                    a.cache + (static_cast<int64_t>(page) * a.Hkv + lh) * blk_bytes, blk_bytes, raw_bar(st));
+        } else {
+          mbar_arrive(raw_bar(st));
+          if (wanted && a.err) *a.err = 1;
+        }
       }
       __syncwarp();
-      if (ok)
-        bulk_load(sb + L::kRaw + st * L::kStage + lane * blk_bytes,
-                  a.cache + (static_cast<int64_t>(lpage) * a.Hkv + lh) * blk_bytes, blk_bytes, raw_bar(st));
       ++lblk;
       ++lnext;
     };
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     uint64_t l[kCols / 2];                       // this key's share of the rows' sums
 #pragma unroll
     for (int c = 0; c < kCols / 2; ++c) l[c] = 0ull;
-    volatile int* dirty = reinterpret_cast<volatile int*>(sm + L::kPages + 16);   // non-finite tree values met
-    volatile int* low_vis = reinterpret_cast<volatile int*>(sm + L::kPages + 20);  // [2] prefix that all rows see
+    volatile int* dirty = reinterpret_cast<volatile int*>(sm + L::kPages + 32);   // non-finite tree values met
+    volatile int* low_vis = reinterpret_cast<volatile int*>(sm + L::kPages + 36);  // [2] prefix that all rows see
     bool force = false, fresh = true;            // a row without reference; a new unit
     int seg_blk = blk, r = 0, t = 0, n0 = 0, cnt = 0;
     int st = 0, turn = 0, it = 0;
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       // this key's scales
       float sk = c2, sv = 1.f;
       if (!tree) {
-        valid = valid && ((*reinterpret_cast<volatile uint32_t*>(sm + L::kPages + 4 * st) >> (tid >> ps_shift)) & 1u);
+        valid = valid && staged[8 * st + (tid >> ps_shift)];
         sk = valid ? c2 * bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off)) : 0.f;
         sv = valid ? bf16_at(reinterpret_cast<const uint16_t*>(raw + scale_off + 2 * a.page_size)) : 0.f;
       }
