@@ -100,6 +100,7 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
 }
 // By a whole warp: true when the phase is over, the same in all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  if (__builtin_expect(__all_sync(0xffffffffu, tc::mbar_test(bar, parity)), 1)) return true;
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, err, code));
 }
 
