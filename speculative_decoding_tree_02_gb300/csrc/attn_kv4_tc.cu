@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       group_off[i] = (k0 >> ps_shift) * static_cast<int>(blk_bytes) + a.page_size * (D / 2) +
                      (k0 & (a.page_size - 1)) * (D / 2) + tid * 8;
     }
+    const int inv_g = 65536 / g + 1;             // row / g = row inv_g / 2^16 for the 64 rows and g <= 64
+    auto node_of = [&](int row) { return row * inv_g >> 16; };
     const float c2 = a.scale * kLog2e;
     // a row's reference (what its scores are taken over) is kept negated; -0: none yet
     float* nref = reinterpret_cast<float*>(sm + L::kRef) + c0;
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     volatile int* dirty = reinterpret_cast<volatile int*>(sm + L::kPages + 32);   // non-finite tree values met
     volatile int* low_vis = reinterpret_cast<volatile int*>(sm + L::kPages + 36);  // [2] prefix that all rows see
     bool force = false, fresh = true;            // a row without reference; a new unit
-    int seg_blk = blk, r = 0, t = 0, n0 = 0, cnt = 0;
+    int seg_blk = blk, unit_e = -1, r = 0, t = 0, n0 = 0, cnt = 0;
     int st = 0, turn = 0, it = 0;
     for (; it < n; ++it) {
       if (blk == x.nb) {                         // next unit
@@ -334,11 +336,14 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       if (fresh) {
         // the unit's queries, K-major with the 128-byte swizzle; its rows (all MMAs of the unit before have completed)
         fresh = false;
-        r = e / p.tiles;
-        t = e % p.tiles;
-        const Span sp = node_span(a, r);
-        n0 = sp.n0;
-        cnt = sp.cnt;
+        if (e != unit_e) {                       // (else another KV head of the same rows)
+          unit_e = e;
+          r = e / p.tiles;
+          t = e % p.tiles;
+          const Span sp = node_span(a, r);
+          n0 = sp.n0;
+          cnt = sp.cnt;
+        }
         const int node0 = t * p.nq, rows = min(p.nq, cnt - node0) * g;
 #pragma unroll 4
         for (int i = tid + 128 * half; i < kRowsT * (D / 8); i += 256) {
@@ -346,15 +351,15 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (rr < rows)
             v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                static_cast<int64_t>(n0 + node0 + rr / g) * a.ldq +
-                                                static_cast<int64_t>(h * g + rr % g) * D + 8 * c);
+                                                static_cast<int64_t>(n0 + node0 + node_of(rr)) * a.ldq +
+                                                static_cast<int64_t>(h * g + rr - node_of(rr) * g) * D + 8 * c);
           *reinterpret_cast<uint4*>(sm + L::kQ + (c >> 3) * L::kQHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (tid < kCols) {
-          const int rr = c0 + tid, gn = n0 + node0 + rr / g;
+          const int rr = c0 + tid, gn = n0 + node0 + node_of(rr);
           nref[tid] = -0.f;
-          row_s[tid] = rr < rows ? gn * a.Hq + h * g + rr % g : -1;
+          row_s[tid] = rr < rows ? gn * a.Hq + h * g + rr - node_of(rr) * g : -1;
           const int vis = rr < rows ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
           vis_s[tid] = vis;
           const int lowest = __reduce_min_sync(0xffffffffu, rr < rows ? vis : 0x7fffffff);
