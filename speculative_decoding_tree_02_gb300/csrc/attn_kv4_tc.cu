@@ -66,8 +66,7 @@ struct Lay {
   static constexpr uint32_t kInv = kCorr + 256;               // float [64]
   static constexpr uint32_t kVis = kInv + 256;                // int [64]
   static constexpr uint32_t kRow = kVis + 256;                // int [64] output row, -1: none
-  static constexpr uint32_t kAnc = kRow + 256;                // u32 [4][64]
-  static constexpr uint32_t kWarpMax = kAnc + 1024;           // int [4][64]
+  static constexpr uint32_t kWarpMax = kRow + 256;            // float [2][4][32]
   static constexpr uint32_t kPages = kWarpMax + 1024;         // u8 [kStages][8] page i of the tile is staged; dirty, low_vis
   static constexpr uint32_t kBars = kPages + 48;              // RAW [kStages], S, PV, DRAIN
   static constexpr uint32_t kTeam = (kBars + 64 + 1023) / 1024 * 1024;    // bytes of a team
@@ -94,6 +93,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+// Maxima that are NaN when a value is: over a warp, of two.
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect() {
@@ -312,8 +322,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     float* inv_s = reinterpret_cast<float*>(sm + L::kInv) + c0;
     int* vis_s = reinterpret_cast<int*>(sm + L::kVis) + c0;
     int* row_s = reinterpret_cast<int*>(sm + L::kRow) + c0;
-    uint32_t* anc_s = reinterpret_cast<uint32_t*>(sm + L::kAnc) + c0;   // [4][64]
-    int* wmax = reinterpret_cast<int*>(sm + L::kWarpMax) + 128 * half;    // [4][32]
+    float* wmax = reinterpret_cast<float*>(sm + L::kWarpMax) + 128 * half;   // [4][32]
     uint64_t l[kCols / 2];                       // this key's share of the rows' sums
 #pragma unroll
     for (int c = 0; c < kCols / 2; ++c) l[c] = 0ull;
@@ -377,6 +386,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
 
       // ---- K: thread = key, half of the dims
       bool valid = tid < nkeys;
+      uint32_t see = 0u;                         // tree tiles: this row's nodes, then this node's rows
       if (!tree) {
         uint4 w[D / 64];
 #pragma unroll
@@ -400,17 +410,10 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           const uint4 w = *reinterpret_cast<const uint4*>(row + 8 * i);
           v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
         }
-        if (tid < kCols) {                       // the rows' masks over the tile's nodes
-          const int at = row_s[tid];
-          uint64_t m[2];
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int word = (key0 >> 6) + w;
-            m[w] = at >= 0 && word < a.anc_words ? a.anc[static_cast<int64_t>(at / a.Hq) * a.anc_words + word] : 0ull;
-          }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) anc_s[w * kRowsT + tid] = static_cast<uint32_t>(m[w >> 1] >> (32 * (w & 1)));
-        }
+        // the mask of row c0 + lane over the 32 nodes of this warp
+        const int node0 = t * p.nq, node = node0 + node_of(c0 + lane), word = (key0 >> 6) + (warp >> 1);
+        if (c0 + lane < min(p.nq, cnt - node0) * g && word < a.anc_words)
+          see = reinterpret_cast<const uint32_t*>(a.anc + static_cast<int64_t>(n0 + node) * a.anc_words + word)[warp & 1];
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t u[16];
@@ -466,16 +469,27 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
             if (32 * c < nkeys) {
               // all loads first (beyond the last node: that node again), in one latency
               const int k0 = 32 * c + (tid & 1);
+              uint32_t odd = 0u;
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 v[i] = *reinterpret_cast<const uint32_t*>(rows + static_cast<int64_t>(min(k0 + 2 * i, nkeys - 1)) * ldv);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                uint32_t e = k0 + 2 * i < nkeys ? v[i] : 0u;
-                if ((e & 0x7f80u) == 0x7f80u) { e &= 0xffff0000u; bad = true; }
-                if ((e & 0x7f800000u) == 0x7f800000u) { e &= 0x0000ffffu; bad = true; }
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, e, 1);
-                v[i] = tid & 1 ? __byte_perm(other, e, 0x7632) : __byte_perm(e, other, 0x5410);
+                if (k0 + 2 * i >= nkeys) v[i] = 0u;
+                odd |= (v[i] & 0x7f807f80u) + 0x00800080u;   // bits 15 and 31: an exponent of ones
+              }
+              if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
+                bad = true;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+                  if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0x0000ffffu;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, v[i], 1);
+                v[i] = tid & 1 ? __byte_perm(other, v[i], 0x7632) : __byte_perm(v[i], other, 0x5410);
               }
             }
             tmem_st16(tmem + L::tV + lane_off + 16 * c, v);
@@ -497,6 +511,15 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
       tmem_st_wait();
 
+      if (tree) {                                // transpose the warp's 32 x 32 mask bits
+        uint32_t low = 0x0000ffffu;
+#pragma unroll
+        for (int j = 16; j; j >>= 1, low ^= low << j) {
+          const uint32_t w = __shfl_xor_sync(0xffffffffu, see, j);
+          see = lane & j ? (see & ~low) | ((w >> j) & low) : (see & low) | ((w << j) & ~low);
+        }
+      }
+
       // ---- softmax: thread = key; scores in base-2 units over the rows' references, two rows to a register pair
       if (!warp_wait(s_bar, it & 1, abort_flag, p.status, 43)) break;
       tc_fence_after();
@@ -517,21 +540,22 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         }
       }
       if (__builtin_expect(tree || low_vis[half] < min(key0 + kKeys, x.len), 0)) {
-        const uint32_t* words = anc_s + warp * kRowsT;
+        if (!tree) {
+          see = 0u;
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(vis_s + c);
+            see |= ((key < q.x ? 1u : 0u) | (key < q.y ? 2u : 0u) | (key < q.z ? 4u : 0u) | (key < q.w ? 8u : 0u)) << c;
+          }
+        }
+        if (!valid) see = 0u;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          const uint4 m = *reinterpret_cast<const uint4*>(words + c);
-          const int4 q = *reinterpret_cast<const int4*>(vis_s + c);
-          const uint32_t w[4] = {m.x, m.y, m.z, m.w};
-          const int vis[4] = {q.x, q.y, q.z, q.w};
-          float v[4];
-          split(y[c / 2], v[0], v[1]);
-          split(y[c / 2 + 1], v[2], v[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(tree ? valid && ((w[i] >> lane) & 1u) : key < vis[i])) v[i] = -INFINITY;
-          y[c / 2] = pair(v[0], v[1]);
-          y[c / 2 + 1] = pair(v[2], v[3]);
+        for (int c = 0; c < kCols / 2; ++c) {
+          float lo, hi;
+          split(y[c], lo, hi);
+          if (!((see >> (2 * c)) & 1u)) lo = -INFINITY;
+          if (!((see >> (2 * c + 1)) & 1u)) hi = -INFINITY;
+          y[c] = pair(lo, hi);
         }
       } else if (!__all_sync(0xffffffffu, valid)) {   // every row sees every valid key
         const uint64_t none = pair(-INFINITY, -INFINITY);
@@ -540,25 +564,20 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
       if (__builtin_expect(slow, 0)) {
         // new references: the rows' maxima so far
-        int mine = static_cast<int>(0x80000000);
+        float mine = 0.f;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           float lo, hi;
           split(y[c / 2], lo, hi);
-          int v = __float_as_int(c & 1 ? hi : lo);
-          v ^= (v >> 31) & 0x7fffffff;           // order of floats as order of integers
-          v = __reduce_max_sync(0xffffffffu, v);
+          const float v = redux_max(c & 1 ? hi : lo);
           if (lane == c) mine = v;
         }
         wmax[warp * kCols + lane] = mine;
         wg_sync(wid);
         bool none = false;
         if (tid < kCols) {
-          int v = wmax[tid];
-#pragma unroll
-          for (int w = 1; w < 4; ++w) v = max(v, wmax[w * kCols + tid]);
-          v ^= (v >> 31) & 0x7fffffff;
-          const float top = __int_as_float(v), old = nref[tid];
+          const float top = max_nan(max_nan(wmax[tid], wmax[kCols + tid]), max_nan(wmax[2 * kCols + tid], wmax[3 * kCols + tid]));
+          const float old = nref[tid];
           const bool unset = __float_as_uint(old) == 0x80000000u, empty = unset && top == -INFINITY;
           float sh = unset ? (empty ? 0.f : top) : fmaxf(top, 0.f);
           if (top != top) sh = top;
@@ -667,12 +686,12 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           ls[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
       }
-      wmax[warp * kCols + lane] = __float_as_int(ls[0]);
+      wmax[warp * kCols + lane] = ls[0];
       wg_sync(wid);
       if (tid < kCols) {
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) sum += __int_as_float(wmax[w * kCols + tid]);
+        for (int w = 0; w < 4; ++w) sum += wmax[w * kCols + tid];
         inv_s[tid] = sum == 0.f ? 0.f : 1.f / sum;
         const float m = -nref[tid];
         if (!whole) {
