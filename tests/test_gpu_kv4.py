@@ -353,6 +353,16 @@ def test_attention_large_logits_and_scale(tv, counts, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("counts,kind", [([40, 3], "random"), ([150, 33], "chain"), ([4, 2], "chain"), ([2, 1], "roots")])
+def test_attention_tree_scores_far_above_the_cached_ones(tv, counts, kind, bf16):
+    """Nodes' keys 16 times as long: the running maxima grow in the tree's own tiles, under its masks."""
+    c = Case(20, counts, [300, 64], 8, 2, 128, 32, bf16, kind)
+    c.k, c.hk = c.k * 16, c.hk * 16            # exact
+    out, lse, _ = c.run(tv)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("counts,cnt", [([16, 16, 9], [5, 0, 9]), ([4, 2, 3], [1, 0, 3])])
 def test_attention_node_cnt_leaves_other_rows(tv, counts, cnt, bf16):
     c = Case(8, counts, [100, 300, 64], 8, 2, 128, 32, bf16, "chain", node_cnt=cnt)
@@ -504,6 +514,46 @@ def test_attention_is_the_same_twice_on_another_stream_and_in_a_graph(tv, counts
         c.lens = lens
         c.check(out, lse)
     assert int(err) == 0 and int(ws[0][:4].view(torch.int32)) == 0
+
+
+def test_two_graphs_at_once_with_a_workspace_each(tv):
+    """Replays on two streams: other requests, other rows, one cache."""
+    cs = [Case(21, n, [700, 129], 8, 2, 128, 64, True, "chain") for n in ([30, 9], [4, 1])]
+    runs = []
+    for c in cs:
+        args, kw = c.args(), c.kwargs()
+        want = tv.tree_verify_attn_kv4(*args, **kw)
+        out, lse, err = (torch.zeros_like(t) for t in want)
+        ws = tv.tree_verify_attn_kv4_workspace(2, c.max_nodes, 8, 2, 128)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tv.tree_verify_attn_kv4(*args, **kw, out=out, lse=lse, err=err, ws=ws)
+        runs.append((g, torch.cuda.Stream(), args, kw, want, out, lse, ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s, *_ in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (_, _, _, _, want, out, lse, _) in zip(cs, runs):
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        c.check(out, lse)
+
+
+def test_append_takes_no_more_rows_than_max_new(tv):
+    rng = np.random.default_rng(22)
+    P, H, d = 16, 2, 64
+    table, n_pages = tables(rng, [40, 40], P)
+    off = np.array([0, 9, 12], np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, 12, 2, H, d, True)
+    cache = np.zeros((n_pages, H, P * (d + 4)), np.uint8)
+    c = torch.zeros(cache.shape, dtype=torch.uint8, device="cuda")
+    take = [0, 1, 2, 3, 4, 9, 10, 11]
+    want = ok.append(cache, P, table, [14, 0], hk[take], hv[take], np.array([0, 5, 8]))
+    new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(np.array([14, 0], np.int32)), dev(off), 5)
+    assert int(err) == 1                       # told, and the first five are there
+    assert np.array_equal(host(new_len), want) and np.array_equal(host(c), cache)
 
 
 def test_cache_offsets_pass_32_bits(tv):

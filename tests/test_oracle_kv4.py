@@ -190,7 +190,9 @@ REFUSALS = [
     (attn_call, EINVAL, dict(Hq=5)), (attn_call, EINVAL, dict(scale=0.0)), (attn_call, EINVAL, dict(scale=float("nan"))),
     (attn_call, EINVAL, dict(scale=float("inf"))), (attn_call, EINVAL, dict(words=0)),
     (attn_call, EINVAL, dict(nodes=65)), (attn_call, EINVAL, dict(anc=None)), (attn_call, EINVAL, dict(ldq=256)),
-    (attn_call, EINVAL, dict(ldk=255)), (attn_call, EINVAL, dict(q="odd")), (attn_call, EINVAL, dict(bt=None)),
+    (attn_call, EINVAL, dict(ldk=255)), (attn_call, EINVAL, dict(ldk=1 << 31)), (attn_call, EINVAL, dict(ldv=1 << 40)),
+    (attn_call, EINVAL, dict(dt=2)), (attn_call, EUNSUPPORTED, dict(bt_ld=1 << 28)),
+    (attn_call, EUNSUPPORTED, dict(B=40000)), (attn_call, EINVAL, dict(q="odd")), (attn_call, EINVAL, dict(bt=None)),
     (attn_call, EUNSUPPORTED, dict(page=48)), (attn_call, EUNSUPPORTED, dict(d=96)),
     (attn_call, EUNSUPPORTED, dict(nodes=1025, words=17)), (attn_call, EUNSUPPORTED, dict(Hq=130, Hkv=2, ldq=1 << 16)),
     (attn_call, EWORKSPACE, dict(ws=None)), (attn_call, EWORKSPACE, dict(ws_bytes=16)),
