@@ -363,7 +363,8 @@ def test_attention_tree_scores_far_above_the_cached_ones(tv, counts, kind, bf16)
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("counts,cnt", [([16, 16, 9], [5, 0, 9]), ([4, 2, 3], [1, 0, 3])])
+@pytest.mark.parametrize("counts,cnt", [([16, 16, 9], [5, 0, 9]), ([4, 2, 3], [1, 0, 3]),
+                                        ([110, 60, 9], [5, 0, 9])])
 def test_attention_node_cnt_leaves_other_rows(tv, counts, cnt, bf16):
     c = Case(8, counts, [100, 300, 64], 8, 2, 128, 32, bf16, "chain", node_cnt=cnt)
     n = int(c.off[-1])
@@ -404,7 +405,7 @@ def test_attention_few_rows_that_see_nothing_or_late(tv, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("counts", [[24, 24, 10], [4, 4, 3]])
+@pytest.mark.parametrize("counts", [[24, 24, 10], [4, 4, 3], [110, 24, 10]])
 def test_attention_ignores_whatever_it_does_not_see(tv, counts, bf16):
     """NaN and infinities in tree rows that a node does not see, in rows of other requests, in rows beyond node_cnt,
     and NaN scales behind the end of the cached tokens."""
@@ -432,7 +433,7 @@ def test_attention_ignores_whatever_it_does_not_see(tv, counts, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("counts", [[10, 6], [4, 3]])
+@pytest.mark.parametrize("counts", [[10, 6], [4, 3], [80, 60]])
 def test_attention_nan_and_infinity_reach_exactly_the_rows_that_see_them(tv, counts, bf16):
     n0, n = counts[0], sum(counts)
     c = Case(11, counts, [40, 40], 8, 2, 128, 16, bf16, "chain")
@@ -466,7 +467,7 @@ def test_attention_nan_and_infinity_reach_exactly_the_rows_that_see_them(tv, cou
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("counts", [[5, 5], [2, 1], [4, 4]])
+@pytest.mark.parametrize("counts", [[5, 5], [2, 1], [4, 4], [80, 70]])
 def test_attention_bad_pages_are_not_visible(tv, counts, bf16):
     c = Case(12, counts, [200, 90], 8, 2, 128, 32, bf16)
     c.table[0, 2] = -1
