@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(128) extent_kernel(const AttnArgs a, int nq, i
 // Piece 0 of a cut unit is slot 1 of the run where the unit starts, piece i
 // slot 0 of the i-th run after it.  CTA = (starting run, eight rows), warp =
 // row, lane = D / 32 dims; the pieces are taken in run order, eight loads in
-// flight.  (One CTA for all 64 rows of a run took 12 us instead of JOINUS.)
+// flight.  Bound by the latency of those loads: 11 us for the 304 runs of 64
+// chains of 64 rows, 6 us for the runs of 64 single tokens (cold caches).
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, const Pieces p, int R, int nq) {
   griddep_wait();

@@ -28,12 +28,22 @@
 // both take the softmax of 32 rows each, write P, and PV runs beside the next
 // tile's K.  A unit cut by a run's end leaves fp32 partials that
 // attn_join joins in run order.
-// Measured on 64 chains of 16 nodes x 32 heads over 512..4096 tokens: with
-// dequantising, softmax and MMA issue in warps of their own that hand tiles
-// over through barriers 185 us (most issue slots went to instruction fetches of
-// five kinds of code and to the polls of waiting warps); with one warpgroup
-// doing everything for its tile 203 us (two warps to a scheduler do not fill
-// it); this TEAMUS us.
+//
+// Bound by issue slots and by the serial chain of a tile: 128 tokens cost a
+// team 4400 cycles (700 instructions to each of its 8 warps, 64% of the slots
+// of the two teams), of which the issue of S and of PV, by a lane whose
+// warpgroup waits for it, are 500 each.  64 chains of 16 nodes x 32 heads over
+// 512..4096 tokens 120 us (22% of the measured copy rate counted in the 132
+// bytes per token and head, 17% of the measured matrix rate), 8 requests of
+// 452 rows per KV head over 8192 tokens 312 us (20% of the matrix rate).
+// Tried on the 64 chains: dequantising, softmax and MMA issue in warps of
+// their own that hand tiles over through barriers 185 us (most issue slots
+// went to instruction fetches of five kinds of code and to the polls of
+// waiting warps); one warpgroup doing everything for its tile 203 us (two
+// warps to a scheduler do not fill it); loads and MMA issue moved to two more
+// warps 159 us (112 registers are left to the others, which spill); the words
+// shared out unevenly to spare the issuing warps 148 us (loops in place of
+// straight code).
 //
 // Every wait is bounded (2 s): on expiry the warpgroup records an error code
 // in the workspace status word and stops; tensor memory is always released.

@@ -106,7 +106,8 @@ __device__ __forceinline__ void table_unit(const float* row, int u, int rot, flo
 
 // ------------------------------------------------------------------ rotation
 // CTA = one token; thread = (unit of the row, head lane), so a thread reads
-// its eight (cos, sin) once for all of its heads.
+// its eight (cos, sin) once for all of its heads.  16411 tokens of 40 heads of
+// 128 in bf16: 55 us, 6.2 TB/s (91% of the measured copy rate).
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(256) rope_kernel(const T* __restrict__ q, int64_t ldq, const T* __restrict__ k,
                                                    int64_t ldk, int Hq, int Hkv, int d,
@@ -162,8 +163,10 @@ struct AppendArgs {
 // CTA rewrites the group's words whole, keeping the nibbles of tokens that it
 // does not append.  The heads of a CTA follow one another with the next head's
 // rows on their way: the chain of lengths, tables and positions and the
-// (cos, sin) of the token are paid once for them.  See heads_per_cta for how
-// many, and the measured times.
+// (cos, sin) of the token are paid once for them (see heads_per_cta).  8 prompts
+// of 512..4096 tokens, 8 heads of 128: 27 us for 95 MB in and out, 3.5 TB/s (52%
+// of the measured copy rate); bound by issue slots (66% taken: the maxima, the
+// divisions and the packing of 2 x 128 elements a token and head).
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) {
   constexpr int kUnits = D / 16;
@@ -322,9 +325,10 @@ struct GatherArgs {
 
 // CTA = (16 cache tokens, `heads` KV heads, request), D threads: thread =
 // (tokens tk and tk + 8, 8 dims) for the rows, so that a warp's store is whole
-// rows; V codes pass through shared memory to turn
-// the group's dim-major words into rows.  The heads of a CTA follow one another
-// with the next head's codes on their way.
+// rows; V codes pass through shared memory to turn the group's dim-major words
+// into rows.  The heads of a CTA follow one another with the next head's codes
+// on their way.  64 requests of 512..4096 tokens, 8 heads of 128 to bf16: 118 us,
+// 6.4 TB/s (95% of the measured copy rate).
 template <typename T, int D>
 __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
   constexpr int kUnits = D / 8;
@@ -400,7 +404,9 @@ __global__ void __launch_bounds__(D) gather_kernel(const GatherArgs a) {
 
 // KV heads that a CTA of append and gather takes one after another: all of
 // them while that leaves enough CTAs for every SM, else fewer.
-// (HEADSNOTE)
+// One head to a CTA against all eight: the accepted paths of 64 requests in and
+// back 12.5 against 15.5 us (the rule: 12.5), prompts of 8 requests 68 against 51
+// (51), 64 requests' prefixes back 164 against 121 (121).
 int heads_per_cta(int64_t groups, int Hkv) {
   const int64_t want = 8ll * sm_count();
   int heads = Hkv;
