@@ -506,8 +506,9 @@ int tv_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, i
  *   cache_len int32 [B]: tokens cached before; row j becomes token
  *           cache_len[r] + j.  Not changed by the call.
  * Outputs: the cache blocks of those tokens (other tokens keep their codes);
- *   new_len int32 [B] or NULL: cache_len[r] + rows appended (not the same
- *   array as cache_len).
+ *   new_len int32 [B] or NULL: cache_len[r] + the rows taken, skipped ones
+ *   among them (a token keeps its place); a negative cache_len as it is.  Not
+ *   the same array as cache_len.
  * A row with a bad page entry, a token past the table, a source row outside
  * [0, total_rows) or a position outside [0, max_pos) is skipped, and 1 is
  * written to *err; so is a request with more rows than max_new (the first

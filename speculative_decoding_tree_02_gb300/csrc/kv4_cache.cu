@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
   const bool bad_len = len < 0 || len + static_cast<int64_t>(count) > cap ||
                        (!a.path && a.row_off[r + 1] - base > a.max_new);
   if (blockIdx.x == 0 && h0 == 0 && tid == 0) {
-    if (a.new_len) a.new_len[r] = len + count;
+    if (a.new_len) a.new_len[r] = len < 0 ? len : len + count;
     if (bad_len && (count > 0 || len < 0) && a.err) *a.err = 1;
   }
   if (len < 0) return;

@@ -557,6 +557,18 @@ def test_append_takes_no_more_rows_than_max_new(tv):
     assert np.array_equal(host(new_len), want) and np.array_equal(host(c), cache)
 
 
+def test_append_counts_skipped_rows_and_leaves_negative_lengths(tv):
+    rng = np.random.default_rng(23)
+    P, H, d = 16, 1, 64
+    table = np.array([[0], [7], [1]], np.int32)          # the second request's page is bad
+    (_, k, v), _ = fused(rng, 9, 1, H, d, True)
+    c = torch.zeros((2, H, P * (d + 4)), dtype=torch.uint8, device="cuda")
+    new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(np.array([15, 2, -2], np.int32)),
+                                 dev(np.array([0, 3, 6, 9], np.int32)), 3)
+    assert int(err) == 1 and host(new_len).tolist() == [18, 5, -2]
+    assert (host(c)[1] == 0).all() and (host(c)[0] != 0).any()
+
+
 def test_cache_offsets_pass_32_bits(tv):
     """Pages behind the first 4 GB of the pool."""
     P, H, d = 128, 8, 128
