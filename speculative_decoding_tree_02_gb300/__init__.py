@@ -491,7 +491,7 @@ def _call_on(dev: int, fn: str, *args):
     if dev < 0:
         raise ValueError("libtreeverify takes device tensors")
     f = getattr(_LIB or load_library(), fn)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):

@@ -58,6 +58,5 @@ TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, i
                         anc_words, B, max_nodes, total_nodes, Hq, Hkv, d, dtype, scale};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TV_BF16) return few_rows(max_nodes, Hq, Hkv) ? kv4::attn_mma(a, ws, st) : kv4::attn_tc(a, ws, st);
-  if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return TV_ECUDA;
-  return kv4::attn_simt(a, st);
+  return kv4::attn_simt(a, ws, st);
 }

@@ -17,7 +17,7 @@ namespace tv {
 namespace kv4 {
 
 template <int D, int R>
-__global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a, int* status) {
   constexpr int kDl = D / 32;            // dims per lane of the value product
   __shared__ __align__(16) float sq[R][D];
   __shared__ __align__(16) float sp_w[4][32][R];   // a warp's weights
@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
   __shared__ float2 sml[4][R];
   griddep_wait();
   griddep_release();
+  if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *status = 0;   // (nothing waits here)
   const int r = blockIdx.z, h = blockIdx.y, g = a.Hq / a.Hkv;
   const Span sp = node_span(a, r);
   const int row0 = blockIdx.x * R, rows = min(R, sp.cnt * g - row0);   // row = node g + head of the group
@@ -229,18 +230,18 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
 }
 
 template <int D, int R>
-int launch(const AttnArgs& a, cudaStream_t st) {
+int launch(const AttnArgs& a, void* ws, cudaStream_t st) {
   const dim3 grid((a.max_nodes * (a.Hq / a.Hkv) + R - 1) / R, a.Hkv, a.B);
-  return launch_pdl(attn_simt_kernel<D, R>, grid, dim3(128), 0, st, a);
+  return launch_pdl(attn_simt_kernel<D, R>, grid, dim3(128), 0, st, a, static_cast<int*>(ws));
 }
 
-int attn_simt(const AttnArgs& a, cudaStream_t st) {
+int attn_simt(const AttnArgs& a, void* ws, cudaStream_t st) {
   // Eight rows to a CTA once that gives every SM one, else one row: 256 CTAs of eight 74 us against 114 with a row
   // each (64 nodes x 32 heads of 128, 1000 tokens), 1024 of them 73 against 123 (64 heads of 64); 128 of them 45
   // against 41, 32 of them 64 against 27.
   const int64_t groups = static_cast<int64_t>((a.max_nodes * (a.Hq / a.Hkv) + 7) / 8) * a.Hkv * a.B;
-  if (groups >= sm_count()) return a.d == 128 ? launch<128, 8>(a, st) : launch<64, 8>(a, st);
-  return a.d == 128 ? launch<128, 1>(a, st) : launch<64, 1>(a, st);
+  if (groups >= sm_count()) return a.d == 128 ? launch<128, 8>(a, ws, st) : launch<64, 8>(a, ws, st);
+  return a.d == 128 ? launch<128, 1>(a, ws, st) : launch<64, 1>(a, ws, st);
 }
 
 }  // namespace kv4

@@ -124,7 +124,7 @@ __device__ __forceinline__ int prefix_len(const AttnArgs& a, int r) {
   return len;
 }
 
-int attn_simt(const AttnArgs& a, cudaStream_t st);            // fp32 rows
+int attn_simt(const AttnArgs& a, void* ws, cudaStream_t st);            // fp32 rows
 int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st);   // bf16, at most 16 rows per KV head
 int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st);    // bf16
 size_t attn_mma_workspace(int B, int max_nodes, int Hq, int Hkv, int d);
