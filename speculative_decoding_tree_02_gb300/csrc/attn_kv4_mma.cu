@@ -21,14 +21,14 @@
 // (measured) take 256 of the 720 cycles that 128 tokens take at the measured
 // copy rate, and there is no hand-over between warps to wait for.
 //
-// The list of all units (request, KV head), in chunks, is cut into equal runs,
-// one per warp; a unit that a run's end cuts leaves fp32 partials that
+// The list of all units (request, KV head), in chunks, is cut into runs of equal
+// cost, one per warp; a unit that a run's end cuts leaves fp32 partials that
 // attn_join joins in run order.
 //
 // Bound by issue slots: 1400 instructions to a warp and chunk for 8 rows, 56%
 // of the slots taken, with the three warps per scheduler that 160 registers
 // leave.  64 requests of 32 heads of 128 over 512..4096 tokens: one token each
-// 51 us (3.1 TB/s, 45% of the measured copy rate), 16 rows per KV head 79 us.
+// 50 us (3.1 TB/s, 46% of the measured copy rate), 16 rows per KV head 76 us.
 // One request over 2048 tokens 13 us + 6 us of joining.
 #include <algorithm>
 
@@ -40,6 +40,9 @@ namespace kv4 {
 namespace {
 
 constexpr int kChunk = 64;     // tokens per chunk
+// What a unit costs beside its chunks, in chunks: 64 single tokens 51.5 us without it, 50.4 at 1, 51.9 at 2, 53 at 3;
+// 16 rows per KV head 79, 76, 73, 75.
+constexpr int kUnitCost = 1;
 
 template <int D, int NB>
 struct Lay {
@@ -112,15 +115,16 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   griddep_release();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // an expired wait writes it seconds later
 
-  // ---- this warp's run: chunks [w0, w1) of the list of all units
+  // ---- this warp's run: [w0, w1) of the list of all units, each kUnitCost places and then its chunks
   const int per = ((a.B + L::kWarps - 1) / L::kWarps + 31) / 32 * 32;   // entries (requests) per warp
-  auto chunks = [&](int e, int end) {
-    return e < end ? static_cast<long long>(unit_of(p, e).nb) * a.Hkv : 0ll;
+  auto cost_of = [&](int e, int end) {
+    const int nb = e < end ? unit_of(p, e).nb : 0;
+    return nb ? static_cast<long long>(nb + kUnitCost) * a.Hkv : 0ll;
   };
   {
     const int lo = min(warp * per, a.B), hi = min(lo + per, a.B);
     long long s = 0;
-    for (int e = lo; e < hi; e += 32) s += chunks(e + lane, hi);
+    for (int e = lo; e < hi; e += 32) s += cost_of(e + lane, hi);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) sums[warp] = s;
@@ -135,13 +139,13 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   if (worker >= G) return;
   const long long w0 = worker * W / G, w1 = (worker + 1) * W / G;
   int e = 0;
-  long long before = 0;                          // chunks before entry e
+  long long before = 0;                          // places before entry e
   {
     int w = 0;
     while (before + sums[w] <= w0) before += sums[w++];
     const int hi = min(w * per + per, a.B);
     for (e = w * per;; e += 32) {
-      const long long c = chunks(e + lane, hi);
+      const long long c = cost_of(e + lane, hi);
       long long x = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -159,8 +163,10 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     }
   }
   Unit u = unit_of(p, e);
-  const int skip = static_cast<int>(w0 - before);
-  int h = skip / u.nb, blk = skip % u.nb;
+  const int skip = static_cast<int>(w0 - before), at = skip % (u.nb + kUnitCost);
+  int h = skip / (u.nb + kUnitCost), blk = max(0, at - kUnitCost);
+  int left = static_cast<int>(w1 - w0) + at;     // places from the start of the unit to the end of the run
+  // (a chunk is in the run while kUnitCost + its index < left)
 
   // ---- the loads run two chunks ahead, their page numbers three
   const int P = a.page_size, Pe = min(P, kChunk), shift = 31 - __clz(Pe);
@@ -175,26 +181,27 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   const int page_shift = 31 - __clz(P);
   int le = e, lh = h, lblk = blk, lpage = -1;    // next chunk to load, this lane's page of it
   Unit lu = u;
-  const int n = static_cast<int>(w1 - w0);       // chunks of the run
-  int lnext = 0;                                 // chunks loaded
+  int lleft = left, lnext = 0;                                 // chunks loaded
   auto look = [&]() {                            // the page numbers of the next chunk to load
     lpage = -1;
-    if (lnext >= n) return;
     if (lblk == lu.nb) {
       lblk = 0;
+      lleft -= lu.nb + kUnitCost;
+      if (kUnitCost >= lleft) return;
       if (++lh == a.Hkv) {
         lh = 0;
         do lu = unit_of(p, ++le);
         while (lu.nb == 0 && le + 1 < a.B);
       }
     }
+    if (kUnitCost + lblk >= lleft) return;
     const int key = lblk * kChunk + (P > kChunk ? 0 : lane << shift);
     if (lblk < lu.np && (P > kChunk ? lane <= kC + 2 : lane < kChunk >> shift) && key < lu.len)
       lpage = a.block_table[static_cast<int64_t>(le) * a.table_ld + (key >> page_shift)];
   };
   unsigned good = 0u;                            // staged pages of the two stages, 8 bits each
   auto load = [&](int st) {
-    if (lnext >= n) return;
+    if (kUnitCost + lblk >= lleft) return;
     const bool wanted = lpage != -1;
     const bool ok = wanted && lpage >= 0 && lpage < a.n_pages;
     // a lane that wants no page has -1 too: entries of -1 are told by the token they should hold
@@ -242,10 +249,11 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   for (int it = -2;;) {
     load(it & 1);                                // the chunk after next (before the first chunk: the first two)
     look();
-    if (++it == n) break;
-    if (it < 0) continue;
+    if (++it < 0) continue;
     const int st = it & 1;
     if (blk == u.nb) {                           // next unit
+      left -= u.nb + kUnitCost;
+      if (kUnitCost >= left) break;
       blk = seg_blk = 0;
       fresh = true;
       if (++h == a.Hkv) {
@@ -254,6 +262,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
         while (u.nb == 0 && e + 1 < a.B);
       }
     }
+    if (kUnitCost + blk >= left) break;
     if (fresh) {
       fresh = false;
       const Span sp = node_span(a, e);
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     }
 
     __syncwarp();                                // the stage was read
-    if (blk != u.nb - 1 && it != n - 1) {
+    if (blk != u.nb - 1 && kUnitCost + blk + 1 < left) {
       ++blk;
       continue;
     }
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
     const bool whole = seg_blk == 0 && blk == u.nb - 1;
     const int64_t slot = 2 * worker + (seg_blk == 0 ? 1 : 0);
     if (seg_blk == 0 && blk != u.nb - 1 && lane == 0) {
-      const long long u1 = w0 + it + (u.nb - blk);        // position after the unit
+      const long long u1 = w1 - left + kUnitCost + u.nb;  // place after the unit
       const long long k = (u1 * G + W - 1) / W - 1;       // run of its last chunk
       p.pieces.desc[worker] = make_int4(static_cast<int>(k) - worker + 1, e, 0, h);
     }

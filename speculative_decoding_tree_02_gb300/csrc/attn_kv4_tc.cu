@@ -23,7 +23,8 @@
 // A CTA is two teams of two warpgroups that share nothing but the SM: each
 // team walks its own run of the list of all units (request, row tile, KV head;
 // a unit's tiles of 128 cached tokens, then of 128 nodes, follow one another),
-// so that one dequantises while the other takes its softmax.  In a team each
+// so that one dequantises while the other takes its softmax; runs are of equal
+// cost (kUnitCost).  In a team each
 // warpgroup writes half of K's columns, then, beside S, half of V^T's; then
 // both take the softmax of 32 rows each, write P, and PV runs beside the next
 // tile's K.  A unit cut by a run's end leaves fp32 partials that
@@ -33,10 +34,10 @@
 // team 4400 cycles (700 instructions to each of its 8 warps, 64% of the slots
 // of the two teams), of which the issue of S and of PV, by a lane whose
 // warpgroup waits for it, are 500 each.  64 chains of 16 nodes x 32 heads over
-// 512..4096 tokens 120 us (22% of the measured copy rate counted in the 132
-// bytes per token and head, 17% of the measured matrix rate), 8 requests of
-// 452 rows per KV head over 8192 tokens 312 us (20% of the matrix rate).
-// Tried on the 64 chains: dequantising, softmax and MMA issue in warps of
+// 512..4096 tokens 105 us (25% of the measured copy rate counted in the 132
+// bytes per token and head, 19% of the measured matrix rate), 8 requests of
+// 452 rows per KV head over 8192 tokens 309 us (20% of the matrix rate).
+// Tried on the 64 chains, against 120..154 us of the teams at those times: dequantising, softmax and MMA issue in warps of
 // their own that hand tiles over through barriers 185 us (most issue slots
 // went to instruction fetches of five kinds of code and to the polls of
 // waiting warps); one warpgroup doing everything for its tile 203 us (two
