@@ -11,8 +11,8 @@ bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
 }
 // Which bf16 kernel: the warps' own mma.sync up to 16 rows per KV head, the
 // tcgen05 tiles above. 64 requests over 512..4096 tokens, 1 over 2048 and 8 over
-// 8192 of 8 KV heads of 128, mma.sync against tcgen05: 4 rows 54/17/35 against
-// 100/17/50 us, 16 rows 76/19/41 against 103/17/52, 32 rows (with twice the
+// 8192 of 8 KV heads of 128, mma.sync against tcgen05: 4 rows 54/15/35 against
+// 100/17/50 us, 16 rows 76/18/41 against 103/17/52, 32 rows (with twice the
 // accumulators) 152/39/72 against 105/19/53.
 bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 16; }
 }  // namespace

@@ -29,7 +29,7 @@
 // of the slots taken, with the three warps per scheduler that 160 registers
 // leave.  64 requests of 32 heads of 128 over 512..4096 tokens: one token each
 // 50 us (3.1 TB/s, 46% of the measured copy rate), 16 rows per KV head 76 us.
-// One request over 2048 tokens 13 us + 6 us of joining.
+// One request over 2048 tokens 14.5 us with its joining.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -132,8 +132,10 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   __syncthreads();
   long long W = 0;
   for (int w = 0; w < L::kWarps; ++w) W += sums[w];
-  // at least two chunks to a run: a shorter one costs more to join than to do
-  const long long G = min(static_cast<long long>(p.workers), (W + 1) / 2);
+  // Runs of one place while two warps to an SM take them all (one request over 2048 tokens 14.5 us, with two places
+  // 16.5), else of two at least (one request over 8192 tokens 20.5 us, with one place 24.5: its units' many pieces are
+  // joined one after another; 16 rows, 16 requests over 500 tokens 20.6 and 22.7).
+  const long long G = min(static_cast<long long>(p.workers), max((W + 1) / 2, min(W, 2ll * gridDim.x)));
   const int worker = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp;   // neighbours on other SMs
   if (lane == 0) p.pieces.desc[worker] = make_int4(0, 0, 0, 0);
   if (worker >= G) return;
