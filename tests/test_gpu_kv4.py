@@ -517,6 +517,15 @@ def test_attention_is_the_same_twice_on_another_stream_and_in_a_graph(tv, counts
     assert int(err) == 0 and int(ws[0][:4].view(torch.int32)) == 0
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("counts,lens", [([1], [40000]), ([20], [40000]), ([1, 2, 1], [1, 30000, 17])])
+def test_attention_one_long_prefix_among_short_ones(tv, counts, lens, bf16):
+    """Units cut into hundreds of pieces beside units of a tile."""
+    c = Case(24, counts, lens, 4, 1, 128, 128, bf16)
+    out, lse, _ = c.run(tv)
+    c.check(out, lse)
+
+
 def test_two_graphs_at_once_with_a_workspace_each(tv):
     """Replays on two streams: other requests, other rows, one cache."""
     cs = [Case(21, n, [700, 129], 8, 2, 128, 64, True, "chain") for n in ([30, 9], [4, 1])]
