@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     const int inv_g = 65536 / g + 1;             // row / g = row inv_g / 2^16 for the 64 rows and g <= 64
     auto node_of = [&](int row) { return row * inv_g >> 16; };
     const float c2 = a.scale * kLog2e;
-    // a row's reference (what its scores are taken over) is kept negated; -0: none yet
+    // a row's reference (what its scores are taken over) is kept negated; 0 while it has none
     float* nref = reinterpret_cast<float*>(sm + L::kRef) + c0;
     float* shift_s = reinterpret_cast<float*>(sm + L::kShift) + c0;
     float* corr_s = reinterpret_cast<float*>(sm + L::kCorr) + c0;
@@ -349,6 +349,9 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     volatile int* dirty = reinterpret_cast<volatile int*>(sm + L::kPages + 32);   // non-finite tree values met
     volatile int* low_vis = reinterpret_cast<volatile int*>(sm + L::kPages + 36);  // [2] prefix that all rows see
     bool force = false, fresh = true;            // a row without reference; a new unit
+    // Threads 0 .. 31 of a warpgroup: row c0 + tid has no reference yet. Kept apart from its value: any number can be one
+    // (a row of zeros has the reference 0).
+    bool unset = true;
     int seg_blk = blk, unit_e = -1, r = 0, t = 0, n0 = 0, cnt = 0;
     int st = 0, turn = 0, it = 0;
     for (;; ++it) {
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (tid < kCols) {
           const int rr = c0 + tid, gn = n0 + node0 + node_of(rr);
-          nref[tid] = -0.f;
+          nref[tid] = 0.f;
           row_s[tid] = rr < rows ? gn * a.Hq + h * g + rr - node_of(rr) * g : -1;
           const int vis = rr < rows ? (a.vis_prefix ? a.vis_prefix[gn] : 0x7fffffff) : 0;
           vis_s[tid] = vis;
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
           if (tid == 0) low_vis[half] = lowest;
         }
         force = false;
+        unset = true;
         if (tid == 0 && half == 0) *dirty = 0;
         team_sync(tbar);
       }
@@ -601,13 +605,14 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         if (tid < kCols) {
           const float top = max_nan(max_nan(wmax[tid], wmax[kCols + tid]), max_nan(wmax[2 * kCols + tid], wmax[3 * kCols + tid]));
           const float old = nref[tid];
-          const bool unset = __float_as_uint(old) == 0x80000000u, empty = unset && top == -INFINITY;
+          const bool empty = unset && top == -INFINITY;
           float sh = unset ? (empty ? 0.f : top) : fmaxf(top, 0.f);
           if (top != top) sh = top;
-          nref[tid] = empty ? -0.f : old - sh;
+          nref[tid] = old - sh;                  // (none: old = 0, and sh = 0 if the row is still empty)
           none = row_s[tid] >= 0 && empty;
           corr_s[tid] = unset ? 0.f : ex2(-sh);
           shift_s[tid] = -sh;
+          unset = empty;
         }
         force = any_of<128>(wid, none);
 #pragma unroll

@@ -622,6 +622,92 @@ def test_gathered_prefix_feeds_the_contiguous_attention(tv):
     assert (np.abs(host(lse) - host(l2)) <= 2.0 ** -8 * sa + 1e-4).all()
 
 
+# -------------------------------------------------- rows whose maximum is zero
+def scale_keys(c, r, tokens, factor):
+    """Multiplies the cached keys of these tokens by a power of two; 0: zero rows as kv4_append leaves them."""
+    _, kn, ks, _, _ = c.pool
+    pg, sl = c.table[r, tokens // c.P], tokens % c.P
+    heads = np.arange(ks.shape[1])
+    if factor:
+        ks[pg, :, sl] *= np.float32(factor)
+    else:
+        kn[pg, :, sl], ks[pg, :, sl] = 0, ok.SCALE_MIN
+        byte = ok._k_at(c.P, sl[:, None], np.arange(c.d))[0]
+        c.cache[pg[:, None, None], heads[:, None], byte[:, None]] = 0x88
+    b = ok.bf16_bits(ks[pg, :, sl])
+    at = (c.P * c.d + 2 * sl)[:, None]
+    c.cache[pg[:, None], heads, at] = b & 255
+    c.cache[pg[:, None], heads, at + 1] = b >> 8
+
+
+def zero_queries(c, nodes, heads):
+    c.q[nodes], c.hq[nodes] = 0, 0
+    c.q[:, heads], c.hq[:, heads] = 0, 0
+
+
+ZERO_ROWS = [([20, 9], [400, 300]), ([40], [260]), ([4, 2], [400, 300]), ([2], [260]),   # row tiles of 64; few rows
+             ([20] * 64, list(range(257, 385, 2)))]      # several tiles of a unit in one run
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("vis", [False, True])
+@pytest.mark.parametrize("counts,lens", ZERO_ROWS)
+def test_attention_zero_queries_among_growing_rows(tv, counts, lens, vis, d, bf16):
+    """Queries of zeros (padded nodes, a head of zeros): their scores are zero throughout, while the other rows' maxima
+    grow in a later tile of keys and in the tree.  With prefixes per node, one row of the tile sees no prefix."""
+    c = Case(30, counts, lens, 8, 2, d, 64, bf16, "chain", vis=vis)
+    zero_queries(c, [1, counts[0] - 1], [3])
+    for r, n in enumerate(lens):
+        scale_keys(c, r, np.arange(128, n), 16)
+    c.k, c.hk = c.k * 64, c.hk * 64            # exact
+    if vis:
+        c.vis[:] = np.repeat(lens, counts)
+        c.vis[0] = 0
+    out, lse, err = c.run(tv)
+    assert int(err) == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("vis", [False, True])
+@pytest.mark.parametrize("factor", [2, 16])
+@pytest.mark.parametrize("counts,lens", ZERO_ROWS)
+def test_attention_zero_keys_before_larger_scores(tv, counts, lens, factor, vis, d, bf16):
+    """128 cached keys of zeros (padding that was appended), then keys whose scores are somewhat or far above."""
+    c = Case(31, counts, lens, 8, 2, d, 32, bf16, "roots", vis=vis)
+    for r, n in enumerate(lens):
+        scale_keys(c, r, np.arange(128), 0)
+        scale_keys(c, r, np.arange(128, n), factor)
+    if vis:
+        c.vis[:] = np.repeat(lens, counts)
+        c.vis[counts[0] // 2] = 130
+    out, lse, err = c.run(tv)
+    assert int(err) == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("vis", [False, True])
+@pytest.mark.parametrize("counts,d", [([20] * 8, 128), ([20] * 8, 64), ([4] * 24, 128)])
+def test_attention_zero_rows_in_units_that_are_cut(tv, counts, d, vis):
+    """The same in units that several runs share, a run having a few tiles of each."""
+    n = 4000
+    c = Case(32, counts, [n] * len(counts), 8, 2, d, 128, True, "chain", vis=vis)
+    zero_queries(c, [3, sum(counts) - 1], [5])
+    for r in range(len(counts)):
+        if r % 2:
+            scale_keys(c, r, np.arange(128), 0)
+        t = np.arange(128, n)
+        scale_keys(c, r, t[t // 128 % 3 == 1], 4)       # every third tile above the one before it
+    if vis:
+        c.vis[:] = n
+        c.vis[1] = 0
+    out, lse, err = c.run(tv)
+    assert int(err) == 0
+    c.check(out, lse)
+
+
 # ------------------------------------------------------------ a run together
 @pytest.mark.parametrize("Hq,Hkv,d,P", [(8, 2, 128, 16), (4, 1, 64, 32)])
 def test_prompt_then_verification_steps(tv, Hq, Hkv, d, P):
