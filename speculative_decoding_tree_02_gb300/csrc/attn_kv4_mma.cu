@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
           for (int k = 0; k < 4; ++k) o[d][i][k] = 0.f;
       __syncwarp();
     }
+    // (a warp may leave by itself: no barrier of the CTA follows)
     if (!warp_wait(bars + 8 * st, (it >> 1) & 1, abort_flag, p.status, 61)) break;
     const uint8_t* stage = mine + st * L::kStage;
     const bool tree = blk == u.np;
@@ -643,11 +644,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   }
   // after an expired wait: copies in flight land before the CTA ends
   if (*abort_flag) {
-    for (int it = max(0, lnext - 2); it < lnext; ++it) {
-      const long long t0 = clock64();
-      while (!tc::mbar_try(bars + 8 * (it & 1), (it >> 1) & 1) && clock64() - t0 < kWaitClocks) {
-      }
-    }
+    for (int it = max(0, lnext - 2); it < lnext; ++it) drain(bars + 8 * (it & 1), (it >> 1) & 1);
   }
 }
 

@@ -46,8 +46,13 @@
 // shared out unevenly to spare the issuing warps 148 us (loops in place of
 // straight code).
 //
-// Every wait is bounded (2 s): on expiry the warpgroup records an error code
-// in the workspace status word and stops; tensor memory is always released.
+// Every wait is bounded (2 s). A warp whose wait expires records an error code
+// in the workspace status word, raises its team's abort flag and goes on with
+// whatever is there (addresses follow from the lengths and tables alone, so
+// all accesses stay in bounds) up to the team's vote before PV, which sends the
+// whole team out of the loop at once: no barrier ever counts a warp that has
+// left. The team then waits, bounded again, for its MMAs and copies in flight;
+// tensor memory is always released.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -81,10 +86,10 @@ struct Lay {
   static constexpr uint32_t kVis = kInv + 256;                // int [64]
   static constexpr uint32_t kRow = kVis + 256;                // int [64] output row, -1: none
   static constexpr uint32_t kWarpMax = kRow + 256;            // float [2][4][32]
-  static constexpr uint32_t kPages = kWarpMax + 1024;         // u8 [kStages][8] page i of the tile is staged; dirty, low_vis
-  static constexpr uint32_t kBars = kPages + 48;              // RAW [kStages], S, PV, DRAIN
+  static constexpr uint32_t kPages = kWarpMax + 1024;         // u8 [kStages][8] page i of the tile is staged; dirty, low_vis, abort flag
+  static constexpr uint32_t kBars = kPages + 48;              // RAW [kStages], S, PV
   static constexpr uint32_t kTeam = (kBars + 64 + 1023) / 1024 * 1024;    // bytes of a team
-  static constexpr uint32_t kMisc = 2 * kTeam;                // tensor memory address, abort flag, entry sums
+  static constexpr uint32_t kMisc = 2 * kTeam;                // tensor memory address, entry sums
   static constexpr uint32_t kBytes = kMisc + 192 + 1024;      // + alignment slack
   static_assert(kBytes <= 232448, "shared memory");
   // tensor memory of a team (256 columns): K, V, S, O
@@ -142,6 +147,17 @@ __device__ __forceinline__ bool any_of(int id, bool p) {
   return r != 0;
 }
 
+// By a whole warp: until the phase is over or the wait has expired, which the abort flag then tells; the warp goes on
+// either way. The slow part is a call, so that the tile's registers need not meet its own (in line: 3% slower).
+__device__ __noinline__ void slow_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  bounded_wait(bar, parity, abort_flag, err, code);
+}
+__device__ __forceinline__ void team_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_test(bar, parity)), 1)) return;
+  slow_wait(bar, parity, abort_flag, err, code);
+  __syncwarp();
+}
+
 // Key tiles of an entry (request x row tile): prefix tiles over the tokens
 // that any of its rows sees, then tree tiles from the lowest visible node on.
 struct Extent {
@@ -176,16 +192,15 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   uint8_t* sm = sm0 + team * L::kTeam;
   const uint32_t sb = smem_u32(sm);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm0 + L::kMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm0 + L::kMisc + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kPages + 44);
   long long* sums = reinterpret_cast<long long*>(sm0 + L::kMisc + 16);
   auto raw_bar = [&](int st) { return sb + L::kBars + 8u * st; };
-  const uint32_t s_bar = sb + L::kBars + 8 * kStages, pv_bar = s_bar + 8, drain_bar = s_bar + 16;
+  const uint32_t s_bar = sb + L::kBars + 8 * kStages, pv_bar = s_bar + 8;
   const uint32_t blk_bytes = static_cast<uint32_t>(a.page_size) * (D + 4);
   const int ps_shift = 31 - __clz(a.page_size), per_tile = kKeys >> ps_shift;
   if (tid == 0 && half == 0) {
-    for (int i = 0; i < kStages + 3; ++i)
-      mbar_init(sb + L::kBars + 8 * i, i < kStages ? per_tile : i == kStages + 2 ? 2 : 1);
-    if (team == 0) *abort_flag = 0;
+    for (int i = 0; i < kStages + 2; ++i) mbar_init(sb + L::kBars + 8 * i, i < kStages ? per_tile : 1);
+    *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   griddep_wait();
@@ -352,6 +367,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
     // Threads 0 .. 31 of a warpgroup: row c0 + tid has no reference yet. Kept apart from its value: any number can be one
     // (a row of zeros has the reference 0).
     bool unset = true;
+    bool aborted = false;                        // the team's vote ended the loop
     int seg_blk = blk, unit_e = -1, r = 0, t = 0, n0 = 0, cnt = 0;
     int st = 0, turn = 0, it = 0;
     for (;; ++it) {
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       const bool tree = blk >= x.np, last = blk == x.nb - 1 || kUnitCost + blk + 1 >= left;
       const int key0 = (tree ? x.t0 + blk - x.np : blk) * kKeys;
       const int nkeys = min(kKeys, (tree ? cnt : x.len) - key0);
-      if (!warp_wait(raw_bar(st), turn, abort_flag, p.status, 41)) break;
+      team_wait(raw_bar(st), turn, abort_flag, p.status, 41);
       const uint8_t* raw = sm + L::kRaw + st * L::kStage;
 
       // ---- K: thread = key, half of the dims
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       __syncwarp();
 
       // ---- V^T: thread = dim, half of the tokens, once PV of the tile before has read the last one
-      if (it > 0 && !warp_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 42)) break;
+      if (it > 0) team_wait(pv_bar, (it - 1) & 1, abort_flag, p.status, 42);
       tc_fence_after();
       if (32 * warp < D) {                       // d = 64: the upper lanes' results are not used
         if (!tree) {
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
 
       // ---- softmax: thread = key; scores in base-2 units over the rows' references, two rows to a register pair
-      if (!warp_wait(s_bar, it & 1, abort_flag, p.status, 43)) break;
+      team_wait(s_bar, it & 1, abort_flag, p.status, 43);
       tc_fence_after();
       uint64_t y[kCols / 2];
       for (bool slow = first || force;;) {
@@ -670,10 +686,14 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
-      // a score beyond a reference by 2^8: the same again over new references
-      slow = any_of<256>(tbar, !slow && fmaxf(mx[0], mx[1]) > 8.f);
+      // a score beyond a reference by 2^8: the same again over new references; a wait that expired: out of the loop
+      slow = any_of<256>(tbar, *abort_flag != 0 || (!slow && fmaxf(mx[0], mx[1]) > 8.f));
       if (__builtin_expect(!slow, 1)) break;
+      // The same for all threads: whoever raised it did so before the vote, there being no wait between two votes.
+      aborted = *abort_flag != 0;
+      if (aborted) break;
       }
+      if (__builtin_expect(aborted, 0)) break;
       if (half == 1 && warp == 0 && elect()) {
         tc_fence_after();
         constexpr uint32_t idO = idesc_bf16(128, kRowsT, 1);
@@ -729,7 +749,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
         }
       }
       wg_sync(wid);
-      if (!warp_wait(pv_bar, it & 1, abort_flag, p.status, 44)) break;
+      team_wait(pv_bar, it & 1, abort_flag, p.status, 44);   // (expired: the next tile waits for the same phase)
       tc_fence_after();
       if (32 * warp < D) {
 #pragma unroll 1
@@ -781,18 +801,16 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
       tc_fence_before();
       team_sync(tbar);                           // all have read O and the rows' arrays: the next unit may begin
     }
-    // every MMA issued has completed, and after an expired wait every copy has landed, before the CTA ends
-    if (tid == 0) {
-      umma_commit(drain_bar);
-      bounded_wait(drain_bar, 0, abort_flag, p.status, 45);
-    }
-    __syncwarp();
-    if (loader && *abort_flag)
-      for (int i = max(0, lnext - kStages); i < lnext; ++i) {
-        const long long t0 = clock64();
-        while (!mbar_try(raw_bar(i % kStages), (i / kStages) & 1) && clock64() - t0 < kWaitClocks) {
-        }
+    // All that was issued has been waited for, but after an expired wait: then PV of the tile before, S of the tile whose
+    // vote ended the loop, and the copies of the staged tiles may be in flight still, and end before the CTA does.
+    if (*abort_flag) {
+      if (tid == 0) {
+        if (it > 0) drain(pv_bar, (it - 1) & 1);
+        if (aborted) drain(s_bar, it & 1);
       }
+      if (loader)
+        for (int i = max(0, lnext - kStages); i < lnext; ++i) drain(raw_bar(i % kStages), (i / kStages) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -98,6 +98,13 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
   atomicExch(err, code);
   return false;
 }
+// For work in flight when a kernel ends: until it is done, at most kWaitClocks, whatever became of other waits.
+__device__ __forceinline__ bool drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!tc::mbar_try(bar, parity))
+    if (clock64() - t0 > kWaitClocks) return false;
+  return true;
+}
 // By a whole warp: true when the phase is over, the same in all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
   if (__builtin_expect(__all_sync(0xffffffffu, tc::mbar_test(bar, parity)), 1)) return true;

@@ -246,3 +246,16 @@ def test_binding_refuses_wrong_tensors(tv):
         tv.tree_verify_attn_kv4(q, cache, 16, i32(1, 2), i32(1), row, row, i32(2),
                                 torch.zeros((4, 1), dtype=torch.int64), 4, err=i32(1), ws=torch.zeros(1 << 20,
                                                                                                  dtype=torch.uint8))
+
+
+def test_no_warp_of_a_team_leaves_its_loop_at_a_wait():
+    """The barriers of the tcgen05 kernel count all threads of a team, so a wait that expires must not take its warp
+    out of the loop: it is noted, and the team's vote before PV sends all of it out.  (Read from the source: a wait
+    that expires is not provoked on a GPU.)"""
+    import re
+    src = open(os.path.join(os.path.dirname(LIB), "csrc", "attn_kv4_tc.cu")).read()
+    body = src[src.index("attn_kernel(const __grid_constant__"):]
+    waits = re.findall(r"^.*wait\w*\(.*abort_flag.*$", body, re.M)
+    assert len(waits) == 4 and all(re.match(r"\s*(if \(it > 0\) )?team_wait\([^;]*\);(\s*//.*)?$", w) for w in waits)
+    assert "void team_wait(" in src                           # nothing to branch on
+    assert "slow = any_of<256>(tbar, *abort_flag != 0 ||" in body and "if (__builtin_expect(aborted, 0)) break;" in body
