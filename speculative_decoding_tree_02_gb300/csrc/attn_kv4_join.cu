@@ -1,6 +1,8 @@
 // tree_verify_attn_kv4: what the two tensor-core kernels share on the side —
 // the extents of row tiles whose keys do not follow from the lengths alone,
-// and the joining of units that were cut.
+// the joining of units that were cut, and the report of an expired wait.
+#include <cstdlib>
+
 #include "kv4_device.cuh"
 
 namespace tv {
@@ -43,16 +45,35 @@ __global__ void __launch_bounds__(128) extent_kernel(const AttnArgs a, int nq, i
   if (lane == 0) out[e] = make_int4(live ? vis : 0, t0, nt, 0);
 }
 
+// A wait ran out: units are missing, so every row of the call reports it, not what the memory held.
+template <int D>
+__device__ __noinline__ void fail_rows(const AttnArgs& a) {
+  const int ctas = static_cast<int>(gridDim.x * gridDim.y), cta = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);
+  if (cta == 0 && threadIdx.x == 0 && a.err) *a.err = 1;
+  for (int r = cta; r < a.B; r += ctas) {
+    const Span s = node_span(a, r);
+    const int64_t row0 = static_cast<int64_t>(s.n0) * a.Hq, rows = static_cast<int64_t>(s.cnt) * a.Hq;
+    for (int64_t i = threadIdx.x; i < rows * D; i += blockDim.x) static_cast<uint16_t*>(a.out)[row0 * D + i] = 0x7fc0;
+    if (a.lse)
+      for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) a.lse[row0 + i] = __uint_as_float(0x7fc00000u);
+  }
+}
+
 // Piece 0 of a cut unit is slot 1 of the run where the unit starts, piece i
 // slot 0 of the i-th run after it.  CTA = (starting run, eight rows), warp =
 // row, lane = D / 32 dims; the pieces are taken in run order, eight loads in
 // flight.  Bound by the latency of those loads: 11 us for the 304 runs of 64
 // chains of 64 rows, 6 us for the runs of 64 single tokens (cold caches).
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, const Pieces p, int R, int nq) {
+__global__ void __launch_bounds__(256, 4) join_kernel(const AttnArgs a, const Pieces p, const int* status, int R,
+                                                   int nq) {
   griddep_wait();
   griddep_release();
   const int4 d = p.desc[blockIdx.x];             // pieces, request, row tile, KV head
+  if (__builtin_expect(*status != 0, 0)) {
+    fail_rows<D>(a);
+    return;
+  }
   if (d.x < 2) return;
   const int g = a.Hq / a.Hkv, lane = threadIdx.x & 31;
   const Span s = node_span(a, d.y);
@@ -109,9 +130,17 @@ int attn_extents(const AttnArgs& a, int nq, int tiles, int4* out, cudaStream_t s
   return launch_pdl(extent_kernel, dim3((a.B * tiles + 3) / 4), dim3(128), 0, st, a, nq, tiles, out);
 }
 
-int attn_join(const AttnArgs& a, const Pieces& p, int runs, int R, int nq, cudaStream_t st) {
-  return a.d == 128 ? launch_pdl(join_kernel<128>, dim3(runs, R / 8), dim3(256), 0, st, a, p, R, nq)
-                    : launch_pdl(join_kernel<64>, dim3(runs, R / 8), dim3(256), 0, st, a, p, R, nq);
+int attn_join(const AttnArgs& a, const Pieces& p, const int* status, int runs, int R, int nq, cudaStream_t st) {
+  return a.d == 128 ? launch_pdl(join_kernel<128>, dim3(runs, R / 8), dim3(256), 0, st, a, p, status, R, nq)
+                    : launch_pdl(join_kernel<64>, dim3(runs, R / 8), dim3(256), 0, st, a, p, status, R, nq);
+}
+
+int initial_status() {
+  static const int planted = [] {
+    const char* e = std::getenv("TV_TEST_ATTN_KV4_STATUS");
+    return e ? std::atoi(e) : 0;
+  }();
+  return planted;
 }
 
 size_t pieces_bytes(int runs, int R, int d) {

@@ -59,6 +59,7 @@ struct Lay {
 struct MmaArgs {
   AttnArgs a;
   int* status;
+  int status0;            // its first value
   Pieces pieces;          // runs = workers, 8 NB rows
   const int4* extents;    // [B] x = visible prefix (per-node prefixes), or NULL
   int workers;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(32 * Lay<D, NB>::kWarps, 1) mma_kernel(const _
   if (threadIdx.x == 0) *abort_flag = 0;
   griddep_wait();
   griddep_release();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // an expired wait writes it seconds later
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = p.status0;   // an expired wait writes it seconds later
 
   // ---- this warp's run: [w0, w1) of the list of all units, each kUnitCost places and then its chunks
   const int per = ((a.B + L::kWarps - 1) / L::kWarps + 31) / 32 * 32;   // entries (requests) per warp
@@ -660,7 +661,7 @@ int launch(const MmaArgs& p, cudaStream_t st) {
   if (!smem_limit(mma_kernel<D, NB>, static_cast<int>(L::kBytes))) return TV_ECUDA;
   const int rc = launch_pdl(mma_kernel<D, NB>, dim3(p.workers / L::kWarps), dim3(32 * L::kWarps), L::kBytes, st, p);
   if (rc != TV_OK) return rc;
-  return attn_join(p.a, p.pieces, p.workers, 8 * NB, p.a.max_nodes, st);
+  return attn_join(p.a, p.pieces, p.status, p.workers, 8 * NB, p.a.max_nodes, st);
 }
 
 }  // namespace
@@ -679,6 +680,7 @@ int attn_mma(const AttnArgs& a, void* ws, cudaStream_t st) {
   p.workers = sm_count() * warps_of(nb);
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<int*>(base);
+  p.status0 = initial_status();
   int4* extents = reinterpret_cast<int4*>(base + 256);
   p.pieces = pieces_at(base + 256 + align256(static_cast<size_t>(a.B) * sizeof(int4)), p.workers, 8 * nb);
   if (a.vis_prefix) {

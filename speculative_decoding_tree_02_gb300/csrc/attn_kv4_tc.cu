@@ -99,6 +99,7 @@ struct Lay {
 struct TcArgs {
   AttnArgs a;
   int* status;
+  int status0;            // its first value
   Pieces pieces;          // runs = 2 grid
   const int4* extents;    // [B * tiles] from attn_extents, or NULL
   int nq, tiles, grid;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(512, 1) attn_kernel(const __grid_constant__ Tc
   }
   griddep_wait();
   griddep_release();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;   // an expired wait writes it seconds later
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = p.status0;   // an expired wait writes it seconds later
   if (threadIdx.x < 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm0 + L::kMisc)), "r"(512)
                  : "memory");
@@ -824,7 +825,7 @@ template <int D>
 int launch(const TcArgs& p, cudaStream_t st) {
   if (!smem_limit(attn_kernel<D>, static_cast<int>(Lay<D>::kBytes))) return TV_ECUDA;
   const int rc = launch_pdl(attn_kernel<D>, dim3(p.grid), dim3(512), Lay<D>::kBytes, st, p);
-  return rc != TV_OK ? rc : attn_join(p.a, p.pieces, 2 * p.grid, kRowsT, p.nq, st);
+  return rc != TV_OK ? rc : attn_join(p.a, p.pieces, p.status, 2 * p.grid, kRowsT, p.nq, st);
 }
 
 }  // namespace
@@ -845,6 +846,7 @@ int attn_tc(const AttnArgs& a, void* ws, cudaStream_t st) {
   p.tiles = (a.max_nodes + p.nq - 1) / p.nq;
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<int*>(base);
+  p.status0 = initial_status();
   int4* extents = reinterpret_cast<int4*>(base + 256);
   p.pieces = pieces_at(base + 256 + align256(static_cast<size_t>(a.B) * p.tiles * sizeof(int4)), 2 * p.grid, kRowsT);
   if (a.vis_prefix || a.max_nodes > kKeys) {

@@ -127,7 +127,11 @@ struct Pieces {
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t pieces_bytes(int runs, int R, int d);
 Pieces pieces_at(char* base, int runs, int R);
-int attn_join(const AttnArgs& a, const Pieces& p, int runs, int R, int nq, cudaStream_t st);
+// `status`: the call's status word, written by the kernel before.
+int attn_join(const AttnArgs& a, const Pieces& p, const int* status, int runs, int R, int nq, cudaStream_t st);
+// What a call writes to its status word at the start: 0, except when the caller's process plants a failure to test the
+// failure path (TV_TEST_ATTN_KV4_STATUS, read on the host).
+int initial_status();
 
 }  // namespace kv4
 }  // namespace tv

@@ -708,6 +708,42 @@ def test_attention_zero_rows_in_units_that_are_cut(tv, counts, d, vis):
     c.check(out, lse)
 
 
+def test_attention_expired_wait_reports_failure_in_subprocess(tv):
+    """When a bounded wait of the tensor-core kernels runs out, every row of the call is NaN, *err is 1 and the status
+    word is not zero; rows that node_cnt leaves out stay.  The failure is planted on the host (TV_TEST_ATTN_KV4_STATUS
+    sets the status word where the call would clear it), so no wait runs out."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = ['tests', '.']
+import numpy as np, torch, speculative_decoding_tree_02_gb300 as tv
+from test_gpu_kv4 import Case
+for counts, cnt in (([40, 12, 3], [40, 0, 2]), ([2, 1, 4], [1, 0, 4]), ([150, 3, 1], [150, 2, 1])):
+    for vis in (False, True):
+        c = Case(40, counts, [300, 20, 0], 8, 2, 128, 32, True, 'chain', vis=vis, node_cnt=cnt)
+        n = sum(counts)
+        ws = tv.tree_verify_attn_kv4_workspace(3, max(counts), 8, 2, 128)
+        out = torch.full((n, 8, 128), 5.0, dtype=torch.bfloat16, device='cuda')
+        lse = torch.full((n, 8), 5.0, device='cuda')
+        _, _, err = c.run(tv, out=out, lse=lse, ws=ws)
+        torch.cuda.synchronize()
+        assert int(err) == 1 and int(ws[:4].view(torch.int32)) == 3
+        live = [int(c.off[r]) + i for r in range(3) for i in range(cnt[r])]
+        left = [i for i in range(n) if i not in live]
+        assert torch.isnan(out[live]).all() and torch.isnan(lse[live]).all()
+        assert (out[left] == 5).all() and (lse[left] == 5).all()
+        out, lse, err = c.run(tv, want_lse=False)
+        assert int(err) == 1 and lse is None and torch.isnan(out[live]).all()
+print('failure reported')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, TV_TEST_ATTN_KV4_STATUS="3"),
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "failure reported" in r.stdout, r.stderr[-3000:]
+
+
 # ------------------------------------------------------------ a run together
 @pytest.mark.parametrize("Hq,Hkv,d,P", [(8, 2, 128, 16), (4, 1, 64, 32)])
 def test_prompt_then_verification_steps(tv, Hq, Hkv, d, P):
