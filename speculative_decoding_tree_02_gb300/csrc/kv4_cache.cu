@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
     if (a.new_len) a.new_len[r] = len < 0 ? len : len + count;
     if (bad_len && (count > 0 || len < 0) && a.err) *a.err = 1;
   }
-  if (len < 0) return;
+  if (len < 0 || count == 0) return;             // (nothing to append: no table entry is needed)
   const int64_t g64 = len / 16 + static_cast<int64_t>(blockIdx.x);   // 16-token group of the request
   if (16 * g64 >= min(len + static_cast<int64_t>(count), cap)) return;   // (beyond the table: reported above)
   const int group = static_cast<int>(g64);
@@ -475,6 +475,7 @@ TV_API int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, in
   if (B == 0) return TV_OK;
   if (!row_off || !cache_len || (new_len && new_len == cache_len)) return TV_EINVAL;
   if (path && path_ld <= 0) return TV_EINVAL;
+  if (table_ld > 0 && !block_table) return TV_EINVAL;
   if (total_rows > 0 && max_new > 0) {
     if (!k || !v || !cache || !block_table || (rot_dim > 0 && !table)) return TV_EINVAL;
   }

@@ -578,6 +578,32 @@ def test_append_counts_skipped_rows_and_leaves_negative_lengths(tv):
     assert (host(c)[1] == 0).all() and (host(c)[0] != 0).any()
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("by_path", [True, False])
+@pytest.mark.parametrize("idle_len", [20, 16, 0, 48])
+def test_append_leaves_an_idle_request_alone(tv, idle_len, by_path, bf16):
+    """A request that appends nothing needs no table entry: its pages may have been given back (-1, or a page that is
+    another request's by now), its length kept."""
+    rng = np.random.default_rng(idle_len)
+    P, H, d, N = 16, 2, 64, 3
+    table = np.array([[-1, -1, -1], [3, 1, 0], [99, 99, 1]], np.int32)
+    lens = np.array([idle_len, 15, idle_len], np.int32)
+    path = np.array([[-1, 0, 1], [0, 2, -1], [-1, -1, -1]], np.int32) if by_path else None
+    off = np.array([0, N, 2 * N, 3 * N] if by_path else [0, 0, N, N], np.int32)
+    (_, k, v), (_, hk, hv) = fused(rng, int(off[-1]), 1, H, d, bf16)
+    before = rng.integers(0, 256, (4, H, P * (d + 4))).astype(np.uint8)
+    want = before.copy()
+    want_len = ok.append(want, P, table, lens, hk, hv, off, path)
+    c = dev(before)
+    new_len, err = tv.kv4_append(k, v, c, P, dev(table), dev(lens), dev(off), N, path=dev(path))
+    assert int(err) == 0 and np.array_equal(host(new_len), want_len) and np.array_equal(host(c), want)
+    # nobody appends: by the bound, by the rows
+    for kk, vv, o, m in ((k, v, off, 0), (k[:0], v[:0], np.zeros(4, np.int32), N)):
+        c = dev(before)
+        new_len, err = tv.kv4_append(kk, vv, c, P, dev(np.full_like(table, -1)), dev(lens), dev(o * 0), m)
+        assert int(err) == 0 and np.array_equal(host(new_len), lens) and np.array_equal(host(c), before)
+
+
 def test_cache_offsets_pass_32_bits(tv):
     """Pages behind the first 4 GB of the pool."""
     P, H, d = 128, 8, 128

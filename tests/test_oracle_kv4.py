@@ -209,6 +209,11 @@ def test_calls_are_refused_before_any_launch(tv, call, want, kw):
     assert call(tv.load_library(), b, **kw) == want
 
 
+@pytest.mark.parametrize("kw", [dict(max_new=0), dict(rows=0), dict(rows=0, max_new=0), dict()])
+def test_append_wants_its_block_table_whatever_the_rows(tv, kw):
+    assert append_call(tv.load_library(), 1 << 12, **kw, bt=None) == EINVAL
+
+
 def test_cache_size_counts_blocks_and_refuses_other_shapes(tv):
     lib = tv.load_library()
     assert lib.kv4_cache_size(3, 64, 8, 128) == 3 * 8 * 64 * 132
