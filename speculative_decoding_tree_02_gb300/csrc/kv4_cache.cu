@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(D, 768 / D) append_kernel(const AppendArgs a) 
   }
   count = max(count, 0);
   const int64_t cap = static_cast<int64_t>(a.table_ld) * a.P;
-  const bool bad_len = len < 0 || len + static_cast<int64_t>(count) > cap ||
-                       (!a.path && a.row_off[r + 1] - base > a.max_new);
+  const bool bad = len < 0 || (count > 0 && len + static_cast<int64_t>(count) > cap) ||
+                   (!a.path && a.row_off[r + 1] - base > a.max_new);
   if (blockIdx.x == 0 && h0 == 0 && tid == 0) {
     if (a.new_len) a.new_len[r] = len < 0 ? len : len + count;
-    if (bad_len && (count > 0 || len < 0) && a.err) *a.err = 1;
+    if (bad && a.err) *a.err = 1;
   }
   if (len < 0 || count == 0) return;             // (nothing to append: no table entry is needed)
   const int64_t g64 = len / 16 + static_cast<int64_t>(blockIdx.x);   // 16-token group of the request

@@ -566,6 +566,16 @@ def test_append_takes_no_more_rows_than_max_new(tv):
     assert np.array_equal(host(new_len), want) and np.array_equal(host(c), cache)
 
 
+def test_append_tells_of_rows_beyond_a_max_new_of_zero(tv):
+    P, H, d = 16, 1, 64
+    (_, k, v), _ = fused(np.random.default_rng(25), 4, 1, H, d, True)
+    for off, want in (([0, 0, 4], 1), ([0, 0, 0], 0)):
+        c = torch.zeros((2, H, P * (d + 4)), dtype=torch.uint8, device="cuda")
+        lens = dev(np.array([3, 5], np.int32))
+        new_len, err = tv.kv4_append(k, v, c, P, dev(np.array([[0], [1]], np.int32)), lens, dev(np.array(off, np.int32)), 0)
+        assert int(err) == want and torch.equal(new_len, lens) and (c == 0).all()
+
+
 def test_append_counts_skipped_rows_and_leaves_negative_lengths(tv):
     rng = np.random.default_rng(23)
     P, H, d = 16, 1, 64
