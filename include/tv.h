@@ -556,7 +556,7 @@ int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* blo
  * Outputs: out [total_nodes, Hq, d] dtype; lse float [total_nodes, Hq] or
  *   NULL.  Rows of nodes that node_cnt leaves out are not written.
  * Workspace: tree_verify_attn_kv4_workspace_size(...) bytes, 256-byte
- *   aligned; its first int32 is a status word as in tree_verify_attn.  When it
+ *   aligned, enough for calls with fewer requests or nodes too; its first int32 is a status word as in tree_verify_attn.  When it
  *   is not 0 (a device-side wait ran out), out and lse are NaN for all rows of
  *   the call, and 1 is written to *err.
  * -------------------------------------------------------------------------- */

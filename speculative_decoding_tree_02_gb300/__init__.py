@@ -620,8 +620,8 @@ def kv4_gather(cache, page_size, block_table, out_off, max_rows, start=None, tot
 
 
 def tree_verify_attn_kv4_workspace(B, max_nodes, Hq, Hkv, d, dtype=torch.bfloat16, device="cuda"):
-    """A workspace for tree_verify_attn_kv4 calls of these sizes (one call at a time); a call that needs more than
-    the workspace it is given is refused."""
+    """A workspace for tree_verify_attn_kv4 calls of up to B requests of up to max_nodes nodes (one call at a time); a
+    call that needs more than the workspace it is given is refused."""
     code = TV_F32 if dtype == torch.float32 else TV_BF16
     return _ws(load_library().tree_verify_attn_kv4_workspace_size(B, max_nodes, Hq, Hkv, d, code), device)
 

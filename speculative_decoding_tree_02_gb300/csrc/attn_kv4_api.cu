@@ -1,6 +1,8 @@
 // tree_verify_attn_kv4 entry point: host validation, workspace, dispatch by type
 // (bf16 rows on the tensor cores, fp32 rows on the CUDA cores: their products
 // would lose bits in a bf16 MMA).
+#include <algorithm>
+
 #include "kv4.cuh"
 
 using namespace tv;
@@ -20,8 +22,14 @@ bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_
 TV_API size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype) {
   if (!shape_ok(B, max_nodes, Hq, Hkv, d) || B == 0 || max_nodes == 0 || Hq / Hkv > 64) return 0;
   if (dtype != TV_BF16) return 256;
-  return few_rows(max_nodes, Hq, Hkv) ? kv4::attn_mma_workspace(B, max_nodes, Hq, Hkv, d)
-                                      : kv4::attn_tc_workspace(B, max_nodes, Hq, Hkv, d);
+  // enough for every smaller call too, whichever kernel it takes: a server keeps one workspace for its largest trees
+  const int g = Hq / Hkv;
+  size_t bytes = few_rows(max_nodes, Hq, Hkv) ? 0 : kv4::attn_tc_workspace(B, max_nodes, Hq, Hkv, d);
+  for (const int rows : {8, 16}) {
+    const int nodes = std::min(max_nodes, rows / g);
+    if (nodes > 0) bytes = std::max(bytes, kv4::attn_mma_workspace(B, nodes, Hq, Hkv, d));
+  }
+  return bytes;
 }
 
 TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pages, int page_size,

@@ -551,6 +551,15 @@ def test_two_graphs_at_once_with_a_workspace_each(tv):
         c.check(out, lse)
 
 
+def test_one_workspace_for_the_largest_trees_serves_all_calls(tv):
+    ws = tv.tree_verify_attn_kv4_workspace(8, 113, 32, 8, 128)
+    for seed, counts in enumerate(([113, 4], [1, 1, 1], [4, 2], [3], [60])):
+        c = Case(50 + seed, counts, [200] * len(counts), 32, 8, 128, 64, True, "chain")
+        out, lse, err = c.run(tv, ws=ws)
+        assert int(err) == 0
+        c.check(out, lse)
+
+
 def test_append_takes_no_more_rows_than_max_new(tv):
     rng = np.random.default_rng(22)
     P, H, d = 16, 2, 64

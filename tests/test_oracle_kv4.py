@@ -221,6 +221,20 @@ def test_cache_size_counts_blocks_and_refuses_other_shapes(tv):
         assert lib.kv4_cache_size(*bad) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 1), (7, 1), (32, 8), (64, 2), (64, 1), (9, 9), (40, 2)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_workspace_covers_smaller_calls(tv, Hq, Hkv, d, dtype):
+    """A server keeps one workspace for its most requests and largest trees."""
+    size = tv.load_library().tree_verify_attn_kv4_workspace_size
+    last = 0
+    for nodes in (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 33, 64, 65, 113, 128, 129, 500, 1024):
+        by_b = [size(B, nodes, Hq, Hkv, d, dtype) for B in (1, 2, 3, 16, 17, 64, 100, 1000)]
+        assert by_b == sorted(by_b) and by_b[0] > 0
+        assert size(64, nodes, Hq, Hkv, d, dtype) >= last
+        last = size(64, nodes, Hq, Hkv, d, dtype)
+
+
 def test_binding_refuses_wrong_tensors(tv):
     import torch
     cache = torch.zeros((2, 1, 16 * 68), dtype=torch.uint8)
