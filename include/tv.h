@@ -549,7 +549,8 @@ int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* blo
  *           [0, table_ld * page_size]; a clamped one writes 1 to *err)
  *   node_off, node_cnt, anc, anc_words, vis_prefix, max_nodes, scale: as in
  *           tree_verify_attn (nodes outside [0, total_nodes) do not exist)
- *   d in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 64
+ *   d in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 64; table_ld * page_size at most
+ *           2^31 - 65536, and less for hundreds of KV heads (TV_EUNSUPPORTED)
  * A cached token with a bad page entry is not visible (1 is written to *err).
  * What a node does not see does not reach its output, whatever it holds: NaN
  * in other nodes' rows, stale tokens behind cache_len.

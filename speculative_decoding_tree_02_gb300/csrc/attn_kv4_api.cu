@@ -17,6 +17,13 @@ bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
 // 100/17/50 us, 16 rows 76/18/41 against 103/17/52, 32 rows (with twice the
 // accumulators) 152/39/72 against 105/19/53.
 bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 16; }
+// The kernels count a request's tokens, the places of its row tile's units (a unit's tiles, and a fixed part) and those of
+// a run in 32 bits: tokens with room for a tile beyond the last, 2^38 places in all for at least 2^7 runs.
+bool counts_fit(int B, int max_nodes, int Hq, int Hkv, int64_t cap) {
+  const int nq = 64 / (Hq / Hkv);
+  const int64_t places = (cap / 64 + 24) * Hkv, tiles = static_cast<int64_t>(B) * ((max_nodes + nq - 1) / nq);
+  return cap <= 0x7fff0000ll && places <= 0x7fffffffll && tiles * places <= 1ll << 38;
+}
 }  // namespace
 
 TV_API size_t tree_verify_attn_kv4_workspace_size(int B, int max_nodes, int Hq, int Hkv, int d, int dtype) {
@@ -43,8 +50,8 @@ TV_API int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, i
   if (dtype != TV_F32 && dtype != TV_BF16) return TV_EINVAL;
   if (d != 64 && d != 128) return TV_EUNSUPPORTED;
   if (!kv4::page_size_ok(page_size) || Hq / Hkv > 64 || max_nodes > TV_MAX_NODES) return TV_EUNSUPPORTED;
-  if (static_cast<int64_t>(table_ld) * page_size > 0x7fffffffll) return TV_EUNSUPPORTED;
   if (static_cast<int64_t>(B) * Hkv > 65535 || Hq > 65535) return TV_EUNSUPPORTED;
+  if (!counts_fit(B, max_nodes, Hq, Hkv, static_cast<int64_t>(table_ld) * page_size)) return TV_EUNSUPPORTED;
   if (anc_words < (max_nodes + 63) / 64 || anc_words < 1) return TV_EINVAL;
   if (!(scale > 0.f) || scale > 3.402823466e38f) return TV_EINVAL;
   if (B == 0 || max_nodes == 0 || total_nodes == 0) return TV_OK;

@@ -221,6 +221,15 @@ def test_cache_size_counts_blocks_and_refuses_other_shapes(tv):
         assert lib.kv4_cache_size(*bad) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(bt_ld=(1 << 27) - 1), dict(bt_ld=(1 << 24) - 1, page=128, dt=0), dict(bt_ld=(1 << 27) - 4095),   # tokens
+    dict(bt_ld=1 << 26, Hq=128, Hkv=128, ldq=1 << 14, ldk=1 << 14, ldv=1 << 14),              # tiles of a request
+    dict(bt_ld=1 << 22, Hq=128, Hkv=128, ldq=1 << 14, ldk=1 << 14, ldv=1 << 14, B=400, nodes=1024, words=16)])   # in all
+def test_attention_refuses_what_its_counters_cannot_hold(tv, kw):
+    """A prefix of 2^31 - 16 tokens: the tile after the last begins past 2^31."""
+    assert attn_call(tv.load_library(), 1 << 12, **kw) == EUNSUPPORTED
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 1), (7, 1), (32, 8), (64, 2), (64, 1), (9, 9), (40, 2)])
 @pytest.mark.parametrize("dtype", [0, 1])
