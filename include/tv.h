@@ -458,7 +458,7 @@ int blockpilot_mlp(const void* last_logits, int64_t ld, const float* row_lse, co
  *   in fp32 (bf16_up rounds up to bf16); a row with a NaN or infinity gets
  *   s = NaN and reads back as NaN as a whole.  132 bytes per token and head
  *   for K and V at d = 128, against 512 in bf16.
- * block_table  int32 [B, table_ld]: page of tokens [P*i, P*(i+1)) of request r
+ * block_table  int32 [B, table_ld] (NULL only with table_ld 0): page of tokens [P*i, P*(i+1)) of request r
  *   at [r, i].  Only entries that a token needs are read.  An entry outside
  *   [0, n_pages) is bad: nothing is read or written through it, and 1 is
  *   written to *err (device int32, may be NULL; never cleared by the calls).
@@ -532,7 +532,7 @@ int kv4_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype
  * Tokens with a bad page entry or past the table, and all rows of a request
  * whose start or out_off is out of range, are not written, and 1 is written
  * to *err; so it is for more rows than max_rows (the first max_rows are
- * written).
+ * written).  With max_rows or total_rows 0 the call does nothing.
  * -------------------------------------------------------------------------- */
 int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
                const int32_t* start, const int32_t* out_off, int B, int max_rows, int total_rows, int Hkv, int d,
@@ -554,6 +554,9 @@ int kv4_gather(const void* cache, int n_pages, int page_size, const int32_t* blo
  * A cached token with a bad page entry is not visible (1 is written to *err).
  * What a node does not see does not reach its output, whatever it holds: NaN
  * in other nodes' rows, stale tokens behind cache_len.
+ * max_nodes also chooses the bf16 kernel: calls of max_nodes * Hq / Hkv <= 16
+ *   take the one for few rows, all others tiles of 64 rows, however few of the
+ *   nodes are live.  A call for single tokens gives max_nodes = 1.
  * Outputs: out [total_nodes, Hq, d] dtype; lse float [total_nodes, Hq] or
  *   NULL.  Rows of nodes that node_cnt leaves out are not written.
  * Workspace: tree_verify_attn_kv4_workspace_size(...) bytes, 256-byte

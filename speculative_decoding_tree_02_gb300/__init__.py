@@ -630,7 +630,8 @@ def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_
                          vis_prefix=None, node_cnt=None, scale=None, out=None, lse=None, want_lse=True, ws=None,
                          err=None):
     """tree_verify_attn with the prefix in a paged 4-bit cache.  q, k_tree, v_tree: [n, heads, d], row strides free.
-    Returns out, lse, err."""
+    Returns out, lse, err; err is 1 after a bad page or length, and with NaN outputs after a device-side wait that ran
+    out.  Give the tightest max_nodes: 16 rows (max_nodes * Hq / Hkv) or fewer take the kernel for few rows."""
     dev = q.get_device()
     n, Hq, d = q.shape
     n_pages, Hkv, dc = _cache_geometry(cache, page_size)

@@ -15,7 +15,9 @@ bool shape_ok(int B, int max_nodes, int Hq, int Hkv, int d) {
 // tcgen05 tiles above. 64 requests over 512..4096 tokens, 1 over 2048 and 8 over
 // 8192 of 8 KV heads of 128, mma.sync against tcgen05: 4 rows 54/15/35 against
 // 100/17/50 us, 16 rows 76/18/41 against 103/17/52, 32 rows (with twice the
-// accumulators) 152/39/72 against 105/19/53.
+// accumulators) 152/39/72 against 105/19/53.  max_nodes is the caller's bound:
+// the live nodes are known on the device only, and a captured call keeps its
+// kernel whatever they are.
 bool few_rows(int max_nodes, int Hq, int Hkv) { return static_cast<int64_t>(max_nodes) * (Hq / Hkv) <= 16; }
 // The kernels count a request's tokens, the places of its row tile's units (a unit's tiles, and a fixed part) and those of
 // a run in 32 bits: tokens with room for a tile beyond the last, 2^38 places in all for at least 2^7 runs.

@@ -62,7 +62,7 @@ __device__ __noinline__ void fail_rows(const AttnArgs& a) {
 // Piece 0 of a cut unit is slot 1 of the run where the unit starts, piece i
 // slot 0 of the i-th run after it.  CTA = (starting run, eight rows), warp =
 // row, lane = D / 32 dims; the pieces are taken in run order, eight loads in
-// flight.  Bound by the latency of those loads: 11 us for the 304 runs of 64
+// flight.  Bound by the latency of those loads: 12 us for the 304 runs of 64
 // chains of 64 rows, 6 us for the runs of 64 single tokens (cold caches).
 template <int D>
 __global__ void __launch_bounds__(256, 4) join_kernel(const AttnArgs a, const Pieces p, const int* status, int R,

@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kChunk = 64;     // tokens per chunk
 // What a unit costs beside its chunks, in chunks: 64 single tokens 51.5 us without it, 50.4 at 1, 51.9 at 2, 53 at 3;
-// 16 rows per KV head 79, 76, 73, 75.
+// 16 rows per KV head 79, 76, 73, 75 (8 KV heads of 128; other geometries take the same number untimed).
 constexpr int kUnitCost = 1;
 
 template <int D, int NB>

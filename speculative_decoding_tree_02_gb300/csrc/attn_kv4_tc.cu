@@ -69,7 +69,8 @@ constexpr int kRowsT = 64;        // rows per tile
 constexpr int kCols = 32;         // rows per warpgroup in the softmax
 constexpr int kStages = 4;        // staged tiles per team
 // What a unit costs beside its tiles, in tiles: its queries, its first tile's references, its tile of nodes, its output.
-// A tree of 512 units of 1 to 33 tiles 172 us without it, 115 at 2, 104 at 3, 105 at 6; 64 chains 122, 107, 105, 109.
+// A tree of 512 units of 1 to 33 tiles 172 us without it, 115 at 2, 104 at 3, 105 at 6; 64 chains 122, 107, 105, 109
+// (both of 8 KV heads of 128; other geometries take the same number untimed).
 constexpr int kUnitCost = 3;
 
 template <int D>
