@@ -285,6 +285,52 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
                               size_t ws_bytes, tv_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * accept_sampled — verification of drafted tokens against the target's
+ * probabilities at each request's temperature, top-k and top-p.
+ * Graft page §2 (third gear): draft and retrieved nodes face the same rule and
+ * the result is lossless; SpecOPD page §03: the acceptance probability under
+ * exact rejection sampling.  The pages give no procedure for retrieved nodes,
+ * which have no draft distribution, nor for truncated sampling.  Reading:
+ *   p at a node: softmax(logits / T) of what top-k and then top-p keep.  Both
+ *   keep whole classes of equal logits: top-k the tokens with fewer than k
+ *   higher ones, top-p those above which less than top_p of the mass that
+ *   top-k left lies (the highest class always).  T <= 0 (or NaN): all mass on
+ *   the highest logit, the lowest index among equals.  NaN logits count as -inf.
+ *   From the root, the children of the current node are tried in index order,
+ *   p' = p at first.  Child c with token x is accepted iff
+ *     u_node[c] * q(x) < p'(x)   drawn from q, the drafter's distribution at
+ *                                the current node; a rejection makes p'
+ *                                max(0, p' - q), renormalised
+ *     u_node[c] < p'(x)          proposed without a distribution (retrieved,
+ *                                or a drafter's favourites); a rejection
+ *                                removes x from p', renormalised
+ *   (nothing left, which only rounding can bring about: p' = p).  With no
+ *   child accepted the bonus token maximises p'(v) / race[v], the lowest index
+ *   among equals: with exponential variates in race a draw from p'.  A row of
+ *   -inf and NaN alone has p = 0 and gives -1.
+ *   parent, tok int32 [n] (request-local parents, parents before children)
+ *   p_logits [n, ld] dtype: target logits at each node
+ *   q_prob   float [n, ldq] or NULL (no child is drawn): the distribution that
+ *            the drawn children of each node came from
+ *   drawn    uint8 [n] or NULL (all, if q_prob is given): node was drawn
+ *   temperature float [B] or NULL (1); top_k int32 [B] or NULL (0 or less: off);
+ *            top_p float [B] or NULL (1 or more, or NaN: off)
+ *   u_node   float [n] in [0, 1); race float [B, ldr], positive
+ *   total_nodes  rows of the inputs; max_nodes <= TV_MAX_NODES; V <= 2^20
+ * Outputs: as accept_rejection_sampling (accept_len -1, best_node -1, bonus -1
+ *   for a request without nodes).
+ * Workspace: accept_sampled_workspace_size(...) bytes, 16-byte aligned.
+ * Arithmetic: fp32, each row read twice at most; a decision whose numbers lie
+ *   within ~1e-6 (relative) of each other may differ from exact arithmetic.
+ * -------------------------------------------------------------------------- */
+size_t accept_sampled_workspace_size(int B, int total_nodes, int V);
+int accept_sampled(const int32_t* parent, const int32_t* tok, const void* p_logits, int dtype, int V, int64_t ld,
+                   const float* q_prob, int64_t ldq, const uint8_t* drawn, const int32_t* node_off, int B,
+                   int max_nodes, int total_nodes, int max_depth, const float* temperature, const int32_t* top_k,
+                   const float* top_p, const float* u_node, const float* race, int64_t ldr, int32_t* accept_len,
+                   int32_t* best_node, int32_t* path, int32_t* bonus, void* ws, size_t ws_bytes, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * graft_adj_update — online update of Graft's V x k successor table.
  * Graft page §2 (second/third gear) and §6: after verification, every
  * verified position, accepted or rejected, rewrites the row of its token with
@@ -571,6 +617,82 @@ int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pa
                          const int32_t* node_cnt, const uint64_t* anc, int anc_words, const int32_t* vis_prefix,
                          int B, int max_nodes, int total_nodes, int Hq, int Hkv, int d, int dtype, float scale,
                          void* out, float* lse, void* ws, size_t ws_bytes, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Eviction from the paged 4-bit cache by accumulated attention weight (no
+ * counterpart in the source pages): kv4_attn_mass, kv4_evict_select,
+ * kv4_compact.  Each KV head keeps tokens of its own, all heads of a request
+ * the same number.  After an eviction a token's index is no longer its
+ * position: later kv4_append calls give pos.
+ * -------------------------------------------------------------------------- */
+/* --------------------------------------------------------------------------
+ * kv4_attn_mass — the attention weight that cached tokens received, added to
+ * what they had:
+ *   m[r,h,t] = sum over the request's rows i that see t and the query heads hq
+ *              of KV head h of exp(scale * q[i,hq].k[t,h] - lse[i,hq])
+ *   score_out[r,h,t] = decay * score_in[r,h,t] + m[r,h,t],  t < cache_len[r]
+ * k: the cached key (its codes' values).  lse: of the attention that the
+ * weights belong to (tree_verify_attn_kv4).
+ *   q [total_rows, ldq] dtype, Hq heads of d from the row's start, rotated as
+ *           for the attention; lse float [total_rows, Hq]
+ *   row_off, path, path_ld: the rows of each request, as in kv4_append (after
+ *           an append: the accepted rows); max_rows bounds their number
+ *   causal  1: row j of a request sees its first old_len[r] + j + 1 cached
+ *           tokens (the rows' own tokens follow old_len); 0: all of them
+ *   vis_prefix int32 [total_rows] or NULL: a row sees at most the first
+ *           vis_prefix[row] tokens
+ *   old_len int32 [B] (NULL allowed unless causal: = cache_len): tokens that
+ *           score_in covers; the others had nothing
+ *   score_in [B, Hkv, score_in_ld] or NULL (zeros); may be score_out
+ *   max_len bounds cache_len (launch geometry), <= score_out_ld, score_in_ld
+ *   decay in [0, 1] (0: score_in is not read)
+ * Outputs: score_out float [B, Hkv, score_out_ld], entries from cache_len on
+ *   are not written.
+ * A row with lse = -inf (it saw nothing) weighs nothing; a NaN row makes the
+ * tokens that it sees NaN.  A token with a bad page entry gets no weight, a row
+ * outside [0, total_rows) gives none, tokens beyond max_len or the table and
+ * rows beyond max_rows are left out: each writes 1 to *err.
+ * -------------------------------------------------------------------------- */
+int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype, const void* cache, int n_pages,
+                  int page_size, const int32_t* block_table, int table_ld, const int32_t* cache_len,
+                  const int32_t* row_off, const int32_t* path, int path_ld, const int32_t* vis_prefix,
+                  const int32_t* old_len, int causal, int B, int max_rows, int total_rows, int max_len, int Hq, int Hkv,
+                  int d, float scale, float decay, const float* score_in, int64_t score_in_ld, float* score_out,
+                  int64_t score_out_ld, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kv4_evict_select — which tokens stay: n = min(cache_len[r], budget[r]) per
+ * head, namely the first n_sink, the last n_recent (where n does not suffice,
+ * the sinks first, then the latest) and of those between the ones with the
+ * highest score, the lower index among equals (NaN below all, zeros alike).
+ *   score [B, Hkv, score_ld] float; max_len bounds cache_len, at most 393216
+ * Outputs: idx int32 [B, Hkv, idx_ld]: the kept tokens, ascending, -1 behind
+ *   them; score_out [B, Hkv, score_out_ld] float or NULL: their scores (may be
+ *   score: the rows shrink in place); new_len int32 [B]: n.
+ * More kept tokens than idx_ld: idx_ld of them, and 1 is written to *err; so it
+ * is for a negative budget (0).  A cache_len outside [0, max_len]: new_len is
+ * cache_len, nothing is kept, 1 is written to *err.
+ * -------------------------------------------------------------------------- */
+int kv4_evict_select(const float* score, int64_t score_ld, const int32_t* cache_len, const int32_t* budget, int n_sink,
+                     int n_recent, int B, int Hkv, int max_len, int32_t* idx, int64_t idx_ld, float* score_out,
+                     int64_t score_out_ld, int32_t* new_len, int32_t* err, tv_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kv4_compact — moves token idx[r,h,j] of each head to token j, j < new_len[r]:
+ * codes and scales as they are.
+ *   idx int32 [B, Hkv, idx_ld]: ascending in each row, as kv4_evict_select
+ *           gives it; max_keep <= idx_ld bounds new_len (launch geometry)
+ *   dst_table int32 [B, dst_ld] or NULL.  NULL: in place, on the request's own
+ *           pages (no two requests share one).  Else the tokens go to these
+ *           pages, which are nobody's source in the call: sources may be shared.
+ * Other tokens of the destination keep what they hold (in place: those from
+ * new_len on).  A token whose index is outside [0, cache_len[r]) or whose
+ * source or destination page is bad is not moved, and 1 is written to *err; so
+ * it is for a new_len outside [0, max_keep] (clamped).
+ * -------------------------------------------------------------------------- */
+int kv4_compact(void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
+                const int32_t* cache_len, const int32_t* idx, int64_t idx_ld, const int32_t* new_len, int B, int max_keep,
+                const int32_t* dst_table, int dst_ld, int Hkv, int d, int32_t* err, tv_stream_t stream);
 
 #ifdef __cplusplus
 }

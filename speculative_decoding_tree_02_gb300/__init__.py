@@ -26,6 +26,7 @@ __all__ = [
     "stage_templates", "assemble_hybrid", "LIB_PATH", "load_library", "EXPORTS",
     "graft_stage_decide", "graft_replace", "dcut_choose_rho", "best_first_template", "accept_rejection_sampling",
     "tv_rope", "kv4_new_cache", "kv4_append", "kv4_gather", "tree_verify_attn_kv4", "tree_verify_attn_kv4_workspace",
+    "accept_sampled", "accept_sampled_workspace", "kv4_attn_mass", "kv4_evict_select", "kv4_compact",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtreeverify.so")
@@ -66,6 +67,13 @@ _SIGS = {
     "tree_verify_attn_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "tree_verify_attn_kv4": (_I, [_P, _I64, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _I, _I,
                                   _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "accept_sampled_workspace_size": (_SZ, [_I, _I, _I]),
+    "accept_sampled": (_I, [_P, _P, _P, _I, _I, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _P, _P,
+                            _P, _P, _P, _SZ, _P]),
+    "kv4_attn_mass": (_I, [_P, _I64, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                           _F, _F, _P, _I64, _P, _I64, _P, _P]),
+    "kv4_evict_select": (_I, [_P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _P, _P]),
+    "kv4_compact": (_I, [_P, _I, _I, _P, _I, _P, _P, _I64, _P, _I, _I, _P, _I, _I, _I, _P, _P]),
     "blockpilot_mlp": (_I, [_P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
 EXPORTS = tuple(_SIGS)
@@ -665,3 +673,154 @@ def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_
              _dense(out, "out", q.dtype, dev, (n, Hq, d)), _dense(lse, "lse", torch.float32, dev, (n, Hq)),
              _dense(ws, "ws", torch.uint8, dev, (ws.numel(),)), ws.numel(), perr)
     return out, lse, err
+
+
+# ------------------------------------------------- eviction from the 4-bit cache
+def _scores(t: Optional[torch.Tensor], name: str, dev: int, B: int, H: int):
+    """(address, columns) of float32 [B, H, columns] scores; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [{B}, {H}, columns]")
+    return _dense(t, name, torch.float32, dev, (B, H, t.shape[2])), t.shape[2]
+
+
+def kv4_attn_mass(q, lse, cache, page_size, block_table, cache_len, row_off, max_rows, score=None, old_len=None,
+                  path=None, vis_prefix=None, causal=False, scale=None, decay=1.0, max_len=None, score_out=None,
+                  err=None):
+    """Adds to ``score`` float32 [B, Hkv, columns] (None: zeros) the attention weight that the cached tokens received
+    from rows of q [n, Hq, d] (row stride free) whose attention gave ``lse`` float32 [n, Hq].  ``path`` int32 [B, m]
+    picks rows as in kv4_append; ``causal``: row j sees old_len + j + 1 cached tokens.  ``max_len`` bounds cache_len
+    (default: what the scores and the table have room for).  ``score_out`` may be ``score``.  Returns score_out, err."""
+    dev = q.get_device()
+    n, Hq, d = q.shape
+    n_pages, Hkv, dc = _cache_geometry(cache, page_size)
+    if dc != d:
+        raise ValueError(f"the cache holds heads of {dc}, q has {d}")
+    if cache.get_device() != dev:
+        raise ValueError(f"cache is on {cache.device}, expected device {dev}")
+    dt = _act_dtype(q, "q")
+    B = cache_len.numel()
+    if scale is None:
+        scale = 1.0 / d ** 0.5
+    pq, ldq = _rows(q, "q", q.dtype, dev, n, Hq, d)
+    table, cols = _table(block_table, B, dev)
+    pin, ld_in = _scores(score, "score", dev, B, Hkv)
+    if score_out is None:
+        if score is None and max_len is None:
+            raise ValueError("kv4_attn_mass needs score, score_out or max_len")
+        score_out = torch.zeros((B, Hkv, ld_in if score is not None else max_len), dtype=torch.float32, device=q.device)
+    pout, ld_out = _scores(score_out, "score_out", dev, B, Hkv)
+    if max_len is None:
+        max_len = min(ld_out, cols * page_size)
+        if score is not None:
+            max_len = min(max_len, ld_in)
+    err, perr = _new_err(err, q)
+    i32 = torch.int32
+    _call_on(dev, "kv4_attn_mass", pq, ldq, _dense(lse, "lse", torch.float32, dev, (n, Hq)), dt, cache.data_ptr(), n_pages,
+             page_size, table, cols, _dense(cache_len, "cache_len", i32, dev, (B,)),
+             _dense(row_off, "row_off", i32, dev, (B + 1,)),
+             *(_table(path, B, dev, "path") if path is not None else (None, 0)),
+             _dense(vis_prefix, "vis_prefix", i32, dev, (n,)), _dense(old_len, "old_len", i32, dev, (B,)), int(causal), B,
+             max_rows, n, max_len, Hq, Hkv, d, float(scale), float(decay), pin, ld_in, pout, ld_out, perr)
+    return score_out, err
+
+
+def kv4_evict_select(score, cache_len, budget, max_len, n_sink=0, n_recent=0, max_keep=None, idx=None, score_out=None,
+                     new_len=None, err=None):
+    """Chooses min(cache_len, budget) tokens per request and head: the first ``n_sink``, the last ``n_recent`` and the
+    highest scores between.  Give ``idx`` int32 [B, Hkv, columns] or ``max_keep`` (its columns, at least the largest
+    budget that applies).  ``score_out`` may be ``score``.  Returns idx (ascending, -1 behind), score_out, new_len, err."""
+    B, H, ld = score.shape
+    dev = score.get_device()
+    if idx is None:
+        if max_keep is None:
+            raise ValueError("kv4_evict_select needs idx or max_keep")
+        idx = torch.empty((B, H, max_keep), dtype=torch.int32, device=score.device)
+    i32 = torch.int32
+    pidx = _dense(idx, "idx", i32, dev, (B, H, idx.shape[-1]))
+    if score_out is None:
+        score_out = torch.empty((B, H, idx.shape[2]), dtype=torch.float32, device=score.device)
+    pout, ld_out = _scores(score_out, "score_out", dev, B, H)
+    if new_len is None:
+        new_len = torch.empty(B, dtype=i32, device=score.device)
+    err, perr = _new_err(err, score)
+    _call_on(dev, "kv4_evict_select", _dense(score, "score", torch.float32, dev, (B, H, ld)), ld,
+             _dense(cache_len, "cache_len", i32, dev, (B,)), _dense(budget, "budget", i32, dev, (B,)), n_sink, n_recent, B, H,
+             max_len, pidx, idx.shape[2], pout, ld_out, _dense(new_len, "new_len", i32, dev, (B,)), perr)
+    return idx, score_out, new_len, err
+
+
+def kv4_compact(cache, page_size, block_table, cache_len, idx, new_len, max_keep, dst_table=None, err=None):
+    """Moves token idx[r, h, j] of each head to token j < new_len[r], in place or (``dst_table`` int32 [B, columns]) to
+    pages that no request of the call reads.  Rows of ``idx`` ascend.  Returns err."""
+    dev = cache.get_device()
+    n_pages, Hkv, d = _cache_geometry(cache, page_size)
+    B = cache_len.numel()
+    if idx.dim() != 3:
+        raise ValueError(f"idx must be [{B}, {Hkv}, columns]")
+    err, perr = _new_err(err, cache)
+    i32 = torch.int32
+    table, cols = _table(block_table, B, dev)
+    dst, dst_cols = _table(dst_table, B, dev, "dst_table") if dst_table is not None else (None, 0)
+    _call_on(dev, "kv4_compact", cache.data_ptr(), n_pages, page_size, table, cols,
+             _dense(cache_len, "cache_len", i32, dev, (B,)), _dense(idx, "idx", i32, dev, (B, Hkv, idx.shape[2])),
+             idx.shape[2], _dense(new_len, "new_len", i32, dev, (B,)), B, max_keep, dst, dst_cols, Hkv, d, perr)
+    return err
+
+
+# ------------------------------------------- verification at temperature, top-k, top-p
+def _logit_rows(t: torch.Tensor, name: str, dtype, dev: int, n: int, V: int):
+    """(address, elements between rows) of [n, V] rows, the row stride free."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    if t.shape != (n, V):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, V)}")
+    s0, s1 = t.stride()
+    if (s1 != 1 and V > 1) or (n > 1 and s0 < V):
+        raise ValueError(f"{name}: rows must be packed and not overlap")
+    return t.data_ptr(), (s0 if n > 1 else V)
+
+
+def accept_sampled_workspace(B, total_nodes, V, device="cuda"):
+    """A workspace for accept_sampled calls of up to total_nodes nodes (one call at a time)."""
+    return _ws(load_library().accept_sampled_workspace_size(B, total_nodes, V), device)
+
+
+def accept_sampled(parent, tok, p_logits, node_off, u_node, race, q_prob=None, drawn=None, temperature=None, top_k=None,
+                   top_p=None, max_nodes=None, max_depth=None, ws=None, outputs=None):
+    """Verifies drafted tokens against the target's distribution at each request's ``temperature`` float32 [B], ``top_k``
+    int32 [B] and ``top_p`` float32 [B].  p_logits [n, V] (row stride free); ``q_prob`` float32 [n, V]: what a node's
+    drawn children came from; ``drawn`` uint8 [n] (None: all, if q_prob is given); ``u_node`` float32 [n] uniforms;
+    ``race`` float32 [B, V] exponential variates.  Returns accept_len, best_node int32 [B], path int32
+    [B, max_depth + 1], bonus int32 [B]."""
+    n, V = p_logits.shape
+    dev = p_logits.get_device()
+    dt = _act_dtype(p_logits, "p_logits")
+    B = node_off.numel() - 1
+    if max_nodes is None:
+        max_nodes = min(n, MAX_NODES)
+    if max_depth is None:
+        max_depth = max(max_nodes - 1, 0)
+    i32, f32 = torch.int32, torch.float32
+    if ws is None:
+        ws = accept_sampled_workspace(B, n, V, p_logits.device)
+    if outputs is None:
+        outputs = (*(torch.empty(B, dtype=i32, device=p_logits.device) for _ in range(2)),
+                   torch.empty((B, max_depth + 1), dtype=i32, device=p_logits.device),
+                   torch.empty(B, dtype=i32, device=p_logits.device))
+    acc, best, path, bonus = outputs
+    pp, ld = _logit_rows(p_logits, "p_logits", p_logits.dtype, dev, n, V)
+    pq, ldq = _logit_rows(q_prob, "q_prob", f32, dev, n, V) if q_prob is not None else (None, 0)
+    pr, ldr = _logit_rows(race, "race", f32, dev, B, V)
+    _call_on(dev, "accept_sampled", _dense(parent, "parent", i32, dev, (n,)), _dense(tok, "tok", i32, dev, (n,)), pp, dt, V,
+             ld, pq, ldq, _dense(drawn, "drawn", torch.uint8, dev, (n,)),
+             _dense(node_off, "node_off", i32, dev, (B + 1,)), B, max_nodes, n, max_depth,
+             _dense(temperature, "temperature", f32, dev, (B,)), _dense(top_k, "top_k", i32, dev, (B,)),
+             _dense(top_p, "top_p", f32, dev, (B,)), _dense(u_node, "u_node", f32, dev, (n,)), pr, ldr,
+             _dense(acc, "accept_len", i32, dev, (B,)), _dense(best, "best_node", i32, dev, (B,)),
+             _dense(path, "path", i32, dev, (B, max_depth + 1)), _dense(bonus, "bonus", i32, dev, (B,)),
+             _dense(ws, "ws", torch.uint8, dev, (ws.numel(),)), ws.numel())
+    return acc, best, path, bonus

@@ -1,0 +1,408 @@
+// Eviction from the paged 4-bit cache: kv4_evict_select chooses the tokens that
+// a request keeps by their accumulated weights, kv4_compact moves them
+// together.  Every KV head keeps tokens of its own, all heads of a request the
+// same number.
+#include <algorithm>
+
+#include "cluster.cuh"
+#include "kv4.cuh"
+
+namespace tv {
+namespace kv4 {
+namespace {
+
+// -------------------------------------------------------------------- select
+struct SelectArgs {
+  const float* score;
+  const int32_t* cache_len;
+  const int32_t* budget;
+  int32_t* idx;
+  float* score_out;
+  int32_t* new_len;
+  int32_t* err;
+  int64_t score_ld, idx_ld, out_ld;
+  int n_sink, n_recent, Hkv, max_len, slice;
+};
+
+// Order of the scores as unsigned integers: zeros alike, NaN below all.
+__device__ __forceinline__ uint32_t score_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return x == x ? b ^ (b >> 31 ? 0xffffffffu : 0x80000000u) : 0u;
+}
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 256;
+
+// A cluster of up to 8 CTAs = one (request, KV head); each CTA stages a slice
+// of the row of scores in shared memory, so that the row is read once and
+// score_out may be the same array.  The threshold is found by four passes over
+// eight bits of the key each (counts per digit, added over the cluster), then
+// kept tokens get their places from counts in index order, ties included.
+// Latency bound: 64 x 8 rows of 512..4096 scores and one row set of 131072.
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const uint32_t csize) {
+  extern __shared__ float xs[];
+  __shared__ uint32_t hist[2][kBins];
+  __shared__ uint32_t tot[kBins];
+  __shared__ uint32_t pub[2][2];                       // kept-for-sure and tied tokens of this CTA's slice
+  __shared__ uint32_t wsum[kSelWarps][2];
+  __shared__ uint32_t s_key, s_need;
+  griddep_wait();
+  griddep_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cl::rank();
+  const int r = blockIdx.z, h = blockIdx.y;
+  const int64_t row = static_cast<int64_t>(r) * a.Hkv + h;
+  const int len = a.cache_len[r], want = a.budget[r];
+  const bool bad = len < 0 || len > a.max_len;
+  int n = bad ? 0 : min(len, max(want, 0));
+  const bool cut = n > a.idx_ld;
+  if (cut) n = static_cast<int>(a.idx_ld);
+  if (rank == 0 && h == 0 && tid == 0) {
+    a.new_len[r] = bad ? len : n;
+    if ((bad || cut || want < 0) && a.err) *a.err = 1;
+  }
+  int32_t* idx = a.idx + row * a.idx_ld;
+  for (int64_t j = n + static_cast<int64_t>(rank) * kSelThreads + tid; j < a.idx_ld;
+       j += static_cast<int64_t>(csize) * kSelThreads)
+    idx[j] = -1;
+  if (n == 0) return;                                  // (the same in all CTAs of the cluster)
+
+  // forced tokens: [0, ms) and [len - mr, len); of those between, `rest`
+  const int ms = min(a.n_sink, n), mr = min(a.n_recent, n - ms);
+  const int mid0 = ms, mid1 = len - mr, rest = n - ms - mr;
+  const int i0 = min(len, static_cast<int>(rank) * a.slice), i1 = min(len, i0 + a.slice);
+  const float* src = a.score + row * a.score_ld;
+  for (int i = i0 + tid; i < i1; i += kSelThreads) xs[i - i0] = src[i];
+
+  // the `rest`-th highest key between, and how many of its equals are taken
+  uint32_t key = 0, need = 0xffffffffu;                // everything between
+  if (rest < mid1 - mid0) {
+    if (rest == 0) {
+      key = 0xffffffffu;                               // (above every key)
+      need = 0;
+    } else {
+      uint32_t left = rest;
+      const int j0 = max(i0, mid0), j1 = min(i1, mid1);
+      key = 0;
+      for (int b = tid; b < kBins; b += kSelThreads) hist[0][b] = 0;
+      __syncthreads();
+      for (int pass = 0; pass < 4; ++pass) {
+        const int sh = 24 - 8 * pass;
+        uint32_t* hs = hist[pass & 1];
+        for (int i = j0 + tid; i < j1; i += kSelThreads) {
+          const uint32_t k = score_key(xs[i - i0]);
+          if (pass == 0 || (k >> (sh + 8)) == (key >> (sh + 8))) atomicAdd(&hs[(k >> sh) & 255u], 1u);
+        }
+        if (csize > 1) cl::sync();
+        else __syncthreads();
+        if (tid < kBins) {
+          uint32_t t = 0;
+          for (uint32_t c = 0; c < csize; ++c) t += csize > 1 ? cl::peek(&hs[tid], c) : hs[tid];
+          tot[tid] = t;
+          hist[(pass & 1) ^ 1][tid] = 0;               // (its readers passed this pass's barrier)
+        }
+        __syncthreads();
+        if (warp == 0) {
+          // digits from the highest: lane l owns 255 - 8 l .. 248 - 8 l
+          uint32_t mine = 0, v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mine += v[u] = tot[255 - 8 * lane - u];
+          uint32_t inc = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          uint32_t before = inc - mine;
+          if (before < left && left <= inc) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (before < left && left <= before + v[u]) {
+                s_key = key | (static_cast<uint32_t>(255 - 8 * lane - u) << sh);
+                s_need = left - before;
+              }
+              before += v[u];
+            }
+          }
+        }
+        __syncthreads();
+        key = s_key;
+        left = s_need;
+      }
+      need = left;
+    }
+  }
+  __syncthreads();
+
+  // places: a warp owns a run of the slice
+  const int run = ((i1 - i0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int w0 = min(i1, i0 + warp * run), w1 = min(i1, w0 + run);
+  auto sure = [&](int i, uint32_t k) { return i < mid0 || i >= mid1 || k > key; };
+  uint32_t n_sure = 0, n_tie = 0;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = score_key(xs[i - i0]);
+    const bool s = sure(i, k);
+    n_sure += s;
+    n_tie += !s && k == key;
+  }
+  n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+  n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+  if (lane == 0) { wsum[warp][0] = n_sure; wsum[warp][1] = n_tie; }
+  __syncthreads();
+  uint32_t at_sure = 0, at_tie = 0;
+  for (int w = 0; w < warp; ++w) { at_sure += wsum[w][0]; at_tie += wsum[w][1]; }
+  if (csize > 1) {
+    if (tid == 0) {
+      uint32_t s = 0, t = 0;
+      for (int w = 0; w < kSelWarps; ++w) { s += wsum[w][0]; t += wsum[w][1]; }
+      pub[0][0] = s;
+      pub[0][1] = t;
+    }
+    cl::sync();                                        // (also: every score is staged before one is written)
+    for (uint32_t c = 0; c < rank; ++c) { at_sure += cl::peek(&pub[0][0], c); at_tie += cl::peek(&pub[0][1], c); }
+  }
+  float* out = a.score_out ? a.score_out + row * a.out_ld : nullptr;
+  for (int b = w0; b < w1; b += 32) {
+    const int i = b + lane;
+    const bool in = i < w1;
+    const float x = in ? xs[i - i0] : 0.f;
+    const uint32_t k = score_key(x);
+    const bool s = in && sure(i, k), t = in && !s && k == key;
+    const unsigned ms_ = __ballot_sync(0xffffffffu, s), mt = __ballot_sync(0xffffffffu, t);
+    const unsigned below = (1u << lane) - 1u;
+    const uint32_t ties = at_tie + __popc(mt & below);
+    if (s || (t && ties < need)) {
+      const uint32_t j = at_sure + __popc(ms_ & below) + min(ties, need);
+      idx[j] = i;
+      if (out) out[j] = x;
+    }
+    at_sure += __popc(ms_);
+    at_tie += __popc(mt);
+  }
+  if (csize > 1) cl::sync();                           // no CTA leaves while another may read its shared memory
+}
+
+// ------------------------------------------------------------------- compact
+struct CompactArgs {
+  uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* dst_table;     // NULL: in place
+  const int32_t* cache_len;
+  const int32_t* new_len;
+  const int32_t* idx;
+  int32_t* err;
+  int64_t idx_ld;
+  int n_pages, P, table_ld, dst_ld, Hkv, max_keep;
+};
+
+constexpr int kWin = 64;        // tokens that D threads move at a time
+
+// D threads move a window of 64 kept tokens of one (request, KV head): keys
+// and scales token by token in 16-byte units, values dim by dim (thread = dim):
+// the 16 nibbles of a destination word are picked from the words of their
+// source groups.  A group of the destination belongs to one window, so words
+// are written whole; nibbles of tokens that do not move are kept.
+//   kInPlace: the windows of a (request, KV head) are taken in order by one
+//   cluster, blockDim.y windows to a CTA at a time.  Kept tokens only move
+//   towards the front, so what one round writes lies before all that later
+//   rounds read; one cluster barrier between a round's reads and its writes
+//   makes that hold inside the round too.
+//   else: every window is a CTA of its own.
+template <int D, bool kInPlace>
+__global__ void __launch_bounds__(kInPlace ? 4 * D : D) compact_kernel(const CompactArgs a) {
+  __shared__ int64_t s_block[4][kWin];    // byte offset of a token's source block, -1: does not move
+  __shared__ int s_slot[4][kWin];
+  griddep_wait();
+  griddep_release();
+  const int dim = threadIdx.x, y = threadIdx.y;
+  const int r = blockIdx.z, h = blockIdx.y;
+  const int len = a.cache_len[r];
+  int n = a.new_len[r];
+  const int64_t cap = static_cast<int64_t>(a.table_ld) * a.P;
+  const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.table_ld;
+  const int32_t* dtable = kInPlace ? table : a.dst_table + static_cast<int64_t>(r) * a.dst_ld;
+  const int dld = kInPlace ? a.table_ld : a.dst_ld;
+  const int32_t* idx = a.idx + (static_cast<int64_t>(r) * a.Hkv + h) * a.idx_ld;
+  if (n > a.max_keep || n < 0) {
+    if (blockIdx.x == 0 && h == 0 && dim == 0 && y == 0 && a.err) *a.err = 1;
+    n = max(0, min(n, a.max_keep));
+  }
+  constexpr int kUnits = kWin * (D / 32) / D;   // 16-byte units of keys per thread: 2
+  for (int w = kInPlace ? (blockIdx.x * blockDim.y) : blockIdx.x;; w += gridDim.x * blockDim.y) {
+    // a CTA of a cluster stays for the barriers as long as any of its CTAs has a window
+    if ((kInPlace ? w - static_cast<int>(blockIdx.x * blockDim.y) : w) * kWin >= n) return;
+    const int j0 = (w + y) * kWin;
+    bool bad = false;
+    for (int i = dim; i < kWin; i += D) {
+      const int j = j0 + i;
+      int64_t blk = -1;
+      int slot = 0;
+      if (j < n) {
+        const int t = idx[j];
+        bad = true;
+        if (t >= 0 && t < len && t < cap) {
+          const int page = table[t / a.P];
+          if (page >= 0 && page < a.n_pages) {
+            bad = false;
+            slot = t % a.P;
+            if (!kInPlace || t != j) blk = (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
+          }
+        }
+      }
+      s_block[y][i] = blk;
+      s_slot[y][i] = slot;
+    }
+    __syncthreads();
+    // reads
+    uint4 kc[kUnits];
+    uint2 vw[kWin / 16], vmask[kWin / 16];
+    uint16_t sc[2 * kWin / D];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = u * D + dim, i = unit % kWin, c = unit / kWin;
+      const int64_t blk = s_block[y][i];
+      if (blk >= 0) kc[u] = *reinterpret_cast<const uint4*>(a.cache + blk + k_word(a.P, s_slot[y][i], 32 * c));
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * kWin / D; ++u) {
+      const int unit = u * D + dim, i = unit % kWin;
+      const int64_t blk = s_block[y][i];
+      if (blk >= 0)
+        sc[u] = *reinterpret_cast<const uint16_t*>(
+            a.cache + blk + (unit < kWin ? k_scale(a.P, D, s_slot[y][i]) : v_scale(a.P, D, s_slot[y][i])));
+    }
+#pragma unroll
+    for (int q = 0; q < kWin / 16; ++q) {
+      uint32_t word[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t blk = s_block[y][16 * q + e];
+        const int s = s_slot[y][16 * q + e];
+        word[e] = 0;
+        if (blk >= 0)
+          word[e] = *reinterpret_cast<const uint32_t*>(a.cache + blk + v_group(a.P, D, s >> 4, dim) + ((s >> 3) & 1) * 4);
+      }
+      uint32_t v[2] = {0u, 0u}, m[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t blk = s_block[y][16 * q + e];
+        const int s = s_slot[y][16 * q + e] & 7;
+        const int to = 4 * nibble_of(e & 7);
+        v[e >> 3] |= ((word[e] >> (4 * nibble_of(s))) & 15u) << to;
+        if (blk >= 0) m[e >> 3] |= 15u << to;
+      }
+      vw[q] = make_uint2(v[0], v[1]);
+      vmask[q] = make_uint2(m[0], m[1]);
+    }
+    if constexpr (kInPlace) cl::sync();
+    // writes
+    auto target = [&](int j) -> uint8_t* {
+      const int pg = j / a.P;
+      const int page = pg < dld ? dtable[pg] : -1;
+      if (page < 0 || page >= a.n_pages) {
+        bad = true;
+        return nullptr;
+      }
+      return a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
+    };
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = u * D + dim, i = unit % kWin, c = unit / kWin;
+      if (s_block[y][i] < 0) continue;
+      if (uint8_t* blk = target(j0 + i)) *reinterpret_cast<uint4*>(blk + k_word(a.P, (j0 + i) % a.P, 32 * c)) = kc[u];
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * kWin / D; ++u) {
+      const int unit = u * D + dim, i = unit % kWin;
+      if (s_block[y][i] < 0) continue;
+      if (uint8_t* blk = target(j0 + i))
+        *reinterpret_cast<uint16_t*>(blk + (unit < kWin ? k_scale(a.P, D, (j0 + i) % a.P)
+                                                        : v_scale(a.P, D, (j0 + i) % a.P))) = sc[u];
+    }
+#pragma unroll
+    for (int q = 0; q < kWin / 16; ++q) {
+      if ((vmask[q].x | vmask[q].y) == 0u) continue;
+      const int j = j0 + 16 * q;
+      if (uint8_t* blk = target(j)) {
+        uint2* dst = reinterpret_cast<uint2*>(blk + v_group(a.P, D, j % a.P / 16, dim));
+        uint2 v = vw[q];
+        if ((vmask[q].x & vmask[q].y) != 0xffffffffu) {
+          const uint2 old = *dst;
+          v.x |= old.x & ~vmask[q].x;
+          v.y |= old.y & ~vmask[q].y;
+        }
+        *dst = v;
+      }
+    }
+    if (bad && a.err) *a.err = 1;
+    if constexpr (!kInPlace) return;
+    __syncthreads();                                   // (the next round rewrites s_block)
+  }
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace tv
+
+using namespace tv;
+
+namespace {
+// CTAs of a cluster of select_kernel: as many as leave each a slice of at most
+// 4096 scores, at most 8.
+constexpr int kSlice = 4096, kMaxSlice = 49152;
+int select_cluster(int max_len) {
+  int c = 1;
+  while (c < 8 && (max_len + c - 1) / c > kSlice) c *= 2;
+  return c;
+}
+}  // namespace
+
+TV_API int kv4_evict_select(const float* score, int64_t score_ld, const int32_t* cache_len, const int32_t* budget,
+                            int n_sink, int n_recent, int B, int Hkv, int max_len, int32_t* idx, int64_t idx_ld,
+                            float* score_out, int64_t score_out_ld, int32_t* new_len, int32_t* err,
+                            tv_stream_t stream) {
+  if (B < 0 || Hkv <= 0 || max_len < 0 || n_sink < 0 || n_recent < 0 || idx_ld < 0 || score_ld < max_len)
+    return TV_EINVAL;
+  if (score_out && score_out_ld < std::min<int64_t>(idx_ld, max_len)) return TV_EINVAL;
+  if (B > 65535 || Hkv > 65535 || max_len > 8 * kMaxSlice) return TV_EUNSUPPORTED;
+  if (B == 0) return TV_OK;
+  if (!cache_len || !budget || !new_len || new_len == cache_len) return TV_EINVAL;
+  if ((max_len > 0 && !score) || (idx_ld > 0 && !idx)) return TV_EINVAL;
+  if (score_out == score && score_out_ld != score_ld) return TV_EINVAL;
+  const int c = select_cluster(max_len), slice = (max_len + c - 1) / c;
+  const int bytes = std::max(slice, 1) * 4;
+  if (bytes > 40 << 10 && !smem_limit(kv4::select_kernel, kMaxSlice * 4)) return TV_ECUDA;
+  const kv4::SelectArgs a{score, cache_len, budget, idx, score_out, new_len, err, score_ld, idx_ld, score_out_ld,
+                          n_sink, n_recent, Hkv, max_len, slice};
+  return cl::launch_pdl(kv4::select_kernel, c, dim3(c, Hkv, B), dim3(kv4::kSelThreads), bytes,
+                        reinterpret_cast<cudaStream_t>(stream), a, static_cast<uint32_t>(c));
+}
+
+TV_API int kv4_compact(void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
+                       const int32_t* cache_len, const int32_t* idx, int64_t idx_ld, const int32_t* new_len, int B,
+                       int max_keep, const int32_t* dst_table, int dst_ld, int Hkv, int d, int32_t* err,
+                       tv_stream_t stream) {
+  if (B < 0 || max_keep < 0 || n_pages < 0 || table_ld < 0 || dst_ld < 0 || Hkv <= 0 || page_size <= 0 || idx_ld < 0)
+    return TV_EINVAL;
+  if (!kv4::page_size_ok(page_size) || (d != 64 && d != 128)) return TV_EUNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || static_cast<int64_t>(table_ld) * page_size > 0x7fffffffll ||
+      static_cast<int64_t>(dst_ld) * page_size > 0x7fffffffll || max_keep > 0x7fffffff - 4096)
+    return TV_EUNSUPPORTED;
+  if (max_keep > idx_ld) return TV_EINVAL;
+  if (B == 0 || max_keep == 0) return TV_OK;
+  if (!cache || !block_table || !cache_len || !idx || !new_len || !aligned(cache, 16)) return TV_EINVAL;
+  const kv4::CompactArgs a{static_cast<uint8_t*>(cache), block_table, dst_table, cache_len, new_len, idx, err, idx_ld,
+                           n_pages, page_size, table_ld, dst_ld, Hkv, max_keep};
+  const int windows = (max_keep + kv4::kWin - 1) / kv4::kWin;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dst_table)
+    return d == 128 ? launch_pdl(kv4::compact_kernel<128, false>, dim3(windows, Hkv, B), dim3(128), 0, st, a)
+                    : launch_pdl(kv4::compact_kernel<64, false>, dim3(windows, Hkv, B), dim3(64), 0, st, a);
+  // in place: four windows to a CTA, clusters large enough that the (request, head) pairs fill the SMs
+  int c = 1;
+  while (c < 8 && 4 * c < windows && static_cast<int64_t>(B) * Hkv * c < 2ll * sm_count()) c *= 2;
+  return d == 128
+             ? cl::launch_pdl(kv4::compact_kernel<128, true>, c, dim3(c, Hkv, B), dim3(128, 4), 0, st, a)
+             : cl::launch_pdl(kv4::compact_kernel<64, true>, c, dim3(c, Hkv, B), dim3(64, 4), 0, st, a);
+}
