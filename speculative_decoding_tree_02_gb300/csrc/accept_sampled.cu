@@ -9,6 +9,8 @@
 // and for the last token.  Rejections only ever turn the distribution into
 // max(0, a p - b q) without the tokens that were removed, so two numbers and a
 // bit mask stand for it and no row is written.
+#include <cuda_bf16.h>
+
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -82,12 +84,22 @@ struct RowArgs {
   bool vec;
 };
 
+constexpr int kList = 512;         // listed logits of a warp
+constexpr int kSort = 1024;        // listed logits of a row
+constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
+constexpr int kScratch = kBins * kAsThreads * 4;
+static_assert(kScratch / 2 == kAsWarps * kList * 4, "the lists fill the second half of the scratch");
+
 struct RowShared {
-  float xf[2][kBins];            // exchanged with the cluster, by parity
+  float xf[2][kBins];              // exchanged with the cluster, by parity
   int xi[2][2];
   float tot[kBins];
   float wred[kAsWarps];
   int wred_i[kAsWarps];
+  int listed[kAsWarps];            // logits that passed the list's condition, per warp
+  float scan[kAsWarps];
+  int hit;
+  float out;                       // what the first CTA found
 };
 
 // Sums over the cluster of up to 32 numbers that lie in sh.xf[e & 1] of each
@@ -112,11 +124,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 // The bin in which the running sum over tot[0], tot[1], .. reaches `target`
 // (the last one with anything in it, if none does), and the sum before it.
-__device__ __forceinline__ int crossing(const float* tot, float target, float before, float& above) {
+__device__ __forceinline__ int crossing(const float* tot, int n, float target, float before, float& above) {
   int at = 0;
   float run = before;
   above = before;
-  for (int b = 0; b < kBins; ++b) {
+  for (int b = 0; b < n; ++b) {
     const float t = tot[b];
     if (t > 0.f) {
       at = b;
@@ -128,8 +140,74 @@ __device__ __forceinline__ int crossing(const float* tot, float target, float be
   return at;
 }
 
+// Eight staged logits, free of NaN and +inf.
+__device__ __forceinline__ void staged8(const uint16_t* xs, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(xs);
+  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void staged8(const float* xs, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(xs), b = *reinterpret_cast<const float4*>(xs + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+// Stages eight logits (NaN as -inf, +inf as the largest number); their maximum.
+__device__ __forceinline__ float stage8(uint16_t* xs, const float (&x)[8]) {
+  const __nv_bfloat162 lo = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
+  const __nv_bfloat162 hi = __halves2bfloat162(__ushort_as_bfloat16(0x7f7f), __ushort_as_bfloat16(0x7f7f));
+  uint32_t w[4];
+  __nv_bfloat162 m = lo;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w[e] = (__float_as_uint(x[2 * e]) >> 16) | (__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
+    const __nv_bfloat162 v = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), lo), hi);
+    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+    m = __hmax2(m, v);
+  }
+  *reinterpret_cast<uint4*>(xs) = make_uint4(w[0], w[1], w[2], w[3]);
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float stage8(float* xs, const float (&x)[8]) {
+  float y[8], m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = fminf(fmaxf(x[e], -INFINITY), 3.402823466e38f);
+    m = fmaxf(m, y[e]);
+  }
+  *reinterpret_cast<float4*>(xs) = make_float4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<float4*>(xs + 4) = make_float4(y[4], y[5], y[6], y[7]);
+  return m;
+}
+
+// By the CTA: sorts v[0, n) (n <= kSort), highest first; v has room for the next power of two.
+__device__ __forceinline__ void sort_desc(float* v, int n) {
+  int n2 = 2;
+  while (n2 < n) n2 *= 2;
+  for (int i = n + threadIdx.x; i < n2; i += kAsThreads) v[i] = -INFINITY;
+  for (int k = 2; k <= n2; k *= 2)
+    for (int j = k / 2; j; j /= 2) {
+      __syncthreads();
+      for (int t = threadIdx.x; t < n2 / 2; t += kAsThreads) {
+        const int i = 2 * j * (t / j) + t % j;
+        const float x = v[i], y = v[i + j];
+        if ((x < y) == ((i & k) == 0)) { v[i] = y; v[i + j] = x; }
+      }
+    }
+  __syncthreads();
+}
+
+// One row of logits: a cluster of 8 CTAs.  The slice of a CTA is staged in
+// shared memory and read once from there in most calls: the highest logit is
+// known by then, so one pass sums the weights and lists those above 2^-12 of
+// the highest, a handful in a peaked distribution; the first CTA sorts the
+// lists of all and finds the threshold by a prefix sum while the others leave.
+// Where the list does not reach the threshold (flat distributions, large k)
+// or overflows, the logits are binned by powers of two of the weight, the
+// threshold's bin by 32nd parts of it, twice, until a bin is short enough to
+// be listed; ties beyond that are told apart by four bits of the ordered bits
+// at a time.  All sums have a fixed order.
 template <typename T, bool kTrunc>
-__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads) row_kernel(const RowArgs a) {
+__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads, 3) row_kernel(const RowArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowShared sh;
   griddep_wait();
@@ -145,7 +223,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   const int v0 = min(V, static_cast<int>(rank) * S), v1 = min(V, v0 + S);
   const float temp = a.temperature ? a.temperature[r] : 1.f;
   const bool greedy = !(temp > 0.f);
-  const float c = fminf(kLog2e / temp, 1e30f);
+  const float c = fmaxf(fminf(kLog2e / temp, 1e30f), 1e-30f);
   int k = kTrunc && a.top_k ? a.top_k[r] : 0;
   if (k >= V) k = 0;
   const float nucleus = kTrunc && a.top_p ? a.top_p[r] : 1.f;
@@ -159,6 +237,12 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   for (int v = v0 + 8 * tid; v < v1; v += 8 * kAsThreads) {
     float x[8];
     load8(p, v, v1, a.vec, x);
+    if constexpr (kTrunc) {
+      if (stage) {
+        m = fmaxf(m, stage8(xs + (v - v0), x));
+        continue;
+      }
+    }
     float m8 = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) m8 = fmaxf(m8, x[e]);
@@ -168,21 +252,6 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
 #pragma unroll
         for (int e = 7; e >= 0; --e)
           if (x[e] == m8) at = v + e;
-      }
-      continue;
-    }
-    if (stage) {
-      m = fmaxf(m, m8);
-      if constexpr (kTrunc) {
-        if constexpr (sizeof(T) == 2) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(x[2 * e]) >> 16) | (__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
-          *reinterpret_cast<uint4*>(xs + (v - v0)) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          *reinterpret_cast<float4*>(xs + (v - v0)) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(xs + (v - v0) + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
       }
       continue;
     }
@@ -201,9 +270,9 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   const int wi = __reduce_min_sync(0xffffffffu, m == wm && greedy ? at : 0x7fffffff);
   if (lane == 0) sh.wred_i[warp] = wi;
   __syncthreads();
-  float top = sh.wred[0];
-  for (int w = 1; w < kAsWarps; ++w) top = fmaxf(top, sh.wred[w]);
   if (tid == 0) {
+    float top = sh.wred[0];
+    for (int w = 1; w < kAsWarps; ++w) top = fmaxf(top, sh.wred[w]);
     int first = 0x7fffffff;
     for (int w = 0; w < kAsWarps; ++w)
       if (sh.wred[w] == top) first = min(first, sh.wred_i[w]);
@@ -213,6 +282,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   cl::sync();
   float all = -INFINITY;
   int first = 0x7fffffff;
+#pragma unroll
   for (uint32_t q = 0; q < kAsCluster; ++q) {
     const float t = cl::peek(&sh.xf[e & 1][0], q);
     const int f = cl::peek(&sh.xi[e & 1][0], q);
@@ -230,146 +300,323 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
     cl::sync();                                   // no CTA leaves while another may read its shared memory
     return;
   }
-  const float mine = m;
-  top = fminf(all, 3.402823466e38f);
+  const float top = fminf(all, 3.402823466e38f);
   out.top = top;
   float mass = 0.f;
-  if (!stage) {
-    if (mine == -INFINITY) s = 0.f;
-    else s *= ex2(fmaxf((mine - top) * c, -1e30f));
-    s = warp_sum(s);
-    if (lane == 0) sh.wred[warp] = s;
+  // sum of a number per thread over the cluster
+  auto total = [&](float x) {
+    x = warp_sum(x);
+    if (lane == 0) sh.wred[warp] = x;
     __syncthreads();
     if (tid == 0) {
-      float t = 0.f;
-      for (int w = 0; w < kAsWarps; ++w) t += sh.wred[w];
-      sh.xf[e & 1][0] = t;
+      x = 0.f;
+      for (int w = 0; w < kAsWarps; ++w) x += sh.wred[w];
+      sh.xf[e & 1][0] = x;
     }
     cluster_sums(sh, e++, 1);
-    mass = sh.tot[0];
+    return sh.tot[0];
+  };
+  if (!stage) {
+    if (m == -INFINITY) s = 0.f;
+    else s *= ex2(fmaxf((m - top) * c, -1e30f));
+    mass = total(s);
   }
   if constexpr (kTrunc) {
     if (stage && all > -INFINITY) {
       float* hist = reinterpret_cast<float*>(dyn + ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)));
+      float* list = hist + kScratch / 8;          // second half: a run for each warp
+      const int n = v1 - v0, rounds = (n + 8 * kAsThreads - 1) / (8 * kAsThreads);
+      auto weight = [&](float l) { return ex2((l - top) * c); };
       // fn(l) of every staged logit of this thread
       auto each = [&](auto&& fn) {
-        for (int v = 8 * tid; v < v1 - v0; v += 8 * kAsThreads) {
-          if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4*>(xs + v);
-            fn(bf16_lo(w.x)); fn(bf16_hi(w.x)); fn(bf16_lo(w.y)); fn(bf16_hi(w.y));
-            fn(bf16_lo(w.z)); fn(bf16_hi(w.z)); fn(bf16_lo(w.w)); fn(bf16_hi(w.w));
-          } else {
-            const float4 w = *reinterpret_cast<const float4*>(xs + v), y = *reinterpret_cast<const float4*>(xs + v + 4);
-            fn(w.x); fn(w.y); fn(w.z); fn(w.w);
-            fn(y.x); fn(y.y); fn(y.z); fn(y.w);
-          }
+        for (int v = 8 * tid; v < n; v += 8 * kAsThreads) {
+          float x[8];
+          staged8(xs + v, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fn(x[j]);
         }
       };
-      // sums of fn's values per bin over the cluster, into sh.tot: every thread adds in a column of its own
-      auto bins = [&](auto&& add) {
+      // Lists the logits in [lo, hi], warp by warp, in a fixed order; adds
+      // the weights of all logits to z and of the listed ones to zl, if asked.
+      auto make_list = [&](float lo, float hi, bool sum, float& z, float& zl) {
+        int cnt = 0;
+        for (int q = 0; q < rounds; ++q) {
+          const int v = 8 * (q * kAsThreads + tid);
+          float x[8];
+          if (v < n) {
+            staged8(xs + v, x);
+          } else {
 #pragma unroll
-        for (int b = 0; b < kBins; ++b) hist[b * kAsThreads + tid] = 0.f;
+            for (int j = 0; j < 8; ++j) x[j] = -INFINITY;
+          }
+          if (sum) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = weight(x[j]);
+            z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+          }
+          const float m8 = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+          if (!__any_sync(0xffffffffu, m8 >= lo) || cnt > kList) continue;
+          uint32_t in = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) in |= (x[j] >= lo && x[j] <= hi ? 1u : 0u) << j;
+          for (unsigned lanes = __ballot_sync(0xffffffffu, in != 0u); lanes; lanes &= lanes - 1u) {
+            const int src = __ffs(static_cast<int>(lanes)) - 1;
+            const int more = __popc(__shfl_sync(0xffffffffu, in, src));
+            if (lane == src) {
+              int to = cnt;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (in >> j & 1u) {
+                  if (to < kList) list[warp * kList + to] = x[j];
+                  ++to;
+                  if (sum) zl += weight(x[j]);
+                }
+            }
+            cnt += more;
+          }
+        }
+        if (lane == 0) sh.listed[warp] = cnt;
+      };
+      // After a cluster barrier: logits on the cluster's lists, -1 when one overflowed or they are too many.
+      int c0, c1;                                 // lane l: the counts of segments l and l + 32 of the 64
+      auto usable = [&]() {
+        c0 = cl::peek(&sh.listed[lane & 7], lane >> 3);
+        c1 = cl::peek(&sh.listed[lane & 7], 4 + (lane >> 3));
+        const bool over = __any_sync(0xffffffffu, c0 > kList || c1 > kList);
+        const int sum = __reduce_add_sync(0xffffffffu, min(c0, kList) + min(c1, kList));
+        return over || sum > kSort ? -1 : sum;
+      };
+      // The first CTA copies the lists of all to the start of its scratch: warp w the segments of CTA w.
+      auto copy = [&]() {
+        int at[8], end = 0;
+        const int before = __reduce_add_sync(0xffffffffu, ((lane >> 3) < warp ? c0 : 0) + (4 + (lane >> 3) < warp ? c1 : 0));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          at[q] = end;
+          end += __shfl_sync(0xffffffffu, warp < 4 ? c0 : c1, 8 * (warp & 3) + q);
+        }
+        for (int t = lane; t < end; t += 32) {
+          int q = 0, o = 0;
+#pragma unroll
+          for (int u = 1; u < 8; ++u)
+            if (t >= at[u]) { q = u; o = at[u]; }
+          hist[before + t] = cl::peek(&list[q * kList + t - o], warp);
+        }
+      };
+      // Prefix sums of the sorted list's weights: into hist[kSort ..].
+      const float* pre = hist + kSort;
+      auto prefix = [&](int cnt) {
+        float w[kSort / kAsThreads], t = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSort / kAsThreads; ++j) {
+          const int q = tid * (kSort / kAsThreads) + j;
+          w[j] = t += q < cnt ? weight(hist[q]) : 0.f;
+        }
+        float inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (lane == 31) sh.scan[warp] = inc;
+        float before = __shfl_up_sync(0xffffffffu, inc, 1);
+        if (lane == 0) before = 0.f;
+        __syncthreads();
+        for (int q = 0; q < warp; ++q) before += sh.scan[q];
+#pragma unroll
+        for (int j = 0; j < kSort / kAsThreads; ++j) hist[kSort + tid * (kSort / kAsThreads) + j] = before + w[j];
+        __syncthreads();
+      };
+      // How many q < cnt have fn(q).
+      auto count = [&](int cnt, auto&& fn) {
+        if (tid == 0) sh.hit = 0;
+        __syncthreads();
+        int mine = 0;
+        for (int q = tid; q < cnt; q += kAsThreads) mine += fn(q) ? 1 : 0;
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 0 && mine) atomicAdd(&sh.hit, mine);
+        __syncthreads();
+        const int h = sh.hit;
+        __syncthreads();
+        return h;
+      };
+      // Of the sorted list (behind `above` in mass): the threshold of top-p at `target`, and the mass down to it.
+      auto settle_p = [&](int cnt, int kept, float above, float target) {
+        const int in = max(1, count(kept, [&](int q) { return above + (q ? pre[q - 1] : 0.f) < target; }));
+        out.floor = hist[in - 1];
+        const int last = count(cnt, [&](int q) { return hist[q] >= out.floor; });
+        mass = above + pre[last - 1];
+      };
+      // The lists hold every logit that matters: the first CTA finds the
+      // threshold, the others are done.
+      auto finish = [&](int cnt, float z) {
+        if (rank == 0) copy();
+        cl::sync();
+        if (rank != 0) return;
+        sort_desc(hist, cnt);
+        prefix(cnt);
+        int kept = cnt;
+        if (by_k) {
+          out.floor = hist[k - 1];
+          kept = count(cnt, [&](int q) { return hist[q] >= out.floor; });
+          mass = z = pre[kept - 1];
+        }
+        if (by_p) settle_p(cnt, kept, 0.f, nucleus * z);
+        out.inv = mass > 0.f ? 1.f / mass : 0.f;
+        if (tid == 0) a.stat[row] = out;
+      };
+
+      // ---- the highest, listed while all are summed
+      float z = 0.f, zl = 0.f;
+      make_list(top - kCut / c, INFINITY, true, z, zl);
+      {
+        const float w0 = warp_sum(z), w1 = warp_sum(zl);
+        if (lane == 0) { sh.wred[warp] = w0; sh.scan[warp] = w1; }
+        __syncthreads();
+        if (tid == 0) {
+          z = zl = 0.f;
+          for (int w = 0; w < kAsWarps; ++w) { z += sh.wred[w]; zl += sh.scan[w]; }
+          sh.xf[e & 1][0] = z;
+          sh.xf[e & 1][1] = zl;
+        }
+        cluster_sums(sh, e++, 2);
+        z = sh.tot[0];
+        zl = sh.tot[1];
+      }
+      int cnt = usable();
+      if (cnt > 0 && (by_k ? k <= cnt : zl >= nucleus * z)) {
+        finish(cnt, z);
+        return;
+      }
+
+      // ---- bins of y = (top - l) c, then of a part of them
+      // sums of values per bin over the cluster, into sh.tot: every thread adds in a column of its own
+      auto bins = [&](int nb, auto&& add) {
+        for (int b = 0; b < nb; ++b) hist[b * kAsThreads + tid] = 0.f;
         each(add);
         __syncthreads();
-        for (int b = warp; b < kBins; b += kAsWarps) {
+        for (int b = warp; b < nb; b += kAsWarps) {
           float t = 0.f;
 #pragma unroll
           for (int u = 0; u < kAsThreads / 32; ++u) t += hist[b * kAsThreads + 32 * u + lane];
           t = warp_sum(t);
           if (lane == 0) sh.xf[e & 1][b] = t;
         }
-        cluster_sums(sh, e++, kBins);
+        cluster_sums(sh, e++, nb);
       };
-      // Threshold: the lowest logit whose class is needed so that tokens
-      // counted (or weighed) from the top reach the target; the first pass
-      // bins by powers of two of the weight, the others by five bits of the
-      // ordered bits of the logits of one bin.
-      float floor_ = -INFINITY;
+      float floor_ = -INFINITY;                   // what top-k leaves
+      // The lowest logit that is needed for the tokens counted (or weighed)
+      // from the top to reach the target.  true: this CTA has nothing left to do.
       auto search = [&](bool weigh, float part) {
-        auto value = [&](float x) { return weigh ? ex2(x) : 1.f; };
-        bins([&](float l) {
-          if (l >= floor_) {
-            const float x = log_weight(l, top, c);
-            hist[min(kBins - 1, static_cast<int>(fminf(-x, 1e6f))) * kAsThreads + tid] += value(x);
+        float lo = floor_, hi = INFINITY, above = 0.f, target = part, y0 = 0.f, inv = 1.f;
+        for (int level = 0; level < 3; ++level) {
+          auto bin_of = [&](float l) { return static_cast<int>(fminf(fmaxf(((top - l) * c - y0) * inv, 0.f), kBins - 1.f)); };
+          if (weigh)
+            bins(kBins, [&](float l) {
+              if (l >= lo && l <= hi) hist[bin_of(l) * kAsThreads + tid] += weight(l);
+            });
+          else
+            bins(kBins, [&](float l) {
+              if (l >= lo && l <= hi) hist[bin_of(l) * kAsThreads + tid] += 1.f;
+            });
+          if (weigh && level == 0) {
+            float t = 0.f;
+            for (int b = 0; b < kBins; ++b) t += sh.tot[b];
+            target = part * t;
           }
-        });
-        float target = part;
-        if (weigh) {
-          float t = 0.f;
-          for (int b = 0; b < kBins; ++b) t += sh.tot[b];
-          target = part * t;
+          const int bin = crossing(sh.tot, kBins, target, above, above);
+          // at most so many logits in the bin, and down to it
+          float most = 0.f, whole = 0.f;
+          for (int b = 0; b <= bin; ++b) {
+            most = weigh ? sh.tot[b] * exp2f(y0 + (b + 1) / inv) : sh.tot[b];
+            whole += most;
+          }
+          const bool everything = level == 0 && by_k && !weigh && whole <= kSort && bin < kBins - 1;
+          // the bin's lowest and highest number, by bisection of the ordered bits
+          if (warp == 0) {
+            const bool low = lane == 0;
+            uint32_t k0 = order_key(-3.402823466e38f), k1 = order_key(top);
+            while (k0 < k1) {
+              const uint32_t mid = k0 + (k1 - k0 + (low ? 0u : 1u)) / 2u;
+              const int b = bin_of(key_value(mid));
+              if (low) {
+                if (b <= bin) k1 = mid;
+                else k0 = mid + 1u;
+              } else {
+                if (b >= bin) k0 = mid;
+                else k1 = mid - 1u;
+              }
+            }
+            if (lane == 0) sh.scan[0] = bin == kBins - 1 && level == 0 ? -INFINITY : key_value(k0);
+            if (lane == 1) sh.scan[1] = bin == 0 && level == 0 ? INFINITY : key_value(k0);
+          }
+          __syncthreads();
+          lo = fmaxf(lo, sh.scan[0]);
+          if (!everything) hi = fminf(hi, sh.scan[1]);
+          __syncthreads();
+          if (everything || most <= kSort) {
+            float u0, u1;
+            make_list(lo, hi, false, u0, u1);
+            cl::sync();
+            cnt = usable();
+            if (cnt > 0) {
+              if (everything) {
+                finish(cnt, 0.f);
+                return true;
+              }
+              if (rank == 0) copy();
+              cl::sync();                         // (this and the next: sh.out is written between two barriers)
+              if (rank == 0) {
+                sort_desc(hist, cnt);
+                if (weigh) {
+                  prefix(cnt);
+                  settle_p(cnt, cnt, above, target);
+                  out.inv = mass > 0.f ? 1.f / mass : 0.f;
+                  if (tid == 0) a.stat[row] = out;
+                } else if (tid == 0) {
+                  sh.out = hist[min(cnt, static_cast<int>(target - above)) - 1];
+                }
+              }
+              if (weigh) return true;
+              cl::sync();
+              floor_ = cl::peek(&sh.out, 0);
+              return false;
+            }
+          }
+          y0 += bin / inv;
+          inv *= kBins;
         }
-        float above;
-        const int bin = crossing(sh.tot, target, 0.f, above);
-        auto inside = [&](float l) {
-          return l >= floor_ && min(kBins - 1, static_cast<int>(fminf(-log_weight(l, top, c), 1e6f))) == bin;
-        };
-        uint32_t lo = 0xffffffffu, hi = 0;
-        each([&](float l) {
-          if (inside(l)) {
+        // flat to the last: by four bits of the ordered bits; keys in [klo, khi], those above `bits` the same in both
+        uint32_t klo = order_key(lo), khi = order_key(fminf(hi, top));
+        int bits = 32 - __clz(static_cast<int>(klo ^ khi));
+        float cls = 0.f;
+        do {
+          const int low = max(0, bits - 4);
+          const uint32_t base = bits >= 32 ? 0u : klo >> bits << bits;
+          bins(16, [&](float l) {
             const uint32_t q = order_key(l);
-            lo = min(lo, q);
-            hi = max(hi, q);
-          }
-        });
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) { sh.wred[warp] = __uint_as_float(lo); sh.wred_i[warp] = static_cast<int>(hi); }
-        __syncthreads();
-        if (tid == 0) {
-          for (int w = 1; w < kAsWarps; ++w) {
-            lo = min(lo, __float_as_uint(sh.wred[w]));
-            hi = max(hi, static_cast<uint32_t>(sh.wred_i[w]));
-          }
-          sh.xi[e & 1][0] = static_cast<int>(lo);
-          sh.xi[e & 1][1] = static_cast<int>(hi);
-        }
-        cl::sync();
-        lo = 0xffffffffu;
-        hi = 0;
-        for (uint32_t q = 0; q < kAsCluster; ++q) {
-          lo = min(lo, static_cast<uint32_t>(cl::peek(&sh.xi[e & 1][0], q)));
-          hi = max(hi, static_cast<uint32_t>(cl::peek(&sh.xi[e & 1][1], q)));
-        }
-        ++e;
-        // keys in [lo, hi]; bits above `bits` are the same in both
-        int bits = 32 - __clz(static_cast<int>(lo ^ hi));
-        float cls = sh.tot[bin];                  // (what a single class weighs, once bits is 0)
-        while (bits > 0) {
-          const int sh_ = max(0, bits - 5);
-          const uint32_t base = bits >= 32 ? 0u : lo >> bits << bits;
-          bins([&](float l) {
-            const uint32_t q = order_key(l);
-            if (l >= floor_ && q >= lo && q <= hi)
-              hist[(kBins - 1 - static_cast<int>((q - base) >> sh_)) * kAsThreads + tid] += value(log_weight(l, top, c));
+            if (q >= klo && q <= khi)
+              hist[(15 - static_cast<int>((q - base) >> low)) * kAsThreads + tid] += weigh ? weight(l) : 1.f;
           });
-          const float before = above;
-          const int d = kBins - 1 - crossing(sh.tot, target, before, above);
-          cls = sh.tot[kBins - 1 - d];
-          const uint32_t l2 = base + (static_cast<uint32_t>(d) << sh_), h2 = l2 + ((1u << sh_) - 1u);
-          lo = max(lo, l2);
-          hi = min(hi, h2);
-          bits = sh_;
-        }
-        floor_ = key_value(lo);
+          const int d = 15 - crossing(sh.tot, 16, target, above, above);
+          cls = sh.tot[15 - d];
+          const uint32_t l2 = base + (static_cast<uint32_t>(d) << low), h2 = l2 + ((1u << low) - 1u);
+          klo = max(klo, l2);
+          khi = min(khi, h2);
+          bits = low;
+        } while (bits > 0);
+        floor_ = key_value(klo);
         mass = above + cls;
+        return false;
       };
-      if (by_k) search(false, static_cast<float>(k));
+      if (by_k && search(false, static_cast<float>(k))) return;
       if (by_p) {
-        search(true, nucleus);
+        if (search(true, nucleus)) return;
       } else {                                    // the mass of the k highest
         float t = 0.f;
-        each([&](float l) { t += l >= floor_ ? ex2(log_weight(l, top, c)) : 0.f; });
-        t = warp_sum(t);
-        if (lane == 0) sh.wred[warp] = t;
-        __syncthreads();
-        if (tid == 0) {
-          t = 0.f;
-          for (int w = 0; w < kAsWarps; ++w) t += sh.wred[w];
-          sh.xf[e & 1][0] = t;
-        }
-        cluster_sums(sh, e++, 1);
-        mass = sh.tot[0];
+        each([&](float l) { t += l >= floor_ ? weight(l) : 0.f; });
+        mass = total(t);
       }
       out.floor = floor_;
     }
@@ -378,6 +625,9 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   if (rank == 0 && tid == 0) a.stat[row] = out;
   cl::sync();                                     // no CTA leaves while another may read its shared memory
 }
+
+constexpr int kWalkThreads = 512;
+constexpr int kWalkWarps = kWalkThreads / 32;
 
 struct WalkArgs {
   const int32_t* parent;
@@ -405,13 +655,13 @@ struct WalkShared {
   uint8_t flag[TV_MAX_NODES];                         // 1: drawn, 2: token removed
   float xf[2];
   int xi[2];
-  float wred[kAsWarps];
-  int wred_i[kAsWarps];
+  float wred[kWalkWarps];
+  int wred_i[kWalkWarps];
 };
 
 // A cluster of 8 CTAs walks one request's tree, all taking the same decisions.
 template <typename T>
-__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads) walk_kernel(const WalkArgs a) {
+__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThreads) walk_kernel(const WalkArgs a) {
   extern __shared__ uint32_t gone[];              // a bit per token of the slice: removed
   __shared__ WalkShared sh;
   griddep_wait();
@@ -425,17 +675,17 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   const int v0 = min(V, static_cast<int>(rank) * S), v1 = min(V, v0 + S);
   const bool scribe = rank == 0 && tid == 0;
   if (rank == 0)
-    for (int d = tid; d <= a.max_depth; d += kAsThreads)
+    for (int d = tid; d <= a.max_depth; d += kWalkThreads)
       a.path[static_cast<int64_t>(r) * (a.max_depth + 1) + d] = d == 0 && n > 0 ? 0 : -1;
   if (n == 0) {                                   // (the whole cluster)
     if (scribe) { a.accept_len[r] = -1; a.best_node[r] = -1; a.bonus[r] = -1; }
     return;
   }
   const T* pl = static_cast<const T*>(a.p);
-  for (int w = tid; w < (S + 31) / 32; w += kAsThreads) gone[w] = 0;
-  for (int i = tid; i < n; i += kAsThreads) { sh.first[i] = -1; sh.next[i] = -1; }
+  for (int w = tid; w < (S + 31) / 32; w += kWalkThreads) gone[w] = 0;
+  for (int i = tid; i < n; i += kWalkThreads) { sh.first[i] = -1; sh.next[i] = -1; }
   // both probabilities of every node's token at its parent
-  for (int i = tid; i < n; i += kAsThreads) {
+  for (int i = tid; i < n; i += kWalkThreads) {
     const int par = a.parent[n0 + i], x = a.tok[n0 + i];
     float px = 0.f, qx = 0.f;
     uint8_t flag = 0;
@@ -464,7 +714,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
   int cur = 0, depth = 0, e = 0, kills = 0;
   auto revive = [&]() {                           // no token is removed any more
     __syncthreads();
-    for (int j = tid; j < kills; j += kAsThreads) {
+    for (int j = tid; j < kills; j += kWalkThreads) {
       const int x = sh.kills[j];
       if (x >= v0 && x < v1) gone[(x - v0) >> 5] = 0;
     }
@@ -497,7 +747,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
       fb = 0.f;
       left = 1.f;
       if (kills) revive();
-      for (int i = tid; i < n; i += kAsThreads) sh.flag[i] &= 1;
+      for (int i = tid; i < n; i += kWalkThreads) sh.flag[i] &= 1;
       __syncthreads();
     };
     int next = -1;
@@ -509,7 +759,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
       }
       if (left < 0.f) {                           // after a rejected draw
         float z = 0.f;
-        for (int v = v0 + 8 * tid; v < v1; v += 8 * kAsThreads) {
+        for (int v = v0 + 8 * tid; v < v1; v += 8 * kWalkThreads) {
           float y[8];
           rest8(v, y);
           z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
@@ -519,7 +769,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
         __syncthreads();
         if (tid == 0) {
           z = 0.f;
-          for (int w = 0; w < kAsWarps; ++w) z += sh.wred[w];
+          for (int w = 0; w < kWalkWarps; ++w) z += sh.wred[w];
           sh.xf[e & 1] = z;
         }
         cl::sync();
@@ -543,7 +793,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
           if (x >= v0 && x < v1) gone[(x - v0) >> 5] |= 1u << ((x - v0) & 31);
         }
         ++kills;
-        for (int i = tid; i < n; i += kAsThreads)
+        for (int i = tid; i < n; i += kWalkThreads)
           if (sh.tok[i] == x) sh.flag[i] |= 2;    // (of nodes under other parents too: cleared at the next node)
         __syncthreads();
       }
@@ -562,7 +812,8 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
         if (turn == 1) reset();                   // (nothing left: the target's own)
         float best = 0.f;
         int at = 0x7fffffff;
-        for (int v = v0 + 8 * tid; v < v1; v += 8 * kAsThreads) {
+#pragma unroll 2
+        for (int v = v0 + 8 * tid; v < v1; v += 8 * kWalkThreads) {
           float y[8], t[8];
           load8(race, v, v1, a.vec_r, t);
           rest8(v, y);
@@ -583,7 +834,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads)
         if (lane == 0) { sh.wred[warp] = best; sh.wred_i[warp] = at; }
         __syncthreads();
         if (tid == 0) {
-          for (int w = 1; w < kAsWarps; ++w)
+          for (int w = 1; w < kWalkWarps; ++w)
             if (better(sh.wred[w], sh.wred_i[w], best, at)) { best = sh.wred[w]; at = sh.wred_i[w]; }
           sh.xf[e & 1] = best;
           sh.xi[e & 1] = at;
@@ -615,7 +866,7 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
   const dim3 rows(static_cast<unsigned>(kAsCluster) * ra.max_nodes, B);
   int rc;
   if (trunc) {
-    const size_t smem = ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kBins * kAsThreads * 4;
+    const size_t smem = ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kScratch;
     if (smem > 220 << 10) return TV_EUNSUPPORTED;
     if (!smem_limit(row_kernel<T, true>, 220 << 10)) return TV_ECUDA;
     rc = launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), smem, st, ra);
@@ -623,7 +874,7 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
     rc = launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), 0, st, ra);
   }
   if (rc != TV_OK) return rc;
-  return launch_pdl(walk_kernel<T>, dim3(static_cast<unsigned>(kAsCluster) * B), dim3(kAsThreads),
+  return launch_pdl(walk_kernel<T>, dim3(static_cast<unsigned>(kAsCluster) * B), dim3(kWalkThreads),
                     static_cast<size_t>(S + 31) / 32 * 4, st, wa);
 }
 
