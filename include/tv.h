@@ -320,7 +320,7 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
  * Outputs: as accept_rejection_sampling (accept_len -1, best_node -1, bonus -1
  *   for a request without nodes).
  * Workspace: accept_sampled_workspace_size(...) bytes, 16-byte aligned.
- * Arithmetic: fp32, each row read twice at most; a decision whose numbers lie
+ * Arithmetic: fp32; a decision whose numbers lie
  *   within ~1e-6 (relative) of each other may differ from exact arithmetic.
  * -------------------------------------------------------------------------- */
 size_t accept_sampled_workspace_size(int B, int total_nodes, int V);

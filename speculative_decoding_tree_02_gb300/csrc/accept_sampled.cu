@@ -2,9 +2,10 @@
 // probabilities (temperature, top-k and top-p of each request) from given
 // random numbers; include/tv.h states the rule.
 //
-// Two kernels.  row_kernel takes every node's row of logits at once: a cluster
-// of 8 CTAs per row finds its maximum, the truncation's threshold and the mass
-// of what is kept, 16 bytes per row.  walk_kernel then needs single logits for
+// Two kernels.  row_kernel takes the nodes' rows of logits side by side: a
+// cluster of 8 CTAs per row finds its maximum, the truncation's threshold and
+// the mass of what is kept, 16 bytes per row; rows that the walk turns out not
+// to reach while others are still waiting are left out.  walk_kernel then needs single logits for
 // the accept tests, and passes over a row only for what a rejected draw leaves
 // and for the last token.  Rejections only ever turn the distribution into
 // max(0, a p - b q) without the tokens that were removed, so two numbers and a
@@ -39,19 +40,33 @@ __device__ __forceinline__ float prob(float l, const RowStat& s) {
   return l >= s.floor ? ex2(log_weight(l, s.top, s.c)) * s.inv : 0.f;
 }
 
-// Eight consecutive logits; -inf past the end.
+// Eight consecutive logits as loaded.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.v[i] = ldg_stream(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+__device__ __forceinline__ void widen8(const Raw8<uint16_t>& r, float (&x)[8]) {
+  const uint4 w = r.v[0];
+  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float (&x)[8]) {
+  const uint4 a = r.v[0], b = r.v[1];
+  x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+  x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+}
+// Eight consecutive numbers, whatever their alignment; -inf past the end.
 template <typename T>
 __device__ __forceinline__ void load8(const T* row, int v, int end, bool vec, float (&x)[8]) {
   if (vec && v + 8 <= end) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + v));
-      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-      x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-    } else {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + v)), b = __ldg(reinterpret_cast<const float4*>(row + v) + 1);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
+    widen8(raw8(row + v), x);
     return;
   }
 #pragma unroll
@@ -61,6 +76,40 @@ __device__ __forceinline__ void load8(const T* row, int v, int end, bool vec, fl
       if constexpr (sizeof(T) == 2) x[e] = bf16_at(reinterpret_cast<const uint16_t*>(row) + v + e);
       else x[e] = row[v + e];
     }
+  }
+}
+// fn(v, x) for the eights of [v0, v1) that a thread owns (v = v0 + 8 tid, then
+// kThreads eights further), kAhead of them on their way at a time.
+template <int kThreads, int kAhead, typename T, typename F>
+__device__ __forceinline__ void sweep(const T* row, int v0, int v1, bool vec, F&& fn) {
+  int v = v0 + 8 * static_cast<int>(threadIdx.x);
+  if (vec) {
+    for (; v + 8 <= v1; v += 8 * kThreads * kAhead) {
+      Raw8<T> w[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (v + 8 * kThreads * u + 8 <= v1) w[u] = raw8(row + v + 8 * kThreads * u);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (v + 8 * kThreads * u + 8 <= v1) {
+          float x[8];
+          widen8(w[u], x);
+          fn(v + 8 * kThreads * u, x);
+        }
+      }
+    }
+    const int tail = v0 + (v1 - v0) / 8 * 8;      // a last, shorter one
+    if (tail < v1 && (tail - v0) / 8 % kThreads == static_cast<int>(threadIdx.x)) {
+      float x[8];
+      load8(row, tail, v1, false, x);
+      fn(tail, x);
+    }
+    return;
+  }
+  for (; v < v1; v += 8 * kThreads) {
+    float x[8];
+    load8(row, v, v1, false, x);
+    fn(v, x);
   }
 }
 template <typename T>
@@ -82,12 +131,26 @@ struct RowArgs {
   int64_t ld;
   int V, max_nodes, total;
   bool vec;
+  // for leaving out rows that the walk cannot reach; dead NULL: none are
+  int32_t* dead;
+  const int32_t* parent;
+  const int32_t* tok;
+  const float* q;
+  const uint8_t* drawn;
+  const float* u_node;
+  int64_t ldq;
 };
+
+// A node's token is accepted: u q < p' for a drawn one, u < p' otherwise.
+__device__ __forceinline__ bool accepted(float u, bool drawn, float q, float have, float left) {
+  return u * (drawn ? q : 1.f) < have / left;
+}
 
 constexpr int kList = 512;         // listed logits of a warp
 constexpr int kSort = 1024;        // listed logits of a row
 constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
 constexpr int kScratch = kBins * kAsThreads * 4;
+static_assert(kScratch >= TV_MAX_NODES * 3, "see judge_children");
 static_assert(kScratch / 2 == kAsWarps * kList * 4, "the lists fill the second half of the scratch");
 
 struct RowShared {
@@ -196,6 +259,88 @@ __device__ __forceinline__ void sort_desc(float* v, int n) {
   __syncthreads();
 }
 
+// Room that a CTA needs to leave out rows: the nodes' parents, and a mark per node.
+constexpr int kPruneBytes = TV_MAX_NODES * 3;
+
+// What is certain about the children of node i, whose row's stat is known: the
+// walk's own tests in its order and arithmetic, as far as they need nothing
+// but single probabilities, up to the first acceptance, the first rejected
+// draw (which leaves a residual) or the 32nd child.  Rejected children and
+// those behind an accepted one cannot be reached, nor can their descendants:
+// all of these get a.dead = 1.  By a CTA, `room` being shared memory.
+template <typename T>
+__device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nodes, int i, const RowStat& st, uint8_t* room) {
+  int16_t* par = reinterpret_cast<int16_t*>(room);
+  uint8_t* mark = room + 2 * TV_MAX_NODES;
+  const int tid = threadIdx.x, lane = tid & 31;
+  __syncthreads();
+  for (int j = i + 1 + tid; j < nodes; j += blockDim.x) {
+    const int p = a.parent[n0 + j];
+    par[j] = static_cast<int16_t>(p >= 0 && p < j ? p : -1);
+    mark[j] = 0;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const T* p = static_cast<const T*>(a.p) + static_cast<int64_t>(n0 + i) * a.ld;
+    int mine = -1, found = 0;                     // lane l: the l-th child
+    int stop = nodes;                             // first node that was not looked at
+    for (int j0 = i + 1; j0 < nodes; j0 += 32) {
+      const unsigned b = __ballot_sync(0xffffffffu, j0 + lane < nodes && par[j0 + lane] == i);
+      if (found + __popc(b) > 32) { stop = j0; break; }
+      for (unsigned m = b; m; m &= m - 1u, ++found)
+        if (lane == found) mine = j0 + __ffs(static_cast<int>(m)) - 1;
+    }
+    float px = 0.f, qx = 0.f, u = 0.f;
+    int x = -1;
+    bool drawn = false, in = false;
+    if (mine >= 0) {
+      x = a.tok[n0 + mine];
+      in = x >= 0 && x < a.V;
+      if (in && st.inv >= 0.f) px = prob(one(p, x), st);
+      if (in && a.q) qx = a.q[static_cast<int64_t>(n0 + i) * a.ldq + x];
+      u = a.u_node[n0 + mine];
+      drawn = a.q && (!a.drawn || a.drawn[n0 + mine]);
+    }
+    float left = 1.f;
+    unsigned dead = 0;
+    for (int ch = 0; ch < found; ++ch) {
+      const int xc = __shfl_sync(0xffffffffu, x, ch);
+      const float pc = __shfl_sync(0xffffffffu, px, ch), qc = __shfl_sync(0xffffffffu, qx, ch),
+                  uc = __shfl_sync(0xffffffffu, u, ch);
+      const bool dc = __shfl_sync(0xffffffffu, drawn, ch), inc = __shfl_sync(0xffffffffu, in, ch);
+      bool yes;
+      if (st.inv < 0.f) {
+        yes = xc == __float_as_int(st.floor);
+      } else {
+        if (!(left > 0.f)) break;
+        // (a token that a rejected sibling had is removed)
+        const bool twice = __any_sync(0xffffffffu, in && x == xc && (dead >> lane & 1u));
+        const float have = twice ? 0.f : pc;
+        yes = accepted(uc, dc, qc, have, left);
+        if (!yes && dc) {
+          dead |= 1u << ch;
+          break;
+        }
+        if (!yes && inc && !twice) left -= have;
+      }
+      if (yes) {                                  // the others behind it
+        dead |= ch < 31 ? ~0u << (ch + 1) : 0u;
+        for (int j = stop + lane; j < nodes; j += 32)
+          if (par[j] == i) mark[j] = 1;
+        break;
+      }
+      dead |= 1u << ch;
+    }
+    if (mine >= 0 && (dead >> lane & 1u)) mark[mine] = 1;
+  }
+  __syncthreads();
+  for (int j = i + 1 + tid; j < nodes; j += blockDim.x) {
+    int x = j;                                    // the child of i that j descends from, if any
+    while (par[x] > i) x = par[x];
+    if (par[x] == i && mark[x]) a.dead[n0 + j] = 1;
+  }
+}
+
 // One row of logits: a cluster of 8 CTAs.  The slice of a CTA is staged in
 // shared memory and read once from there in most calls: the highest logit is
 // known by then, so one pass sums the weights and lists those above 2^-12 of
@@ -214,10 +359,19 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   griddep_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cl::rank();
-  const int r = blockIdx.y, i = blockIdx.x / kAsCluster;
+  const int r = blockIdx.x / kAsCluster, i = blockIdx.y;
   const int n0 = max(a.node_off[r], 0);
-  if (i >= a.node_off[r + 1] - n0 || n0 + i >= a.total) return;      // (the whole cluster)
+  const int nodes = min(min(a.node_off[r + 1], a.total) - n0, a.max_nodes);
+  if (i >= nodes) return;                         // (the whole cluster)
   const int64_t row = n0 + i;
+  if (a.dead && i > 0) {
+    // one CTA looks, so that all do the same
+    if (rank == 0 && tid == 0) sh.hit = *reinterpret_cast<volatile const int32_t*>(a.dead + row);
+    cl::sync();
+    const bool gone = cl::peek(&sh.hit, 0) != 0;
+    cl::sync();
+    if (gone) return;
+  }
   const T* p = static_cast<const T*>(a.p) + row * a.ld;
   const int V = a.V, S = slice_len(V);
   const int v0 = min(V, static_cast<int>(rank) * S), v1 = min(V, v0 + S);
@@ -234,13 +388,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   float m = -INFINITY, s = 0.f;
   int at = 0x7fffffff;
   const bool stage = by_k || by_p;
-  for (int v = v0 + 8 * tid; v < v1; v += 8 * kAsThreads) {
-    float x[8];
-    load8(p, v, v1, a.vec, x);
+  sweep<kAsThreads, 5>(p, v0, v1, a.vec, [&](int v, const float(&x)[8]) {
     if constexpr (kTrunc) {
       if (stage) {
         m = fmaxf(m, stage8(xs + (v - v0), x));
-        continue;
+        return;
       }
     }
     float m8 = x[0];
@@ -253,7 +405,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         for (int e = 7; e >= 0; --e)
           if (x[e] == m8) at = v + e;
       }
-      continue;
+      return;
     }
     if (m8 > 3.402823466e38f) m8 = 3.402823466e38f;
     if (m8 > m) {                                 // running maximum and sum
@@ -262,7 +414,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += ex2(log_weight(x[e], m, c));
-  }
+  });
   int e = 0;
   // over the cluster: the maximum, its first place or the sum
   const float wm = warp_max(m);
@@ -289,6 +441,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
     if (t > all) { all = t; first = f; }          // (ranks in index order: the first of equals stays)
   }
   ++e;
+  // by the first CTA: the row is done
+  auto publish = [&](const RowStat& st) {
+    if (tid == 0) a.stat[row] = st;
+    if (a.dead) judge_children<T>(a, n0, nodes, i, st, dyn);    // (no pass over the slice follows)
+  };
   RowStat out;
   out.c = c;
   out.floor = -INFINITY;
@@ -296,7 +453,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
     out.top = all;
     out.floor = __int_as_float(first == 0x7fffffff ? -1 : first);
     out.inv = -1.f;
-    if (rank == 0 && tid == 0) a.stat[row] = out;
+    if (rank == 0) publish(out);
     cl::sync();                                   // no CTA leaves while another may read its shared memory
     return;
   }
@@ -464,7 +621,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         }
         if (by_p) settle_p(cnt, kept, 0.f, nucleus * z);
         out.inv = mass > 0.f ? 1.f / mass : 0.f;
-        if (tid == 0) a.stat[row] = out;
+        publish(out);
       };
 
       // ---- the highest, listed while all are summed
@@ -573,7 +730,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
                   prefix(cnt);
                   settle_p(cnt, cnt, above, target);
                   out.inv = mass > 0.f ? 1.f / mass : 0.f;
-                  if (tid == 0) a.stat[row] = out;
+                  publish(out);
                 } else if (tid == 0) {
                   sh.out = hist[min(cnt, static_cast<int>(target - above)) - 1];
                 }
@@ -622,11 +779,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
     }
   }
   out.inv = mass > 0.f ? 1.f / mass : 0.f;
-  if (rank == 0 && tid == 0) a.stat[row] = out;
+  if (rank == 0) publish(out);
   cl::sync();                                     // no CTA leaves while another may read its shared memory
 }
 
-constexpr int kWalkThreads = 512;
+constexpr int kWalkThreads = 256;
 constexpr int kWalkWarps = kWalkThreads / 32;
 
 struct WalkArgs {
@@ -661,7 +818,7 @@ struct WalkShared {
 
 // A cluster of 8 CTAs walks one request's tree, all taking the same decisions.
 template <typename T>
-__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThreads) walk_kernel(const WalkArgs a) {
+__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThreads, 4) walk_kernel(const WalkArgs a) {
   extern __shared__ uint32_t gone[];              // a bit per token of the slice: removed
   __shared__ WalkShared sh;
   griddep_wait();
@@ -729,18 +886,21 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
     const bool greedy = st.inv < 0.f;
     // what is left of the distribution: max(0, fa p - fb q), removed tokens apart; its mass (-1: not known)
     float fa = 1.f, fb = 0.f, left = 1.f;
-    // eight tokens of it
-    auto rest8 = [&](int v, float (&x)[8]) {
-      load8(prow, v, v1, a.vec_p, x);
+    // what is left at eight tokens from v on, x their logits
+    auto rest8 = [&](int v, const float(&x)[8], float (&y)[8]) {
       float q[8];
       if (fb > 0.f) load8(qrow, v, v1, a.vec_q, q);
       const uint32_t dead = kills ? gone[(v - v0) >> 5] >> ((v - v0) & 31) : 0u;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = prob(x[j], st);
-        if (fb > 0.f) x[j] = fmaxf(0.f, fmaf(fa, x[j], -fb * q[j]));
-        if (dead & (1u << j) || v + j >= v1) x[j] = 0.f;
+        y[j] = prob(x[j], st);
+        if (fb > 0.f) y[j] = fmaxf(0.f, fmaf(fa, y[j], -fb * q[j]));
+        if (dead & (1u << j) || v + j >= v1) y[j] = 0.f;
       }
+    };
+    // whether any of eight logits is kept
+    auto some = [&](const float(&x)[8]) {
+      return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) >= st.floor;
     };
     auto reset = [&]() {
       fa = 1.f;
@@ -759,11 +919,12 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
       }
       if (left < 0.f) {                           // after a rejected draw
         float z = 0.f;
-        for (int v = v0 + 8 * tid; v < v1; v += 8 * kWalkThreads) {
+        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const float(&x)[8]) {
+          if (!some(x)) return;
           float y[8];
-          rest8(v, y);
+          rest8(v, x, y);
           z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-        }
+        });
         z = warp_sum(z);
         if (lane == 0) sh.wred[warp] = z;
         __syncthreads();
@@ -779,8 +940,8 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
       }
       if (!(left > 0.f)) reset();                 // nothing left (rounding only): the target's own again
       const bool is_drawn = sh.flag[ch] & 1;
-      const float have = sh.flag[ch] & 2 ? 0.f : fmaxf(0.f, fmaf(fa, sh.px[ch], -fb * sh.qx[ch]));
-      if (sh.u[ch] * (is_drawn ? sh.qx[ch] : 1.f) < have / left) { next = ch; break; }
+      const float have = sh.flag[ch] & 2 ? 0.f : fb > 0.f ? fmaxf(0.f, fmaf(fa, sh.px[ch], -fb * sh.qx[ch])) : fa * sh.px[ch];
+      if (accepted(sh.u[ch], is_drawn, sh.qx[ch], have, left)) { next = ch; break; }
       if (is_drawn) {
         fa /= left;
         fb = fb / left + 1.f;
@@ -812,11 +973,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         if (turn == 1) reset();                   // (nothing left: the target's own)
         float best = 0.f;
         int at = 0x7fffffff;
-#pragma unroll 2
-        for (int v = v0 + 8 * tid; v < v1; v += 8 * kWalkThreads) {
+        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const float(&x)[8]) {
+          if (!some(x)) return;
           float y[8], t[8];
           load8(race, v, v1, a.vec_r, t);
-          rest8(v, y);
+          rest8(v, x, y);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (y[j] > 0.f) {
@@ -824,7 +985,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
               if (f > best) { best = f; at = v + j; }
             }
           }
-        }
+        });
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           const float f = __shfl_xor_sync(0xffffffffu, best, o);
@@ -863,15 +1024,21 @@ template <typename T>
 int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
   const bool trunc = ra.top_k || ra.top_p;
   const int S = ((ra.V + kAsCluster - 1) / kAsCluster + 7) / 8 * 8;
-  const dim3 rows(static_cast<unsigned>(kAsCluster) * ra.max_nodes, B);
+  // nodes in the order of their index, the requests' side by side: a row's
+  // descendants come late enough to be left out when it ends the walk
+  const dim3 rows(static_cast<unsigned>(kAsCluster) * B, ra.max_nodes);
   int rc;
+  if (ra.dead && cudaMemsetAsync(ra.dead, 0, static_cast<size_t>(ra.total) * 4, st) != cudaSuccess) {
+    cudaGetLastError();
+    return TV_ECUDA;
+  }
   if (trunc) {
     const size_t smem = ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kScratch;
     if (smem > 220 << 10) return TV_EUNSUPPORTED;
     if (!smem_limit(row_kernel<T, true>, 220 << 10)) return TV_ECUDA;
     rc = launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), smem, st, ra);
   } else {
-    rc = launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), 0, st, ra);
+    rc = launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), kPruneBytes, st, ra);
   }
   if (rc != TV_OK) return rc;
   return launch_pdl(walk_kernel<T>, dim3(static_cast<unsigned>(kAsCluster) * B), dim3(kWalkThreads),
@@ -885,7 +1052,7 @@ using namespace tv;
 
 TV_API size_t accept_sampled_workspace_size(int B, int total_nodes, int V) {
   if (B <= 0 || total_nodes <= 0 || V <= 0) return 0;
-  return static_cast<size_t>(total_nodes) * sizeof(RowStat);
+  return static_cast<size_t>(total_nodes) * (sizeof(RowStat) + 4);
 }
 
 TV_API int accept_sampled(const int32_t* parent, const int32_t* tok, const void* p_logits, int dtype, int V, int64_t ld,
@@ -908,8 +1075,13 @@ TV_API int accept_sampled(const int32_t* parent, const int32_t* tok, const void*
   const bool bf = dtype == TV_BF16;
   const bool vec_p = aligned(p_logits, 16) && ld % (bf ? 8 : 4) == 0;
   const bool vec_q = aligned(q_prob, 16) && ldq % 4 == 0, vec_r = aligned(race, 16) && ldr % 4 == 0;
-  const RowArgs ra{p_logits, node_off, temperature, top_k, top_p, static_cast<RowStat*>(ws), ld, V,
-                   std::max(max_nodes, 1), total_nodes, vec_p};
+  // Rows that cannot be reached are left out where there are more than run at
+  // a time (three CTAs to an SM).
+  const bool prune = static_cast<int64_t>(B) * max_nodes * kAsCluster > 3ll * sm_count() && total_nodes > 0;
+  auto* stat = static_cast<RowStat*>(ws);
+  const RowArgs ra{p_logits, node_off, temperature, top_k, top_p, stat, ld, V, std::max(max_nodes, 1), total_nodes, vec_p,
+                   prune ? reinterpret_cast<int32_t*>(stat + total_nodes) : nullptr, parent, tok, q_prob, drawn, u_node,
+                   ldq};
   const WalkArgs wa{parent, tok, p_logits, q_prob, drawn, node_off, u_node, race, static_cast<const RowStat*>(ws),
                     accept_len, best_node, path, bonus, ld, ldq, ldr, V, max_nodes, max_depth, total_nodes, vec_p, vec_q,
                     vec_r};

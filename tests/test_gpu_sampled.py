@@ -109,7 +109,7 @@ def test_one_row_workspace_strides_and_streams(tv):
         s.synchronize()
         c.check(got)
     with pytest.raises(tv.TVError) as e:
-        c.run(tv, ws=torch.empty(16 * n - 16, dtype=torch.uint8, device="cuda"))
+        c.run(tv, ws=torch.empty(20 * n - 16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -4
 
 

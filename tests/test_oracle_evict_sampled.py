@@ -118,7 +118,7 @@ COMPACT = dict(cache=B_, n_pages=4, page=16, table=B_, table_ld=4, cache_len=B_,
                max_keep=32, dst=None, dst_ld=0, H=1, d=64, err=None, stream=None)
 SAMPLED = dict(parent=B_, tok=B_, p=B_, dtype=1, V=100, ld=100, q=B_, ldq=100, drawn=None, node_off=B_, B=1, max_nodes=4,
                rows=4, max_depth=3, T=None, k=None, tp=None, u=B_, race=B_, ldr=100, acc=B_, best=B_, path=B_, bonus=B_,
-               ws=B_, ws_bytes=64, stream=None)
+               ws=B_, ws_bytes=80, stream=None)
 FLOATS = {"scale", "decay"}
 
 
@@ -161,7 +161,7 @@ def test_compact_refusals(lib, want, change):
     (-1, dict(dtype=3)), (-1, dict(B=-1)), (-1, dict(V=0)), (-1, dict(ld=99)), (-1, dict(ldr=99)), (-1, dict(ldq=99)),
     (-1, dict(q=None, drawn=B_)), (-2, dict(max_nodes=1025)), (-2, dict(V=(1 << 20) + 1, ld=1 << 21, ldq=1 << 21, ldr=1 << 21)),
     (-2, dict(B=70000)), (-1, dict(node_off=None)), (-1, dict(acc=None)), (-1, dict(parent=None)), (-1, dict(p=None)),
-    (-1, dict(u=None)), (-1, dict(race=None)), (-4, dict(ws=None)), (-4, dict(ws_bytes=63)), (-4, dict(ws=ODD)),
+    (-1, dict(u=None)), (-1, dict(race=None)), (-4, dict(ws=None)), (-4, dict(ws_bytes=79)), (-4, dict(ws=ODD)),
     (0, dict(B=0))])
 def test_sampled_refusals(lib, want, change):
     assert call(lib, "accept_sampled", SAMPLED, **change) == want
