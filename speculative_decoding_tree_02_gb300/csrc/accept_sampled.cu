@@ -23,7 +23,7 @@ constexpr int kAsCluster = 8;
 constexpr int kAsThreads = 256;
 constexpr int kAsWarps = kAsThreads / 32;
 constexpr int kAsMaxVocab = 1 << 20;
-constexpr int kBins = 32;
+constexpr int kBins = 16;
 
 // What row_kernel says of a row: p(v) = 2^((l - top) c) inv for l >= floor, else 0;
 // greedy rows (inv = -1): floor holds the chosen token.
@@ -78,8 +78,25 @@ __device__ __forceinline__ void load8(const T* row, int v, int end, bool vec, fl
     }
   }
 }
-// fn(v, x) for the eights of [v0, v1) that a thread owns (v = v0 + 8 tid, then
-// kThreads eights further), kAhead of them on their way at a time.
+// The same as they are stored.
+template <typename T>
+__device__ __forceinline__ Raw8<T> tail8(const T* row, int v, int end) {
+  float x[8];
+  load8(row, v, end, false, x);
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(x[2 * e]) >> 16) | (__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
+    r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    r.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    r.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+  }
+  return r;
+}
+// fn(v, eight) for the eights of [v0, v1) that a thread owns (v = v0 + 8 tid,
+// then kThreads eights further), kAhead of them on their way at a time.
 template <int kThreads, int kAhead, typename T, typename F>
 __device__ __forceinline__ void sweep(const T* row, int v0, int v1, bool vec, F&& fn) {
   int v = v0 + 8 * static_cast<int>(threadIdx.x);
@@ -90,27 +107,26 @@ __device__ __forceinline__ void sweep(const T* row, int v0, int v1, bool vec, F&
       for (int u = 0; u < kAhead; ++u)
         if (v + 8 * kThreads * u + 8 <= v1) w[u] = raw8(row + v + 8 * kThreads * u);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (v + 8 * kThreads * u + 8 <= v1) {
-          float x[8];
-          widen8(w[u], x);
-          fn(v + 8 * kThreads * u, x);
-        }
-      }
+      for (int u = 0; u < kAhead; ++u)
+        if (v + 8 * kThreads * u + 8 <= v1) fn(v + 8 * kThreads * u, w[u]);
     }
     const int tail = v0 + (v1 - v0) / 8 * 8;      // a last, shorter one
-    if (tail < v1 && (tail - v0) / 8 % kThreads == static_cast<int>(threadIdx.x)) {
-      float x[8];
-      load8(row, tail, v1, false, x);
-      fn(tail, x);
-    }
+    if (tail < v1 && (tail - v0) / 8 % kThreads == static_cast<int>(threadIdx.x)) fn(tail, tail8(row, tail, v1));
     return;
   }
-  for (; v < v1; v += 8 * kThreads) {
-    float x[8];
-    load8(row, v, v1, false, x);
-    fn(v, x);
-  }
+  for (; v < v1; v += 8 * kThreads) fn(v, tail8(row, v, v1));
+}
+// Their maximum.
+__device__ __forceinline__ float max8(const Raw8<uint16_t>& r) {
+  const uint4 w = r.v[0];
+  const __nv_bfloat162 m = __hmax2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), *reinterpret_cast<const __nv_bfloat162*>(&w.y)),
+                                   __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), *reinterpret_cast<const __nv_bfloat162*>(&w.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float max8(const Raw8<float>& r) {
+  float x[8];
+  widen8(r, x);
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 }
 template <typename T>
 __device__ __forceinline__ float one(const T* row, int v) {
@@ -146,9 +162,10 @@ __device__ __forceinline__ bool accepted(float u, bool drawn, float q, float hav
   return u * (drawn ? q : 1.f) < have / left;
 }
 
-constexpr int kList = 512;         // listed logits of a warp
+constexpr int kList = 256;         // listed logits of a warp
 constexpr int kSort = 1024;        // listed logits of a row
 constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
+constexpr int kCutPick = 4;        // or, for k up to 64 kCutPick, to a cut found among the threads' maxima
 constexpr int kScratch = kBins * kAsThreads * 4;
 static_assert(kScratch >= TV_MAX_NODES * 3, "see judge_children");
 static_assert(kScratch / 2 == kAsWarps * kList * 4, "the lists fill the second half of the scratch");
@@ -165,7 +182,7 @@ struct RowShared {
   float out;                       // what the first CTA found
 };
 
-// Sums over the cluster of up to 32 numbers that lie in sh.xf[e & 1] of each
+// Sums over the cluster of up to kBins numbers that lie in sh.xf[e & 1] of each
 // CTA; every CTA adds them in the order of the ranks.
 __device__ __forceinline__ void cluster_sums(RowShared& sh, int e, int n) {
   cl::sync();
@@ -204,41 +221,36 @@ __device__ __forceinline__ int crossing(const float* tot, int n, float target, f
 }
 
 // Eight staged logits, free of NaN and +inf.
-__device__ __forceinline__ void staged8(const uint16_t* xs, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(xs);
-  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-}
-__device__ __forceinline__ void staged8(const float* xs, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(xs), b = *reinterpret_cast<const float4*>(xs + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+template <typename T>
+__device__ __forceinline__ Raw8<T> staged8(const T* xs) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(xs)[i];
+  return r;
 }
 // Stages eight logits (NaN as -inf, +inf as the largest number); their maximum.
-__device__ __forceinline__ float stage8(uint16_t* xs, const float (&x)[8]) {
+__device__ __forceinline__ float stage8(uint16_t* xs, Raw8<uint16_t> r) {
   const __nv_bfloat162 lo = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
   const __nv_bfloat162 hi = __halves2bfloat162(__ushort_as_bfloat16(0x7f7f), __ushort_as_bfloat16(0x7f7f));
-  uint32_t w[4];
-  __nv_bfloat162 m = lo;
+  uint32_t* w[4] = {&r.v[0].x, &r.v[0].y, &r.v[0].z, &r.v[0].w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    w[e] = (__float_as_uint(x[2 * e]) >> 16) | (__float_as_uint(x[2 * e + 1]) & 0xffff0000u);
-    const __nv_bfloat162 v = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), lo), hi);
-    w[e] = *reinterpret_cast<const uint32_t*>(&v);
-    m = __hmax2(m, v);
+    const __nv_bfloat162 v = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(w[e]), lo), hi);
+    *w[e] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  *reinterpret_cast<uint4*>(xs) = make_uint4(w[0], w[1], w[2], w[3]);
-  return fmaxf(__low2float(m), __high2float(m));
+  *reinterpret_cast<uint4*>(xs) = r.v[0];
+  return max8(r);
 }
-__device__ __forceinline__ float stage8(float* xs, const float (&x)[8]) {
-  float y[8], m = -INFINITY;
+__device__ __forceinline__ float stage8(float* xs, const Raw8<float>& r) {
+  float x[8], m = -INFINITY;
+  widen8(r, x);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    y[e] = fminf(fmaxf(x[e], -INFINITY), 3.402823466e38f);
-    m = fmaxf(m, y[e]);
+    x[e] = fminf(fmaxf(x[e], -INFINITY), 3.402823466e38f);
+    m = fmaxf(m, x[e]);
   }
-  *reinterpret_cast<float4*>(xs) = make_float4(y[0], y[1], y[2], y[3]);
-  *reinterpret_cast<float4*>(xs + 4) = make_float4(y[4], y[5], y[6], y[7]);
+  *reinterpret_cast<float4*>(xs) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(xs + 4) = make_float4(x[4], x[5], x[6], x[7]);
   return m;
 }
 
@@ -348,11 +360,11 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
 // lists of all and finds the threshold by a prefix sum while the others leave.
 // Where the list does not reach the threshold (flat distributions, large k)
 // or overflows, the logits are binned by powers of two of the weight, the
-// threshold's bin by 32nd parts of it, twice, until a bin is short enough to
+// threshold's bin by 16th parts of it, twice, until a bin is short enough to
 // be listed; ties beyond that are told apart by four bits of the ordered bits
 // at a time.  All sums have a fixed order.
 template <typename T, bool kTrunc>
-__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads, 3) row_kernel(const RowArgs a) {
+__global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads, 4) row_kernel(const RowArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowShared sh;
   griddep_wait();
@@ -369,8 +381,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
     if (rank == 0 && tid == 0) sh.hit = *reinterpret_cast<volatile const int32_t*>(a.dead + row);
     cl::sync();
     const bool gone = cl::peek(&sh.hit, 0) != 0;
-    cl::sync();
-    if (gone) return;
+    cl::arrive();                                 // (the first CTA stays until all have looked)
+    if (gone) {
+      cl::wait();
+      return;
+    }
   }
   const T* p = static_cast<const T*>(a.p) + row * a.ld;
   const int V = a.V, S = slice_len(V);
@@ -388,16 +403,15 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   float m = -INFINITY, s = 0.f;
   int at = 0x7fffffff;
   const bool stage = by_k || by_p;
-  sweep<kAsThreads, 5>(p, v0, v1, a.vec, [&](int v, const float(&x)[8]) {
+  sweep<kAsThreads, 5>(p, v0, v1, a.vec, [&](int v, const Raw8<T>& w) {
     if constexpr (kTrunc) {
       if (stage) {
-        m = fmaxf(m, stage8(xs + (v - v0), x));
+        m = fmaxf(m, stage8(xs + (v - v0), w));
         return;
       }
     }
-    float m8 = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) m8 = fmaxf(m8, x[e]);
+    float x[8], m8 = max8(w);
+    widen8(w, x);
     if (greedy) {
       if (m8 > m) {
         m = m8;
@@ -415,12 +429,24 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += ex2(log_weight(x[e], m, c));
   });
+  if (a.dead && i > 0) cl::wait();
   int e = 0;
   // over the cluster: the maximum, its first place or the sum
   const float wm = warp_max(m);
   if (lane == 0) sh.wred[warp] = wm;
   const int wi = __reduce_min_sync(0xffffffffu, m == wm && greedy ? at : 0x7fffffff);
   if (lane == 0) sh.wred_i[warp] = wi;
+  // For top-k a cut that at least k logits reach: every warp's j-th highest of
+  // its lanes' maxima, 64 j >= k, the lowest of these over the cluster.
+  const int pick = (k + kAsCluster * kAsWarps - 1) / (kAsCluster * kAsWarps);
+  const bool by_cut = kTrunc && by_k && pick <= kCutPick;
+  if (by_cut) {
+    float x = m;
+    for (int t = 1; t < pick; ++t)
+      if (lane == __ffs(static_cast<int>(__ballot_sync(0xffffffffu, x == warp_max(x)))) - 1) x = -INFINITY;
+    x = warp_max(x);
+    if (lane == 0) sh.scan[warp] = x;
+  }
   __syncthreads();
   if (tid == 0) {
     float top = sh.wred[0];
@@ -430,12 +456,18 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       if (sh.wred[w] == top) first = min(first, sh.wred_i[w]);
     sh.xf[e & 1][0] = top;
     sh.xi[e & 1][0] = first;
+    if (by_cut) {
+      float x = sh.scan[0];
+      for (int w = 1; w < kAsWarps; ++w) x = fminf(x, sh.scan[w]);
+      sh.xf[e & 1][1] = x;
+    }
   }
   cl::sync();
-  float all = -INFINITY;
+  float all = -INFINITY, cut = INFINITY;
   int first = 0x7fffffff;
 #pragma unroll
   for (uint32_t q = 0; q < kAsCluster; ++q) {
+    if (by_cut) cut = fminf(cut, cl::peek(&sh.xf[e & 1][1], q));
     const float t = cl::peek(&sh.xf[e & 1][0], q);
     const int f = cl::peek(&sh.xi[e & 1][0], q);
     if (t > all) { all = t; first = f; }          // (ranks in index order: the first of equals stays)
@@ -488,7 +520,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       auto each = [&](auto&& fn) {
         for (int v = 8 * tid; v < n; v += 8 * kAsThreads) {
           float x[8];
-          staged8(xs + v, x);
+          widen8(staged8(xs + v), x);
 #pragma unroll
           for (int j = 0; j < 8; ++j) fn(x[j]);
         }
@@ -499,24 +531,26 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         int cnt = 0;
         for (int q = 0; q < rounds; ++q) {
           const int v = 8 * (q * kAsThreads + tid);
-          float x[8];
+          Raw8<T> raw{};
+          float x[8], m8 = -INFINITY;
           if (v < n) {
-            staged8(xs + v, x);
-          } else {
+            raw = staged8(xs + v);
+            m8 = max8(raw);
+            if (sum) {
+              float y[8];
+              widen8(raw, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = -INFINITY;
+              for (int j = 0; j < 8; ++j) y[j] = weight(x[j]);
+              z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+            }
           }
-          if (sum) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = weight(x[j]);
-            z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-          }
-          const float m8 = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
           if (!__any_sync(0xffffffffu, m8 >= lo) || cnt > kList) continue;
           uint32_t in = 0;
+          if (m8 >= lo) {
+            widen8(raw, x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) in |= (x[j] >= lo && x[j] <= hi ? 1u : 0u) << j;
+            for (int j = 0; j < 8; ++j) in |= (x[j] >= lo && x[j] <= hi ? 1u : 0u) << j;
+          }
           for (unsigned lanes = __ballot_sync(0xffffffffu, in != 0u); lanes; lanes &= lanes - 1u) {
             const int src = __ffs(static_cast<int>(lanes)) - 1;
             const int more = __popc(__shfl_sync(0xffffffffu, in, src));
@@ -625,8 +659,10 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       };
 
       // ---- the highest, listed while all are summed
+      // (all of them, if the list has room for a whole row)
       float z = 0.f, zl = 0.f;
-      make_list(top - kCut / c, INFINITY, true, z, zl);
+      const float lowest = -3.402823466e38f;
+      make_list(V <= kSort ? lowest : fmaxf(by_cut ? cut : top - kCut / c, lowest), INFINITY, !by_k, z, zl);
       {
         const float w0 = warp_sum(z), w1 = warp_sum(zl);
         if (lane == 0) { sh.wred[warp] = w0; sh.scan[warp] = w1; }
@@ -806,7 +842,7 @@ struct WalkArgs {
 };
 
 struct WalkShared {
-  int16_t first[TV_MAX_NODES], next[TV_MAX_NODES];   // child lists in index order
+  int16_t par[TV_MAX_NODES];                          // -1: none, or not before the node
   int32_t tok[TV_MAX_NODES], kills[TV_MAX_NODES];
   float px[TV_MAX_NODES], qx[TV_MAX_NODES], u[TV_MAX_NODES];
   uint8_t flag[TV_MAX_NODES];                         // 1: drawn, 2: token removed
@@ -819,7 +855,8 @@ struct WalkShared {
 // A cluster of 8 CTAs walks one request's tree, all taking the same decisions.
 template <typename T>
 __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThreads, 4) walk_kernel(const WalkArgs a) {
-  extern __shared__ uint32_t gone[];              // a bit per token of the slice: removed
+  extern __shared__ __align__(16) RowStat stats[];    // the nodes' rows
+  uint32_t* gone = reinterpret_cast<uint32_t*>(stats + a.max_nodes);   // a bit per token of the slice: removed
   __shared__ WalkShared sh;
   griddep_wait();
   griddep_release();
@@ -840,19 +877,21 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
   }
   const T* pl = static_cast<const T*>(a.p);
   for (int w = tid; w < (S + 31) / 32; w += kWalkThreads) gone[w] = 0;
-  for (int i = tid; i < n; i += kWalkThreads) { sh.first[i] = -1; sh.next[i] = -1; }
   // both probabilities of every node's token at its parent
   for (int i = tid; i < n; i += kWalkThreads) {
     const int par = a.parent[n0 + i], x = a.tok[n0 + i];
     float px = 0.f, qx = 0.f;
     uint8_t flag = 0;
+    stats[i] = a.stat[n0 + i];
     if (i > 0 && par >= 0 && par < i && x >= 0 && x < V) {
       const int64_t row = n0 + par;
-      const RowStat s = a.stat[row];
-      px = s.inv < 0.f ? 0.f : prob(one(pl + row * a.ld, x), s);
+      const float l = one(pl + row * a.ld, x);
       if (a.q) qx = a.q[row * a.ldq + x];
+      const RowStat s = a.stat[row];
+      px = s.inv < 0.f ? 0.f : prob(l, s);
     }
     if (a.q && (!a.drawn || a.drawn[n0 + i])) flag = 1;
+    sh.par[i] = static_cast<int16_t>(i > 0 && par >= 0 && par < i ? par : -1);
     sh.px[i] = px;
     sh.qx[i] = qx;
     sh.tok[i] = x;
@@ -860,13 +899,14 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
     sh.u[i] = a.u_node[n0 + i];
   }
   __syncthreads();
-  if (tid == 0) {
-    for (int i = n - 1; i >= 1; --i) {
-      const int p = a.parent[n0 + i];
-      if (p >= 0 && p < i) { sh.next[i] = sh.first[p]; sh.first[p] = static_cast<int16_t>(i); }
+  // the first child of node c from index j on, -1: none
+  auto child = [&](int c, int j) {
+    for (; j < n; j += 32) {
+      const unsigned b = __ballot_sync(0xffffffffu, j + lane < n && sh.par[j + lane] == c);
+      if (b) return j + __ffs(static_cast<int>(b)) - 1;
     }
-  }
-  __syncthreads();
+    return -1;
+  };
 
   int cur = 0, depth = 0, e = 0, kills = 0;
   auto revive = [&]() {                           // no token is removed any more
@@ -880,15 +920,16 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
   };
   for (;;) {
     const int64_t row = n0 + cur;
-    const RowStat st = a.stat[row];
+    const RowStat st = stats[cur];
     const T* prow = pl + row * a.ld;
     const float* qrow = a.q ? a.q + row * a.ldq : nullptr;
     const bool greedy = st.inv < 0.f;
     // what is left of the distribution: max(0, fa p - fb q), removed tokens apart; its mass (-1: not known)
     float fa = 1.f, fb = 0.f, left = 1.f;
-    // what is left at eight tokens from v on, x their logits
-    auto rest8 = [&](int v, const float(&x)[8], float (&y)[8]) {
-      float q[8];
+    // what is left at eight tokens from v on, w their logits
+    auto rest8 = [&](int v, const Raw8<T>& w, float (&y)[8]) {
+      float q[8], x[8];
+      widen8(w, x);
       if (fb > 0.f) load8(qrow, v, v1, a.vec_q, q);
       const uint32_t dead = kills ? gone[(v - v0) >> 5] >> ((v - v0) & 31) : 0u;
 #pragma unroll
@@ -897,10 +938,6 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         if (fb > 0.f) y[j] = fmaxf(0.f, fmaf(fa, y[j], -fb * q[j]));
         if (dead & (1u << j) || v + j >= v1) y[j] = 0.f;
       }
-    };
-    // whether any of eight logits is kept
-    auto some = [&](const float(&x)[8]) {
-      return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) >= st.floor;
     };
     auto reset = [&]() {
       fa = 1.f;
@@ -911,7 +948,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
       __syncthreads();
     };
     int next = -1;
-    for (int ch = sh.first[cur]; ch >= 0; ch = sh.next[ch]) {
+    for (int ch = child(cur, cur + 1); ch >= 0; ch = child(cur, ch + 1)) {
       const int x = sh.tok[ch];
       if (greedy) {
         if (x == __float_as_int(st.floor)) { next = ch; break; }
@@ -919,10 +956,10 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
       }
       if (left < 0.f) {                           // after a rejected draw
         float z = 0.f;
-        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const float(&x)[8]) {
-          if (!some(x)) return;
+        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const Raw8<T>& w) {
+          if (!(max8(w) >= st.floor)) return;     // (none of them is kept)
           float y[8];
-          rest8(v, x, y);
+          rest8(v, w, y);
           z += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         });
         z = warp_sum(z);
@@ -973,11 +1010,11 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         if (turn == 1) reset();                   // (nothing left: the target's own)
         float best = 0.f;
         int at = 0x7fffffff;
-        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const float(&x)[8]) {
-          if (!some(x)) return;
+        sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const Raw8<T>& w) {
+          if (!(max8(w) >= st.floor)) return;     // (none of them is kept)
           float y[8], t[8];
           load8(race, v, v1, a.vec_r, t);
-          rest8(v, x, y);
+          rest8(v, w, y);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (y[j] > 0.f) {
@@ -1041,8 +1078,9 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
     rc = launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), kPruneBytes, st, ra);
   }
   if (rc != TV_OK) return rc;
-  return launch_pdl(walk_kernel<T>, dim3(static_cast<unsigned>(kAsCluster) * B), dim3(kWalkThreads),
-                    static_cast<size_t>(S + 31) / 32 * 4, st, wa);
+  const size_t smem = static_cast<size_t>(wa.max_nodes) * sizeof(RowStat) + static_cast<size_t>(S + 31) / 32 * 4;
+  if (smem > 20 << 10 && !smem_limit(walk_kernel<T>, 40 << 10)) return TV_ECUDA;
+  return launch_pdl(walk_kernel<T>, dim3(static_cast<unsigned>(kAsCluster) * B), dim3(kWalkThreads), smem, st, wa);
 }
 
 }  // namespace
@@ -1075,9 +1113,9 @@ TV_API int accept_sampled(const int32_t* parent, const int32_t* tok, const void*
   const bool bf = dtype == TV_BF16;
   const bool vec_p = aligned(p_logits, 16) && ld % (bf ? 8 : 4) == 0;
   const bool vec_q = aligned(q_prob, 16) && ldq % 4 == 0, vec_r = aligned(race, 16) && ldr % 4 == 0;
-  // Rows that cannot be reached are left out where there are more than run at
-  // a time (three CTAs to an SM).
-  const bool prune = static_cast<int64_t>(B) * max_nodes * kAsCluster > 3ll * sm_count() && total_nodes > 0;
+  // Rows that cannot be reached are left out where there are more than twice
+  // what runs at a time (four CTAs to an SM).
+  const bool prune = static_cast<int64_t>(B) * max_nodes * kAsCluster > 8ll * sm_count() && total_nodes > 0;
   auto* stat = static_cast<RowStat*>(ws);
   const RowArgs ra{p_logits, node_off, temperature, top_k, top_p, stat, ld, V, std::max(max_nodes, 1), total_nodes, vec_p,
                    prune ? reinterpret_cast<int32_t*>(stat + total_nodes) : nullptr, parent, tok, q_prob, drawn, u_node,
