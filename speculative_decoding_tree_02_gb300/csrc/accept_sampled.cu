@@ -163,7 +163,7 @@ __device__ __forceinline__ bool accepted(float u, bool drawn, float q, float hav
 }
 
 constexpr int kList = 256;         // listed logits of a warp
-constexpr int kSort = 1024;        // listed logits of a row
+constexpr int kSort = 1024;        // listed logits of a row, at most
 constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
 constexpr int kCutPick = 4;        // or, for k up to 64 kCutPick, to a cut found among the threads' maxima
 constexpr int kScratch = kBins * kAsThreads * 4;
@@ -176,9 +176,11 @@ struct RowShared {
   float tot[kBins];
   float wred[kAsWarps];
   int wred_i[kAsWarps];
+  float wmax[kAsWarps], wcut[kAsWarps], wz[kAsWarps], wzl[kAsWarps];   // per warp, read by the cluster, written once
+  int wfirst[kAsWarps];
   int listed[kAsWarps];            // logits that passed the list's condition, per warp
   float scan[kAsWarps];
-  int hit;
+  int hit;                         // rows that the walk cannot reach: what the first CTA saw
   float out;                       // what the first CTA found
 };
 
@@ -252,23 +254,6 @@ __device__ __forceinline__ float stage8(float* xs, const Raw8<float>& r) {
   *reinterpret_cast<float4*>(xs) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(xs + 4) = make_float4(x[4], x[5], x[6], x[7]);
   return m;
-}
-
-// By the CTA: sorts v[0, n) (n <= kSort), highest first; v has room for the next power of two.
-__device__ __forceinline__ void sort_desc(float* v, int n) {
-  int n2 = 2;
-  while (n2 < n) n2 *= 2;
-  for (int i = n + threadIdx.x; i < n2; i += kAsThreads) v[i] = -INFINITY;
-  for (int k = 2; k <= n2; k *= 2)
-    for (int j = k / 2; j; j /= 2) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < n2 / 2; t += kAsThreads) {
-        const int i = 2 * j * (t / j) + t % j;
-        const float x = v[i], y = v[i + j];
-        if ((x < y) == ((i & k) == 0)) { v[i] = y; v[i + j] = x; }
-      }
-    }
-  __syncthreads();
 }
 
 // Room that a CTA needs to leave out rows: the nodes' parents, and a mark per node.
@@ -356,8 +341,9 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
 // One row of logits: a cluster of 8 CTAs.  The slice of a CTA is staged in
 // shared memory and read once from there in most calls: the highest logit is
 // known by then, so one pass sums the weights and lists those above 2^-12 of
-// the highest, a handful in a peaked distribution; the first CTA sorts the
-// lists of all and finds the threshold by a prefix sum while the others leave.
+// the highest, a handful in a peaked distribution (top-k: those above a cut
+// that the warps' maxima give); the first CTA compares the listed logits with
+// one another, which gives each what lies above it, while the others leave.
 // Where the list does not reach the threshold (flat distributions, large k)
 // or overflows, the logits are binned by powers of two of the weight, the
 // threshold's bin by 16th parts of it, twice, until a bin is short enough to
@@ -395,7 +381,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   const float c = fmaxf(fminf(kLog2e / temp, 1e30f), 1e-30f);
   int k = kTrunc && a.top_k ? a.top_k[r] : 0;
   if (k >= V) k = 0;
-  const float nucleus = kTrunc && a.top_p ? a.top_p[r] : 1.f;
+  const float nucleus = kTrunc && a.top_p ? (a.top_p[r] < 0.f ? 0.f : a.top_p[r]) : 1.f;
   const bool by_k = !greedy && k > 0, by_p = !greedy && nucleus < 1.f;
   T* xs = reinterpret_cast<T*>(dyn);              // the slice, each thread's own eighths
 
@@ -403,13 +389,25 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   float m = -INFINITY, s = 0.f;
   int at = 0x7fffffff;
   const bool stage = by_k || by_p;
-  sweep<kAsThreads, 5>(p, v0, v1, a.vec, [&](int v, const Raw8<T>& w) {
-    if constexpr (kTrunc) {
-      if (stage) {
-        m = fmaxf(m, stage8(xs + (v - v0), w));
-        return;
+  if constexpr (kTrunc) {
+    if (stage) {
+      if (a.vec) {                                // all of them on their way at once
+        for (int v = v0 + 8 * tid; v + 8 <= v1; v += 8 * kAsThreads) {
+          const auto to = static_cast<uint32_t>(__cvta_generic_to_shared(xs + (v - v0)));
+#pragma unroll
+          for (int u = 0; u < static_cast<int>(sizeof(T) / 2); ++u)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * u), "l"(p + v + 16 / sizeof(T) * u)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int v = v0 + 8 * tid; v < v1; v += 8 * kAsThreads)
+          m = fmaxf(m, stage8(xs + (v - v0), v + 8 <= v1 ? staged8(xs + (v - v0)) : tail8(p, v, v1)));
+      } else {
+        sweep<kAsThreads, 5>(p, v0, v1, false, [&](int v, const Raw8<T>& w) { m = fmaxf(m, stage8(xs + (v - v0), w)); });
       }
     }
+  }
+  if (!stage) sweep<kAsThreads, 5>(p, v0, v1, a.vec, [&](int v, const Raw8<T>& w) {
     float x[8], m8 = max8(w);
     widen8(w, x);
     if (greedy) {
@@ -431,48 +429,53 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
   });
   if (a.dead && i > 0) cl::wait();
   int e = 0;
-  // over the cluster: the maximum, its first place or the sum
-  const float wm = warp_max(m);
-  if (lane == 0) sh.wred[warp] = wm;
-  const int wi = __reduce_min_sync(0xffffffffu, m == wm && greedy ? at : 0x7fffffff);
-  if (lane == 0) sh.wred_i[warp] = wi;
-  // For top-k a cut that at least k logits reach: every warp's j-th highest of
-  // its lanes' maxima, 64 j >= k, the lowest of these over the cluster.
+  // every warp's maximum and its first place; for top-k also the j-th highest
+  // of its lanes' maxima, 64 j >= k
   const int pick = (k + kAsCluster * kAsWarps - 1) / (kAsCluster * kAsWarps);
   const bool by_cut = kTrunc && by_k && pick <= kCutPick;
-  if (by_cut) {
-    float x = m;
-    for (int t = 1; t < pick; ++t)
-      if (lane == __ffs(static_cast<int>(__ballot_sync(0xffffffffu, x == warp_max(x)))) - 1) x = -INFINITY;
-    x = warp_max(x);
-    if (lane == 0) sh.scan[warp] = x;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    float top = sh.wred[0];
-    for (int w = 1; w < kAsWarps; ++w) top = fmaxf(top, sh.wred[w]);
-    int first = 0x7fffffff;
-    for (int w = 0; w < kAsWarps; ++w)
-      if (sh.wred[w] == top) first = min(first, sh.wred_i[w]);
-    sh.xf[e & 1][0] = top;
-    sh.xi[e & 1][0] = first;
+  {
+    const float wm = warp_max(m);
+    const int wi = greedy ? __reduce_min_sync(0xffffffffu, m == wm ? at : 0x7fffffff) : 0;
+    if (lane == 0) { sh.wmax[warp] = wm; sh.wfirst[warp] = wi; }
     if (by_cut) {
-      float x = sh.scan[0];
-      for (int w = 1; w < kAsWarps; ++w) x = fminf(x, sh.scan[w]);
-      sh.xf[e & 1][1] = x;
+      float x = m, y = wm;
+      for (int t = 1; t < pick; ++t) {
+        if (lane == __ffs(static_cast<int>(__ballot_sync(0xffffffffu, x == y))) - 1) x = -INFINITY;
+        y = warp_max(x);
+      }
+      if (lane == 0) sh.wcut[warp] = y;
     }
   }
+  // lane l: the numbers of warps l and l + 32 of the cluster's 64
+  auto of64 = [&](const auto* v, auto& c0, auto& c1) {
+    c0 = cl::peek(v + (lane & 7), lane >> 3);
+    c1 = cl::peek(v + (lane & 7), 4 + (lane >> 3));
+  };
   cl::sync();
-  float all = -INFINITY, cut = INFINITY;
+  float all, cut = -INFINITY;
   int first = 0x7fffffff;
-#pragma unroll
-  for (uint32_t q = 0; q < kAsCluster; ++q) {
-    if (by_cut) cut = fminf(cut, cl::peek(&sh.xf[e & 1][1], q));
-    const float t = cl::peek(&sh.xf[e & 1][0], q);
-    const int f = cl::peek(&sh.xi[e & 1][0], q);
-    if (t > all) { all = t; first = f; }          // (ranks in index order: the first of equals stays)
+  {
+    float c0, c1;
+    of64(sh.wmax, c0, c1);
+    all = warp_max(fmaxf(c0, c1));
+    if (greedy) {
+      int f0, f1;
+      of64(sh.wfirst, f0, f1);
+      first = __reduce_min_sync(0xffffffffu, min(c0 == all ? f0 : 0x7fffffff, c1 == all ? f1 : 0x7fffffff));
+    }
+    if (by_cut) {                                 // the highest number that enough warps reach for k logits
+      of64(sh.wcut, c0, c1);
+      const int warps = (k + pick - 1) / pick;
+      int a0 = 0, a1 = 0;
+#pragma unroll 8
+      for (int t = 0; t < 32; ++t) {
+        const float x = __shfl_sync(0xffffffffu, c0, t), y = __shfl_sync(0xffffffffu, c1, t);
+        a0 += (x > c0 ? 1 : 0) + (y > c0 ? 1 : 0);
+        a1 += (x > c1 ? 1 : 0) + (y > c1 ? 1 : 0);
+      }
+      cut = -warp_max(fmaxf(a0 < warps ? -c0 : -INFINITY, a1 < warps ? -c1 : -INFINITY));
+    }
   }
-  ++e;
   // by the first CTA: the row is done
   auto publish = [&](const RowStat& st) {
     if (tid == 0) a.stat[row] = st;
@@ -572,8 +575,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       // After a cluster barrier: logits on the cluster's lists, -1 when one overflowed or they are too many.
       int c0, c1;                                 // lane l: the counts of segments l and l + 32 of the 64
       auto usable = [&]() {
-        c0 = cl::peek(&sh.listed[lane & 7], lane >> 3);
-        c1 = cl::peek(&sh.listed[lane & 7], 4 + (lane >> 3));
+        of64(sh.listed, c0, c1);
         const bool over = __any_sync(0xffffffffu, c0 > kList || c1 > kList);
         const int sum = __reduce_add_sync(0xffffffffu, min(c0, kList) + min(c1, kList));
         return over || sum > kSort ? -1 : sum;
@@ -595,49 +597,70 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
           hist[before + t] = cl::peek(&list[q * kList + t - o], warp);
         }
       };
-      // Prefix sums of the sorted list's weights: into hist[kSort ..].
-      const float* pre = hist + kSort;
-      auto prefix = [&](int cnt) {
-        float w[kSort / kAsThreads], t = 0.f;
-#pragma unroll
-        for (int j = 0; j < kSort / kAsThreads; ++j) {
-          const int q = tid * (kSort / kAsThreads) + j;
-          w[j] = t += q < cnt ? weight(hist[q]) : 0.f;
-        }
-        float inc = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        if (lane == 31) sh.scan[warp] = inc;
-        float before = __shfl_up_sync(0xffffffffu, inc, 1);
-        if (lane == 0) before = 0.f;
+      // Sum over the CTA, by all of its threads.
+      auto cta_sum = [&](float x) {
+        x = warp_sum(x);
         __syncthreads();
-        for (int q = 0; q < warp; ++q) before += sh.scan[q];
-#pragma unroll
-        for (int j = 0; j < kSort / kAsThreads; ++j) hist[kSort + tid * (kSort / kAsThreads) + j] = before + w[j];
+        if (lane == 0) sh.wred[warp] = x;
         __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAsWarps; ++w) x += sh.wred[w];
+        return x;
       };
-      // How many q < cnt have fn(q).
-      auto count = [&](int cnt, auto&& fn) {
-        if (tid == 0) sh.hit = 0;
+      // Of the copied list: how many logits are higher than each and what these
+      // weigh, which tells what top-k (of `left` tokens; 0: off) and top-p (up to
+      // the mass `target`, or its share of z; below 0: off) keep, whole classes as
+      // equals get equal numbers.  Sets out.floor and mass, `above` included.
+      auto settle = [&](int cnt, int left, float above, float target, float share) {
+        constexpr int kOwn = kSort / kAsThreads;
+        float* ws = hist + kSort;                 // weights
+        const int pad = (cnt + 3) / 4 * 4;
+        for (int q = tid; q < pad; q += kAsThreads) {
+          if (q >= cnt) hist[q] = -INFINITY;
+          ws[q] = q < cnt ? weight(hist[q]) : 0.f;
+        }
         __syncthreads();
-        int mine = 0;
-        for (int q = tid; q < cnt; q += kAsThreads) mine += fn(q) ? 1 : 0;
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0 && mine) atomicAdd(&sh.hit, mine);
+        float own[kOwn], mine[kOwn];
+        bool keep[kOwn];
+        float z = 0.f, low = INFINITY;
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u) {
+          const int q = tid + u * kAsThreads;
+          own[u] = q < cnt ? hist[q] : INFINITY;
+          mine[u] = 0.f;
+          int more = 0;
+          if (u * kAsThreads + 32 * warp < cnt) { // (for the warp as a whole)
+            for (int j = 0; j < pad; j += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(hist + j), w = *reinterpret_cast<const float4*>(ws + j);
+              if (l.x > own[u]) { ++more; mine[u] += w.x; }
+              if (l.y > own[u]) { ++more; mine[u] += w.y; }
+              if (l.z > own[u]) { ++more; mine[u] += w.z; }
+              if (l.w > own[u]) { ++more; mine[u] += w.w; }
+            }
+          }
+          keep[u] = q < cnt && (left == 0 || more < left);
+          if (keep[u]) { z += ws[q]; low = fminf(low, own[u]); }
+        }
+        if (left > 0) z = cta_sum(z);
+        if (share >= 0.f) target = share * z;
+        if (target >= 0.f) {
+          z = 0.f;
+          low = INFINITY;
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u) {
+            keep[u] = keep[u] && (above + mine[u] < target || mine[u] == 0.f);      // (the highest class always)
+            if (keep[u]) { z += ws[tid + u * kAsThreads]; low = fminf(low, own[u]); }
+          }
+          z = cta_sum(z);
+        }
+        mass = above + z;
+        low = -warp_max(-low);
+        if (lane == 0) sh.scan[warp] = low;
         __syncthreads();
-        const int h = sh.hit;
-        __syncthreads();
-        return h;
-      };
-      // Of the sorted list (behind `above` in mass): the threshold of top-p at `target`, and the mass down to it.
-      auto settle_p = [&](int cnt, int kept, float above, float target) {
-        const int in = max(1, count(kept, [&](int q) { return above + (q ? pre[q - 1] : 0.f) < target; }));
-        out.floor = hist[in - 1];
-        const int last = count(cnt, [&](int q) { return hist[q] >= out.floor; });
-        mass = above + pre[last - 1];
+#pragma unroll
+        for (int w = 0; w < kAsWarps; ++w) low = fminf(low, sh.scan[w]);
+        out.floor = low;
       };
       // The lists hold every logit that matters: the first CTA finds the
       // threshold, the others are done.
@@ -645,15 +668,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         if (rank == 0) copy();
         cl::sync();
         if (rank != 0) return;
-        sort_desc(hist, cnt);
-        prefix(cnt);
-        int kept = cnt;
-        if (by_k) {
-          out.floor = hist[k - 1];
-          kept = count(cnt, [&](int q) { return hist[q] >= out.floor; });
-          mass = z = pre[kept - 1];
-        }
-        if (by_p) settle_p(cnt, kept, 0.f, nucleus * z);
+        settle(cnt, by_k ? k : 0, 0.f, by_p && !by_k ? nucleus * z : -1.f, by_p && by_k ? nucleus : -1.f);
         out.inv = mass > 0.f ? 1.f / mass : 0.f;
         publish(out);
       };
@@ -663,19 +678,16 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       float z = 0.f, zl = 0.f;
       const float lowest = -3.402823466e38f;
       make_list(V <= kSort ? lowest : fmaxf(by_cut ? cut : top - kCut / c, lowest), INFINITY, !by_k, z, zl);
-      {
-        const float w0 = warp_sum(z), w1 = warp_sum(zl);
-        if (lane == 0) { sh.wred[warp] = w0; sh.scan[warp] = w1; }
-        __syncthreads();
-        if (tid == 0) {
-          z = zl = 0.f;
-          for (int w = 0; w < kAsWarps; ++w) { z += sh.wred[w]; zl += sh.scan[w]; }
-          sh.xf[e & 1][0] = z;
-          sh.xf[e & 1][1] = zl;
-        }
-        cluster_sums(sh, e++, 2);
-        z = sh.tot[0];
-        zl = sh.tot[1];
+      z = warp_sum(z);
+      zl = warp_sum(zl);
+      if (lane == 0) { sh.wz[warp] = z; sh.wzl[warp] = zl; }
+      cl::sync();
+      if (!by_k) {
+        float x, y;
+        of64(sh.wz, x, y);
+        z = warp_sum(x + y);
+        of64(sh.wzl, x, y);
+        zl = warp_sum(x + y);
       }
       int cnt = usable();
       if (cnt > 0 && (by_k ? k <= cnt : zl >= nucleus * z)) {
@@ -761,14 +773,13 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
               if (rank == 0) copy();
               cl::sync();                         // (this and the next: sh.out is written between two barriers)
               if (rank == 0) {
-                sort_desc(hist, cnt);
                 if (weigh) {
-                  prefix(cnt);
-                  settle_p(cnt, cnt, above, target);
+                  settle(cnt, 0, above, target, -1.f);
                   out.inv = mass > 0.f ? 1.f / mass : 0.f;
                   publish(out);
-                } else if (tid == 0) {
-                  sh.out = hist[min(cnt, static_cast<int>(target - above)) - 1];
+                } else {
+                  settle(cnt, max(1, static_cast<int>(target - above)), 0.f, -1.f, -1.f);
+                  if (tid == 0) sh.out = out.floor;
                 }
               }
               if (weigh) return true;
