@@ -298,6 +298,175 @@ __global__ void __launch_bounds__(kTile, 4) mma_kernel(const MassArgs a, const u
   finish(a, sp, row, t0 + tid, true, part[tid], part, rank, parts);
 }
 
+// Up to kFewRows query rows per KV head: all of them stay in shared memory and
+// a warp walks over tiles of 32 tokens, the next tile's codes on their way
+// while it works on one.
+constexpr int kFewRows = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const int run, const uint32_t magic) {
+  constexpr int kRun = D / 32;                    // words, and 16-byte units of a row, of a lane
+  constexpr int kBlock = 8 * D * 2;               // bytes of eight rows
+  extern __shared__ __align__(16) uint8_t qs[];
+  __shared__ __align__(8) float s_lse[kFewRows];
+  __shared__ __align__(8) int s_vis[kFewRows];
+  __shared__ int s_first;
+  griddep_wait();
+  griddep_release();
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int r = blockIdx.z, h = blockIdx.y, g = a.Hq / a.Hkv;
+  const MassSpan sp = mass_span(a, r, &s_first);
+  if (blockIdx.x == 0 && h == 0 && tid == 0 && sp.bad && a.err) *a.err = 1;
+  const int t_lo = static_cast<int>(blockIdx.x) * run, t_hi = min(t_lo + run, sp.len);
+  if (t_lo >= t_hi) return;
+  const int64_t row = static_cast<int64_t>(r) * a.Hkv + h;
+  const int rows = sp.count * g, blocks = (rows + 7) / 8;
+
+  // a warp's tile: codes of tokens t + 8 i (t = the tile's first + lane / 4), and what its own token had
+  struct Tile {
+    uint32_t w[4][kRun];
+    uint16_t sc[4];
+    float had;
+    int page[2];                                  // of tokens 0..15 and 16..31 of the tile
+  };
+  const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.table_ld;
+  const int ps = 31 - __clz(a.P);
+  auto pages = [&](int t0, int (&page)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      page[i] = -1;
+      if (t0 + 16 * i < t_hi) page[i] = __ldg(table + ((t0 + 16 * i) >> ps));
+    }
+  };
+  auto fetch = [&](int t0, Tile& x) {
+    if (t0 >= t_hi) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int page = x.page[i >> 1], t = t0 + (lane >> 2) + 8 * i, slot = t & (a.P - 1);
+#pragma unroll
+      for (int w = 0; w < kRun; ++w) x.w[i][w] = 0;
+      x.sc[i] = 0;
+      if (page >= 0 && page < a.n_pages && t < t_hi) {
+        const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
+        const uint8_t* at = blk + k_word(a.P, slot, (lane & 3) * (D / 4));
+        if constexpr (D == 128) {
+          const uint4 v = ldg_stream(at);
+          x.w[i][0] = v.x; x.w[i][1] = v.y; x.w[i][2] = v.z; x.w[i][3] = v.w;
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+          x.w[i][0] = v.x; x.w[i][1] = v.y;
+        }
+        x.sc[i] = __ldg(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot)));
+      }
+    }
+    const int t = t0 + (lane >> 2) + 8 * (lane & 3);
+    x.had = t < t_hi ? mass_before(a, sp, row, t) : 0.f;
+  };
+  Tile next;
+  int t0 = t_lo + 32 * warp;
+  pages(t0, next.page);
+
+  // the rows, in fragment order
+  for (int u = tid; u < 8 * blocks * (D / 8); u += kTile) {
+    const int i = u / (D / 8), x = u % (D / 8);
+    const uint16_t* src = static_cast<const uint16_t*>(a.q);
+    bool some = i < rows;
+    if (some) {
+      const MassRow m = mass_row(a, sp, r, i / g);
+      some = !m.bad;
+      if (some) src += m.src * a.ldq + static_cast<int64_t>(h * g + i % g) * D + 8 * x;
+    }
+    cp16(tc::smem_u32(qs + (i / 8) * kBlock + (x % kRun) * 512 + ((i % 8) * 4 + x / kRun) * 16), src, some);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int i = tid; i < 8 * blocks; i += kTile) {
+    int vis = 0;
+    float l = kInf;
+    if (i < rows) {
+      const MassRow m = mass_row(a, sp, r, i / g);
+      if (m.bad && a.err) *a.err = 1;
+      if (!m.bad) {
+        l = a.lse[m.src * a.Hq + h * g + i % g];
+        vis = l == -kInf ? 0 : m.vis;             // (a row that saw nothing weighs nothing)
+      }
+    }
+    s_vis[i] = vis;
+    s_lse[i] = l == -kInf ? kInf : l * kLog2e;
+  }
+  fetch(t0, next);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+
+  const float scale2 = a.scale * kLog2e;
+  for (; t0 < t_hi; t0 += kTile) {
+    const Tile cur = next;
+    pages(t0 + kTile, next.page);
+    uint32_t ka[2][2 * kRun][4];
+    float fac[4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int w = 0; w < kRun; ++w) {
+        uint32_t lo[4], hi[4];
+        decode8(cur.w[2 * m][w], lo, magic);
+        decode8(cur.w[2 * m + 1][w], hi, magic);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ka[m][2 * w + p][0] = lo[2 * p];
+          ka[m][2 * w + p][1] = hi[2 * p];
+          ka[m][2 * w + p][2] = lo[2 * p + 1];
+          ka[m][2 * w + p][3] = hi[2 * p + 1];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fac[i] = __uint_as_float(static_cast<uint32_t>(cur.sc[i]) << 16) * scale2;
+    fetch(t0 + kTile, next);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < blocks; ++n) {
+      const int2 vis = *reinterpret_cast<const int2*>(&s_vis[8 * n + 2 * (lane & 3)]);
+      const int vmin = min(vis.x, vis.y), vmax = max(vis.x, vis.y);
+      if (!__any_sync(0xffffffffu, vmax > t0)) continue;
+      const bool whole = __all_sync(0xffffffffu, vmin >= t0 + 32);
+      float acc[2][4] = {};
+#pragma unroll
+      for (int w = 0; w < kRun; ++w) {
+        const uint4 v = *reinterpret_cast<const uint4*>(qs + n * kBlock + w * 512 + lane * 16);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma16816(acc[m], ka[m][2 * w], v.x, v.y);
+          mma16816(acc[m], ka[m][2 * w + 1], v.z, v.w);
+        }
+      }
+      const float2 l = *reinterpret_cast<const float2*>(&s_lse[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = ex2(fmaf(acc[i >> 1][2 * (i & 1)], fac[i], -l.x));
+        const float y = ex2(fmaf(acc[i >> 1][2 * (i & 1) + 1], fac[i], -l.y));
+        if (whole) {
+          sum[i] += x + y;
+        } else {
+          const int t = t0 + (lane >> 2) + 8 * i;
+          sum[i] += (t < vis.x ? x : 0.f) + (t < vis.y ? y : 0.f);
+        }
+      }
+    }
+    // a token's sums lie in four lanes, each of which takes one of their four tokens
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    const int i = lane & 3, t = t0 + (lane >> 2) + 8 * i;
+    const float mine = i == 0 ? sum[0] : i == 1 ? sum[1] : i == 2 ? sum[2] : sum[3];
+    if (t < t_hi) {
+      const int page = i < 2 ? cur.page[0] : cur.page[1];
+      const bool ok = page >= 0 && page < a.n_pages;
+      if (!ok && a.err) *a.err = 1;
+      a.score_out[row * a.out_ld + t] = cur.had + (ok ? mine : 0.f);
+    }
+  }
+}
+
 }  // namespace
 
 int mass_simt(const MassArgs& a, int B, int d, int parts, cudaStream_t st) {
@@ -307,6 +476,16 @@ int mass_simt(const MassArgs& a, int B, int d, int parts, cudaStream_t st) {
                   : cl::launch_pdl(simt_kernel<64>, parts, grid, dim3(kTile), 0, st, a, u);
 }
 int mass_mma(const MassArgs& a, int B, int d, int parts, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.max_rows) * (a.Hq / a.Hkv);
+  if (rows <= kFewRows) {
+    // tokens of a CTA: about four CTAs' worth for each one that is resident, 128 at least
+    const int64_t all = static_cast<int64_t>(a.max_len) * a.Hkv * B;
+    const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (16ll * kTile * sm_count())))) * kTile;
+    const dim3 few(static_cast<unsigned>((a.max_len + run - 1) / run), a.Hkv, B);
+    const size_t smem = static_cast<size_t>((rows + 7) / 8) * 16 * d;
+    return d == 128 ? launch_pdl(few_kernel<128>, few, dim3(kTile), smem, st, a, run, kMagic)
+                    : launch_pdl(few_kernel<64>, few, dim3(kTile), smem, st, a, run, kMagic);
+  }
   const dim3 grid(static_cast<unsigned>((a.max_len + kTile - 1) / kTile) * parts, a.Hkv, B);
   const auto u = static_cast<uint32_t>(parts);
   return d == 128 ? cl::launch_pdl(mma_kernel<128>, parts, grid, dim3(kTile), 0, st, a, u, kMagic)
