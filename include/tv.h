@@ -646,6 +646,7 @@ int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pa
  *   score_in [B, Hkv, score_in_ld] or NULL (zeros); may be score_out
  *   max_len bounds cache_len (launch geometry), <= score_out_ld, score_in_ld
  *   decay in [0, 1] (0: score_in is not read)
+ *   d in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 64
  * Outputs: score_out float [B, Hkv, score_out_ld], entries from cache_len on
  *   are not written.
  * A row with lse = -inf (it saw nothing) weighs nothing; a NaN row makes the

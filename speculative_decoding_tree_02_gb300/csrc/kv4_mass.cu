@@ -2,7 +2,7 @@
 //   m[t] = sum over rows i and the query heads of t's KV head of exp(scale q_i.k_t - lse_i),
 // the weights being those of an attention whose log-sum-exp is given: no
 // maximum, no second pass, and every token is independent of the others.
-// Two kernels here: fp32 rows on the CUDA cores, bf16 rows on mma.sync.
+// Here the kernels for fp32 rows (CUDA cores) and for few bf16 rows (mma.sync), and the entry point.
 #include <algorithm>
 
 #include "kv4_device.cuh"
@@ -124,8 +124,6 @@ __global__ void __launch_bounds__(kTile) simt_kernel(const MassArgs a, const uin
 }
 
 // ------------------------------------------------------------------ bf16 rows
-constexpr int kMmaRows = 64;    // rows staged at a time
-
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -136,172 +134,17 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool some) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-// S = K Q^T with tokens as the rows of the MMA: a warp owns 32 tokens, whose
-// codes it turns into operands once and keeps in registers (64 at d = 128),
-// and passes over all rows, eight at a time.  The dims are permuted alike in
-// both operands so that a lane's share of a token is d / 4 consecutive dims,
-// whole words of codes, and its share of a query row is one run of the row:
-// staged in fragment order, a block of eight rows is read back in 16-byte
-// accesses without conflicts.  The scale of a token and the -lse of a row
-// enter in the exponent, exp(scale s_t (n.q) - lse) = 2^(acc f_t - l).
-// A cluster of up to 8 CTAs shares the rows of one tile of tokens where tiles
-// alone would not fill the SMs.
-template <int D>
-__global__ void __launch_bounds__(kTile, 4) mma_kernel(const MassArgs a, const uint32_t parts, const uint32_t magic) {
-  constexpr int kRun = D / 32;                    // words, and 16-byte units of a row, of a lane
-  constexpr int kBlock = 8 * D * 2;               // bytes of eight rows
-  __shared__ __align__(16) uint8_t qs[2][kMmaRows / 8 * kBlock];
-  __shared__ __align__(8) float s_lse[2][kMmaRows];
-  __shared__ __align__(8) int s_vis[2][kMmaRows];
-  __shared__ float part[kTile];
-  __shared__ int s_first;
-  griddep_wait();
-  griddep_release();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.z, h = blockIdx.y, g = a.Hq / a.Hkv;
-  const uint32_t rank = parts > 1 ? cl::rank() : 0;
-  const int t0 = static_cast<int>(blockIdx.x / parts) * kTile;
-  const MassSpan sp = mass_span(a, r, &s_first);
-  if (blockIdx.x == 0 && h == 0 && tid == 0 && sp.bad && a.err) *a.err = 1;
-  if (t0 >= sp.len) return;                       // (all CTAs of the cluster alike)
-  const int64_t row = static_cast<int64_t>(r) * a.Hkv + h;
-  const int rows = sp.count * g;
-
-  // rows of chunk `c`, on their way into buffer b
-  auto stage = [&](int i0, int b) {
-    for (int u = tid; u < kMmaRows * (D / 8); u += kTile) {
-      const int i = u / (D / 8), x = u % (D / 8);
-      const uint16_t* src = static_cast<const uint16_t*>(a.q);
-      bool some = i0 + i < rows;
-      if (some) {
-        const MassRow m = mass_row(a, sp, r, (i0 + i) / g);
-        some = !m.bad;
-        if (some) src += m.src * a.ldq + static_cast<int64_t>(h * g + (i0 + i) % g) * D + 8 * x;
-      }
-      const int at = (i / 8) * kBlock + (x % kRun) * 512 + ((i % 8) * 4 + x / kRun) * 16;
-      cp16(tc::smem_u32(&qs[b][at]), src, some);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (tid < kMmaRows) {
-      int vis = 0;
-      float l = kInf;
-      if (i0 + tid < rows) {
-        const MassRow m = mass_row(a, sp, r, (i0 + tid) / g);
-        if (m.bad && a.err) *a.err = 1;
-        if (!m.bad) {
-          l = a.lse[m.src * a.Hq + h * g + (i0 + tid) % g];
-          vis = l == -kInf ? 0 : m.vis;           // (a row that saw nothing weighs nothing)
-        }
-      }
-      s_vis[b][tid] = vis;
-      s_lse[b][tid] = l == -kInf ? kInf : l * kLog2e;
-    }
-  };
-  const int step = static_cast<int>(parts) * kMmaRows;
-  int i0 = static_cast<int>(rank) * kMmaRows, b = 0;
-  if (a.causal && !a.vis_prefix) {                // rows j < t0 - old see nothing of this tile
-    const int64_t first = (static_cast<int64_t>(t0) - sp.old) * g;
-    if (first > i0) i0 += static_cast<int>((min(first, static_cast<int64_t>(rows)) - i0) / step * step);
-  }
-  if (i0 < rows) stage(i0, 0);
-
-  // keys: tokens t0 + 32 warp + lane / 4 + 8 i
-  uint32_t ka[2][2 * kRun][4];
-  float fac[4];
-  bool ok[4];
-  uint32_t words[4][kRun];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 32 * warp + (lane >> 2) + 8 * i;
-    const int page = t < sp.len ? mass_page(a, r, t) : -1;
-    if (t < sp.len && page < 0 && a.err) *a.err = 1;
-    ok[i] = page >= 0;
-    fac[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRun; ++w) words[i][w] = 0;
-    if (ok[i]) {
-      const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
-      const int slot = t % a.P;
-      const uint8_t* at = blk + k_word(a.P, slot, (lane & 3) * (D / 4));
-      if constexpr (D == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(at);
-        words[i][0] = v.x; words[i][1] = v.y; words[i][2] = v.z; words[i][3] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(at);
-        words[i][0] = v.x; words[i][1] = v.y;
-      }
-      fac[i] = bf16_at(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot))) * (a.scale * kLog2e);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int w = 0; w < kRun; ++w) {
-      uint32_t lo[4], hi[4];
-      decode8(words[2 * m][w], lo, magic);
-      decode8(words[2 * m + 1][w], hi, magic);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ka[m][2 * w + p][0] = lo[2 * p];
-        ka[m][2 * w + p][1] = hi[2 * p];
-        ka[m][2 * w + p][2] = lo[2 * p + 1];
-        ka[m][2 * w + p][3] = hi[2 * p + 1];
-      }
-    }
-
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (; i0 < rows; i0 += step, b ^= 1) {
-    const bool more = i0 + step < rows;
-    if (more) stage(i0 + step, b ^ 1);
-    if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    const int blocks = (min(kMmaRows, rows - i0) + 7) / 8;
-    const int tw = t0 + 32 * warp;                // first token of the warp
-    for (int n = 0; n < blocks; ++n) {
-      const int2 vis = *reinterpret_cast<const int2*>(&s_vis[b][8 * n + 2 * (lane & 3)]);
-      const int vmin = min(vis.x, vis.y), vmax = max(vis.x, vis.y);
-      if (!__any_sync(0xffffffffu, vmax > tw)) continue;
-      const bool whole = __all_sync(0xffffffffu, vmin >= tw + 32);
-      float acc[2][4] = {};
-#pragma unroll
-      for (int w = 0; w < kRun; ++w) {
-        const uint4 v = *reinterpret_cast<const uint4*>(&qs[b][n * kBlock + w * 512 + lane * 16]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma16816(acc[m], ka[m][2 * w], v.x, v.y);
-          mma16816(acc[m], ka[m][2 * w + 1], v.z, v.w);
-        }
-      }
-      const float2 l = *reinterpret_cast<const float2*>(&s_lse[b][8 * n + 2 * (lane & 3)]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = ex2(fmaf(acc[i >> 1][2 * (i & 1)], fac[i], -l.x));
-        const float y = ex2(fmaf(acc[i >> 1][2 * (i & 1) + 1], fac[i], -l.y));
-        if (whole) {
-          sum[i] += x + y;
-        } else {
-          const int t = tw + (lane >> 2) + 8 * i;
-          sum[i] += (t < vis.x ? x : 0.f) + (t < vis.y ? y : 0.f);
-        }
-      }
-    }
-    __syncthreads();
-  }
-  // a token's sums lie in four lanes; then thread = token
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-    if ((lane & 3) == 0) part[32 * warp + (lane >> 2) + 8 * i] = ok[i] ? sum[i] : 0.f;
-  }
-  __syncwarp();
-  finish(a, sp, row, t0 + tid, true, part[tid], part, rank, parts);
-}
-
-// Up to kFewRows query rows per KV head: all of them stay in shared memory and
-// a warp walks over tiles of 32 tokens, the next tile's codes on their way
+// S = K Q^T with tokens as the rows of the MMA: a warp owns 32 tokens at a
+// time, whose codes it turns into operands once and keeps in registers (64 at
+// d = 128), and passes over all rows, eight at a time.  The dims are permuted
+// alike in both operands so that a lane's share of a token is d / 4 consecutive
+// dims, whole words of codes, and its share of a query row is one run of the
+// row: staged in fragment order, a block of eight rows is read back in 16-byte
+// accesses without conflicts.  The scale of a token and the -lse of a row enter
+// in the exponent, exp(scale s_t (n.q) - lse) = 2^(acc f_t - l).
+// The query rows of a KV head, kFewRows at most, stay in shared memory and a warp
+// walks over tiles of 32 tokens, the next tile's codes on their way
 // while it works on one.
-constexpr int kFewRows = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const int run, const uint32_t magic) {
@@ -469,27 +312,25 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
 
 }  // namespace
 
-int mass_simt(const MassArgs& a, int B, int d, int parts, cudaStream_t st) {
+int mass_simt(const MassArgs& a, int B, int d, cudaStream_t st) {
+  // a cluster shares a tile's rows where the tiles alone leave SMs idle
+  const int64_t tiles = static_cast<int64_t>((a.max_len + kTile - 1) / kTile) * a.Hkv * B;
+  const int64_t chunks = (static_cast<int64_t>(a.max_rows) * (a.Hq / a.Hkv) + kSimtRows - 1) / kSimtRows;
+  int parts = 1;
+  while (parts < 8 && 2 * parts <= chunks && tiles * parts < 2ll * sm_count()) parts *= 2;
   const dim3 grid(static_cast<unsigned>((a.max_len + kTile - 1) / kTile) * parts, a.Hkv, B);
   const auto u = static_cast<uint32_t>(parts);
   return d == 128 ? cl::launch_pdl(simt_kernel<128>, parts, grid, dim3(kTile), 0, st, a, u)
                   : cl::launch_pdl(simt_kernel<64>, parts, grid, dim3(kTile), 0, st, a, u);
 }
-int mass_mma(const MassArgs& a, int B, int d, int parts, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.max_rows) * (a.Hq / a.Hkv);
-  if (rows <= kFewRows) {
-    // tokens of a CTA: about four CTAs' worth for each one that is resident, 128 at least
-    const int64_t all = static_cast<int64_t>(a.max_len) * a.Hkv * B;
-    const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (16ll * kTile * sm_count())))) * kTile;
-    const dim3 few(static_cast<unsigned>((a.max_len + run - 1) / run), a.Hkv, B);
-    const size_t smem = static_cast<size_t>((rows + 7) / 8) * 16 * d;
-    return d == 128 ? launch_pdl(few_kernel<128>, few, dim3(kTile), smem, st, a, run, kMagic)
-                    : launch_pdl(few_kernel<64>, few, dim3(kTile), smem, st, a, run, kMagic);
-  }
-  const dim3 grid(static_cast<unsigned>((a.max_len + kTile - 1) / kTile) * parts, a.Hkv, B);
-  const auto u = static_cast<uint32_t>(parts);
-  return d == 128 ? cl::launch_pdl(mma_kernel<128>, parts, grid, dim3(kTile), 0, st, a, u, kMagic)
-                  : cl::launch_pdl(mma_kernel<64>, parts, grid, dim3(kTile), 0, st, a, u, kMagic);
+int mass_few(const MassArgs& a, int B, int d, cudaStream_t st) {
+  // tokens of a CTA: about four CTAs' worth for each one that is resident, 128 at least
+  const int64_t all = static_cast<int64_t>(a.max_len) * a.Hkv * B, rows = static_cast<int64_t>(a.max_rows) * (a.Hq / a.Hkv);
+  const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (16ll * kTile * sm_count())))) * kTile;
+  const dim3 grid(static_cast<unsigned>((a.max_len + run - 1) / run), a.Hkv, B);
+  const size_t smem = static_cast<size_t>((rows + 7) / 8) * 16 * d;
+  return d == 128 ? launch_pdl(few_kernel<128>, grid, dim3(kTile), smem, st, a, run, kMagic)
+                  : launch_pdl(few_kernel<64>, grid, dim3(kTile), smem, st, a, run, kMagic);
 }
 
 }  // namespace kv4
@@ -506,7 +347,7 @@ TV_API int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype
   if (dtype != TV_F32 && dtype != TV_BF16) return TV_EINVAL;
   if (B < 0 || max_rows < 0 || total_rows < 0 || max_len < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return TV_EINVAL;
   if (n_pages < 0 || table_ld < 0 || page_size <= 0 || path_ld < 0) return TV_EINVAL;
-  if (!kv4::page_size_ok(page_size) || (d != 64 && d != 128)) return TV_EUNSUPPORTED;
+  if (!kv4::page_size_ok(page_size) || (d != 64 && d != 128) || Hq / Hkv > 64) return TV_EUNSUPPORTED;
   if (B > 65535 || Hkv > 65535 || static_cast<int64_t>(table_ld) * page_size > 0x7fffffffll ||
       max_len > 0x7fffffff - 4096 || static_cast<int64_t>(max_rows) * (Hq / Hkv) > 0x7fffffff - 4096)
     return TV_EUNSUPPORTED;
@@ -523,11 +364,8 @@ TV_API int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype
   const kv4::MassArgs a{q, lse, static_cast<const uint8_t*>(cache), block_table, cache_len, row_off, path, vis_prefix,
                         old_len, score_in, score_out, err, ldq, score_in_ld, score_out_ld, n_pages, page_size, table_ld,
                         path_ld, causal, max_rows, total_rows, max_len, Hq, Hkv, scale, decay};
-  // a cluster shares a tile's rows where the tiles alone leave SMs idle
-  const int64_t tiles = static_cast<int64_t>((max_len + kv4::kTile - 1) / kv4::kTile) * Hkv * B;
-  const int64_t chunks = (static_cast<int64_t>(max_rows) * (Hq / Hkv) + kv4::kMmaRows - 1) / kv4::kMmaRows;
-  int parts = 1;
-  while (parts < 8 && 2 * parts <= chunks && tiles * parts < 2ll * sm_count()) parts *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == TV_BF16 ? kv4::mass_mma(a, B, d, parts, st) : kv4::mass_simt(a, B, d, parts, st);
+  const int64_t rows = static_cast<int64_t>(max_rows) * (Hq / Hkv);
+  if (dtype == TV_BF16) return rows <= kv4::kFewRows ? kv4::mass_few(a, B, d, st) : kv4::mass_tc(a, B, d, st);
+  return kv4::mass_simt(a, B, d, st);
 }

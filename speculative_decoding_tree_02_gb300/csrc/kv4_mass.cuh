@@ -85,8 +85,11 @@ __device__ __forceinline__ float mass_before(const MassArgs& a, const MassSpan& 
   return a.decay * a.score_in[row * a.in_ld + t];
 }
 
-int mass_simt(const MassArgs& a, int B, int d, int parts, cudaStream_t st);   // fp32 rows
-int mass_mma(const MassArgs& a, int B, int d, int parts, cudaStream_t st);    // bf16 rows
+constexpr int kFewRows = 128;   // query rows per KV head up to which mass_few takes a call
+
+int mass_simt(const MassArgs& a, int B, int d, cudaStream_t st);   // fp32 rows
+int mass_few(const MassArgs& a, int B, int d, cudaStream_t st);    // bf16, few rows per KV head
+int mass_tc(const MassArgs& a, int B, int d, cudaStream_t st);     // bf16, any number
 
 }  // namespace kv4
 }  // namespace tv

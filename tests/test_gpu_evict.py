@@ -78,6 +78,10 @@ class Mass:
     ([64, 200], [7, 64], 14, 2, 64, 32, dict(causal=False, vis=True, score=False)),
     ([131, 90], [33, 21], 16, 1, 128, 128, dict(vis=True, decay=0.0, scale=0.31)),
     ([500], [200], 12, 3, 64, 64, dict()),
+    ([129], [129], 1, 1, 128, 16, dict()),
+    ([1100, 0, 513], [300, 0, 513], 8, 2, 128, 32, dict(decay=0.5)),
+    ([260, 40], [150, 40], 10, 2, 64, 16, dict(path=True, vis=True)),
+    ([700], [90], 128, 2, 64, 64, dict(causal=False)),
     ([90, 35], [20, 35], 6, 2, 128, 32, dict(path=True, vis=True)),
 ])
 def test_mass_matches(tv, lens, counts, Hq, Hkv, d, P, kw, bf16):

@@ -134,7 +134,7 @@ def call(lib, fn, base, **change):
     (-1, dict(in_ld=64, out_ld=128)), (-1, dict(cache_len=None)), (-1, dict(row_off=None)), (-1, dict(s_out=None)),
     (-1, dict(old=None)), (-1, dict(path=B_, path_ld=0)), (-1, dict(table=None)), (-1, dict(cache=None)), (-1, dict(q=None)),
     (-1, dict(lse=None)), (-1, dict(ldq=120)), (-1, dict(ldq=132)), (-1, dict(q=ODD)), (-1, dict(cache=ODD)),
-    (-2, dict(max_rows=1 << 30, Hq=64, Hkv=1, ldq=4096)), (-2, dict(table_ld=1 << 28)), (0, dict(B=0)), (0, dict(max_len=0))])
+    (-2, dict(max_rows=1 << 30, Hq=64, Hkv=1, ldq=4096)), (-2, dict(Hq=65, Hkv=1, ldq=65 * 64)), (-2, dict(table_ld=1 << 28)), (0, dict(B=0)), (0, dict(max_len=0))])
 def test_attn_mass_refusals(lib, want, change):
     assert call(lib, "kv4_attn_mass", MASS, **change) == want
 
