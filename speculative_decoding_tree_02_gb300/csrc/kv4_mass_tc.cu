@@ -8,10 +8,12 @@
 //
 // A CTA = 256 tokens (two MMA tiles that share every staged row) of one
 // (request, KV head):
-//   warps 0..7   consumers, a warpgroup per tile: exponentials and sums
-//   warps 8..11  producers: 64 rows at a time into shared memory (cp.async,
-//                K-major, 128-byte swizzle), their lse and visible lengths
-//   warp 12      issues the MMAs
+//   warps 0..15   consumers, a warpgroup per tile and half of the columns:
+//                 exponentials and sums
+//   warps 16..19  copy 64 rows at a time into shared memory (cp.async, K-major,
+//                 128-byte swizzle)
+//   warp 20       the rows' lse and visible lengths
+//   warp 21       issues the MMAs
 // S has three buffers per tile, so that the MMAs run ahead of the exponentials.
 //
 // Every wait is bounded (2 s); a role whose wait expires raises the CTA's abort
@@ -31,11 +33,11 @@ constexpr int kTok = 256;       // tokens of a CTA
 constexpr int kRowsC = 64;      // rows of a chunk
 constexpr int kSt = 6;          // staged chunks
 constexpr int kLag = 3;         // of these on their way
-constexpr int kPar = 10;        // chunks whose lse and visible lengths are held: more than kSt + kBuf
 constexpr int kBuf = 3;         // buffers of S per tile
-constexpr int kThreadsT = 416;
+constexpr int kPar = kBuf + 1;  // chunks whose lse and visible lengths are held
+constexpr int kConsumers = 16;  // warps
+constexpr int kThreadsT = 32 * (kConsumers + 6);
 constexpr float kInf = __builtin_huge_valf();
-static_assert(kPar > kSt + kBuf, "a chunk's parameters outlive its rows");
 
 template <int D>
 struct MassLay {
@@ -44,8 +46,8 @@ struct MassLay {
   static constexpr uint32_t kLse = kSt * kStage;              // float [kPar][64], negated
   static constexpr uint32_t kVis = kLse + kPar * 256;         // int [kPar][64]
   static constexpr uint32_t kSpan = kVis + kPar * 256;        // int2 [kPar][2] least and most visible of 32 rows
-  static constexpr uint32_t kPart = kSpan + kPar * 16;        // float [256]
-  static constexpr uint32_t kBars = kPart + 1024;             // full, empty [kSt], pfull [kPar], dfull, dempty [kBuf], done
+  static constexpr uint32_t kPart = kSpan + kPar * 16;        // float [2][256]
+  static constexpr uint32_t kBars = kPart + 2048;             // full, empty [kSt], pfull [kPar], dfull, dempty [kBuf], done
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kSt + kPar + 2 * kBuf + 1);
   // one CTA to an SM: it takes all of the tensor memory
   static constexpr uint32_t kBytes = kMisc + 64 + 1024 > 120 * 1024 ? kMisc + 64 + 1024 : 120 * 1024;
@@ -86,14 +88,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
   if (t0 >= sp.len) return;                       // (all CTAs of the cluster alike)
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) { mbar_init(full(s), 128); mbar_init(empty(s), 1); }
-    for (int s = 0; s < kPar; ++s) mbar_init(pfull(s), 128);
-    for (int s = 0; s < kBuf; ++s) { mbar_init(dfull(s), 1); mbar_init(dempty(s), 8); }
+    for (int s = 0; s < kPar; ++s) mbar_init(pfull(s), 1);
+    for (int s = 0; s < kBuf; ++s) { mbar_init(dfull(s), 1); mbar_init(dempty(s), kConsumers); }
     mbar_init(done, 1);
     s_abort = 0;
     s_status = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == kConsumers + 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm + L::kMisc)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -112,26 +114,27 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
   const int first = skip + static_cast<int>((rank + parts - skip % parts) % parts);
   const int chunks = first < all ? (all - first + static_cast<int>(parts) - 1) / static_cast<int>(parts) : 0;
 
-  const int t = t0 + (tid & 255);                 // consumers: the thread's token
+  // consumers: the thread's tile, columns and token
+  const int tile = (warp >> 2) & 1, half = (warp >> 3) & 1, t = t0 + (tid & 255);
   float fac = 0.f, sum = 0.f;
   bool ok = false;
-  if (warp < 8) {
-    // ---- the token's key -> operand
+  if (warp < kConsumers) {
+    // ---- half of the token's key -> operand
     const int page = t < sp.len ? mass_page(a, r, t) : -1;
     if (t < sp.len && page < 0 && a.err) *a.err = 1;
     ok = page >= 0;
     const int slot = t & (a.P - 1);
     const uint8_t* blk = a.cache + (static_cast<int64_t>(max(page, 0)) * a.Hkv + h) * block_bytes(a.P, D);
-    uint4 w[D / 32];
+    uint4 w[D / 64];
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+    for (int c = 0; c < D / 64; ++c) {
       w[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) w[c] = ldg_stream(blk + k_word(a.P, slot, 32 * c));
+      if (ok) w[c] = ldg_stream(blk + k_word(a.P, slot, 32 * (c + half * (D / 64))));
     }
     if (ok) fac = bf16_at(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot))) * (a.scale * kLog2e);
-    const uint32_t to = tmem + L::tK + (warp >> 2) * (D / 2) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t to = tmem + L::tK + tile * (D / 2) + half * (D / 4) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+    for (int c = 0; c < D / 64; ++c) {
       uint32_t v[16];
       decode8(w[c].x, v, magic);
       decode8(w[c].y, v + 4, magic);
@@ -144,12 +147,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
   }
   __syncthreads();
 
-  if (warp >= 8 && warp < 12) {
-    // ---- producers
-    const int p = tid - 256;
-    // i / g by a multiplication: exact for i < 2^31 and g <= 64
-    const uint64_t inv_g = ((1ull << 40) + g - 1) / g;
-    auto node_of = [&](int i) { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(i)) * inv_g >> 40); };
+  const uint64_t inv_g = ((1ull << 40) + g - 1) / g;
+  // i / g by a multiplication: exact for i < 2^31 and g <= 64
+  auto node_of = [&](int i) { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(i)) * inv_g >> 40); };
+  if (warp >= kConsumers && warp < kConsumers + 4) {
+    // ---- copies of the rows
+    const int p = tid - 32 * kConsumers;
     auto source = [&](int i) {                    // row i of the request's list: its place in q, -1: none
       if (i >= rows) return static_cast<int64_t>(-1);
       const int j = node_of(i);
@@ -168,26 +171,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
       const int i = first * kRowsC + mine, j = node_of(i);
       from += (static_cast<int64_t>(sp.base) + j) * a.ldq + static_cast<int64_t>(h * g + i - j * g) * D;
     }
-    // lse and visible length of this thread's row of chunk c
-    auto params = [&](int c, float& l, int& vis) {
-      const int i = (first + c * static_cast<int>(parts)) * kRowsC + p;
-      l = kInf;
-      vis = 0;
-      if (p >= kRowsC || c >= chunks || i >= rows) return;
-      const int j = node_of(i);
-      const MassRow m = mass_row(a, sp, r, j);
-      if (m.bad && a.err) *a.err = 1;
-      if (m.bad) return;
-      l = a.lse[m.src * a.Hq + h * g + i - j * g];
-      vis = m.vis;
-    };
-    float l0, l1, l2;                             // of the chunks c, c + 1, c + 2: loads take longer than a chunk
-    int n0, n1, n2;
-    params(0, l0, n0);
-    params(1, l1, n1);
     for (int c = 0; c < chunks + kLag; ++c) {
       if (c < chunks) {
-        params(c + 2, l2, n2);
         const int s = c % kSt;
         if (c >= kSt && !warp_wait(empty(s), (c / kSt - 1) & 1, abort_flag, &s_status, 1)) break;
         const int i0 = (first + c * static_cast<int>(parts)) * kRowsC;
@@ -201,19 +186,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
                        : "memory");
         }
         if (even) from += static_cast<int64_t>(parts) * (kRowsC / kStep) * stride;
-        if (p < kRowsC) {
-          const int q = c % kPar;
-          if (l0 == -kInf) n0 = 0;                // (a row that saw nothing weighs nothing)
-          reinterpret_cast<float*>(sm + L::kLse)[q * kRowsC + p] = l0 == -kInf ? -kInf : -(l0 * kLog2e);
-          reinterpret_cast<int*>(sm + L::kVis)[q * kRowsC + p] = n0;
-          const int lo = __reduce_min_sync(0xffffffffu, n0), hi = __reduce_max_sync(0xffffffffu, n0);
-          if (lane == 0) reinterpret_cast<int2*>(sm + L::kSpan)[2 * q + (p >> 5)] = make_int2(lo, hi);
-        }
-        mbar_arrive(pfull(c % kPar));
-        l0 = l1;
-        n0 = n1;
-        l1 = l2;
-        n1 = n2;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (c >= kLag) {                            // the chunk kLag before has arrived
@@ -223,7 +195,52 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp == 12) {
+  } else if (warp == kConsumers + 4) {
+    // ---- lse and visible lengths: lane = rows lane and lane + 32 of a chunk
+    struct Two {
+      float l[2];
+      int vis[2];
+    };
+    auto params = [&](int c) {
+      Two x;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = (first + c * static_cast<int>(parts)) * kRowsC + 32 * u + lane;
+        x.l[u] = kInf;
+        x.vis[u] = 0;
+        if (c >= chunks || i >= rows) continue;
+        const int j = node_of(i);
+        const MassRow m = mass_row(a, sp, r, j);
+        if (m.bad && a.err) *a.err = 1;
+        if (m.bad) continue;
+        x.l[u] = a.lse[m.src * a.Hq + h * g + i - j * g];
+        x.vis[u] = m.vis;
+      }
+      return x;
+    };
+    Two now = params(0), next = params(1);        // loads take longer than a chunk
+    for (int c = 0; c < chunks; ++c) {
+      const Two later = params(c + 2);
+      // Consumers that have loaded S of chunk c - kBuf are through with the chunk before it, whose place this is.
+      // (A barrier may be waited for only by those without whom its next phase cannot end: a parity tells two phases
+      // apart. Here that is chunk c's, for which the consumers wait for this warp.)
+      if (c >= kBuf && !warp_wait(dempty(c % kBuf), (c / kBuf - 1) & 1, abort_flag, &s_status, 6)) break;
+      const int q = c % kPar;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool none = now.l[u] == -kInf;      // (a row that saw nothing weighs nothing)
+        if (none) now.vis[u] = 0;
+        reinterpret_cast<float*>(sm + L::kLse)[q * kRowsC + 32 * u + lane] = none ? -kInf : -(now.l[u] * kLog2e);
+        reinterpret_cast<int*>(sm + L::kVis)[q * kRowsC + 32 * u + lane] = now.vis[u];
+        const int lo = __reduce_min_sync(0xffffffffu, now.vis[u]), hi = __reduce_max_sync(0xffffffffu, now.vis[u]);
+        if (lane == 0) reinterpret_cast<int2*>(sm + L::kSpan)[2 * q + u] = make_int2(lo, hi);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull(q));
+      now = next;
+      next = later;
+    }
+  } else if (warp == kConsumers + 5) {
     // ---- MMAs
     tc_fence_after();
     constexpr uint32_t id = idesc_bf16(128, kRowsC, 0);
@@ -251,83 +268,80 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
     if (!drain(done, 0)) *abort_flag = 1;
   } else {
     // ---- consumers
-    const uint32_t from = tmem + (warp >> 2) * (kBuf * kRowsC) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const int tile0 = t0 + 128 * (warp >> 2);
+    const uint32_t from = tmem + tile * (kBuf * kRowsC) + 32 * half + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int tile0 = t0 + 128 * tile;
     const uint64_t fac2 = pair(fac, fac);
     for (int c = 0; c < chunks; ++c) {
       const int b = c % kBuf, q = c % kPar;
       if (!warp_wait(pfull(q), (c / kPar) & 1, abort_flag, &s_status, 4)) break;
-      const int2 v0 = reinterpret_cast<const int2*>(sm + L::kSpan)[2 * q], v1 = reinterpret_cast<const int2*>(sm + L::kSpan)[2 * q + 1];
+      const int2 v = reinterpret_cast<const int2*>(sm + L::kSpan)[2 * q + half];
       if (!warp_wait(dfull(b), (c / kBuf) & 1, abort_flag, &s_status, 5)) break;
       tc_fence_after();
-      uint32_t x[2][32];
-      tmem_ld32(from + b * kRowsC, x[0]);
-      tmem_ld32(from + b * kRowsC + 32, x[1]);
+      uint32_t x[32];
+      tmem_ld32(from + b * kRowsC, x);
       tmem_ld_wait();
       tc_fence_before();
       if (lane == 0) mbar_arrive(dempty(b));
-      const float* nl = reinterpret_cast<const float*>(sm + L::kLse) + q * kRowsC;
-      const int* vis = reinterpret_cast<const int*>(sm + L::kVis) + q * kRowsC;
+      if (v.y <= tile0) continue;                 // none of these rows sees the tile
+      const float* nl = reinterpret_cast<const float*>(sm + L::kLse) + q * kRowsC + 32 * half;
+      const int* vis = reinterpret_cast<const int*>(sm + L::kVis) + q * kRowsC + 32 * half;
+      uint64_t s2[2] = {0ull, 0ull};
+      if (v.x >= tile0 + 128) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int2 v = half ? v1 : v0;
-        if (v.y <= tile0) continue;               // none of these rows sees the tile
-        uint64_t s2[2] = {0ull, 0ull};
-        if (v.x >= tile0 + 128) {
+        for (int i = 0; i < 32; i += 4) {
+          const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + i);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + 32 * half + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pin(x[half][i + j]);
-            const uint64_t y0 = fma2(pair(__uint_as_float(x[half][i]), __uint_as_float(x[half][i + 1])), fac2, l.x);
-            const uint64_t y1 = fma2(pair(__uint_as_float(x[half][i + 2]), __uint_as_float(x[half][i + 3])), fac2, l.y);
-            float lo, hi;
-            split(y0, lo, hi);
-            s2[0] = add2(s2[0], pair(ex2(lo), ex2(hi)));
-            split(y1, lo, hi);
-            s2[1] = add2(s2[1], pair(ex2(lo), ex2(hi)));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + 32 * half + i);
-            const int4 see = *reinterpret_cast<const int4*>(vis + 32 * half + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pin(x[half][i + j]);
-            const uint64_t y0 = fma2(pair(__uint_as_float(x[half][i]), __uint_as_float(x[half][i + 1])), fac2, l.x);
-            const uint64_t y1 = fma2(pair(__uint_as_float(x[half][i + 2]), __uint_as_float(x[half][i + 3])), fac2, l.y);
-            float lo, hi;
-            split(y0, lo, hi);
-            s2[0] = add2(s2[0], pair(t < see.x ? ex2(lo) : 0.f, t < see.y ? ex2(hi) : 0.f));
-            split(y1, lo, hi);
-            s2[1] = add2(s2[1], pair(t < see.z ? ex2(lo) : 0.f, t < see.w ? ex2(hi) : 0.f));
-          }
+          for (int j = 0; j < 4; ++j) pin(x[i + j]);
+          const uint64_t y0 = fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, l.x);
+          const uint64_t y1 = fma2(pair(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), fac2, l.y);
+          float lo, hi;
+          split(y0, lo, hi);
+          s2[0] = add2(s2[0], pair(ex2(lo), ex2(hi)));
+          split(y1, lo, hi);
+          s2[1] = add2(s2[1], pair(ex2(lo), ex2(hi)));
         }
-        float lo, hi;
-        split(add2(s2[0], s2[1]), lo, hi);
-        sum += lo + hi;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + i);
+          const int4 see = *reinterpret_cast<const int4*>(vis + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pin(x[i + j]);
+          const uint64_t y0 = fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, l.x);
+          const uint64_t y1 = fma2(pair(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), fac2, l.y);
+          float lo, hi;
+          split(y0, lo, hi);
+          s2[0] = add2(s2[0], pair(t < see.x ? ex2(lo) : 0.f, t < see.y ? ex2(hi) : 0.f));
+          split(y1, lo, hi);
+          s2[1] = add2(s2[1], pair(t < see.z ? ex2(lo) : 0.f, t < see.w ? ex2(hi) : 0.f));
+        }
       }
+      float lo, hi;
+      split(add2(s2[0], s2[1]), lo, hi);
+      sum += lo + hi;
     }
+    part[tid] = ok ? sum : 0.f;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kConsumers + 5) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(misc[0]), "r"(512) : "memory");
   }
-  // ---- the parts' sums, in the order of their ranks (a part that gave up: NaN)
-  float mine = s_abort ? __uint_as_float(0x7fc00000u) : ok ? sum : 0.f;
-  if (s_abort && tid == 0 && a.err) *a.err = 1;
-  if (parts > 1) {
-    if (warp < 8) part[tid] = mine;
-    cl::sync();
-    if (rank == 0 && warp < 8) {
-      mine = 0.f;
-      for (uint32_t c = 0; c < parts; ++c) mine += cl::peek(&part[tid], c);
-    }
-    cl::sync();
+  // ---- sums of the halves and parts, in order (of a CTA that gave up: NaN)
+  if (s_abort) {
+    if (warp < kConsumers) part[tid] = __uint_as_float(0x7fc00000u);
+    if (tid == 0 && a.err) *a.err = 1;
   }
-  if (rank == 0 && warp < 8 && t < sp.len) a.score_out[row * a.out_ld + t] = mass_before(a, sp, row, t) + mine;
+  if (parts > 1) cl::sync();
+  else __syncthreads();
+  if (rank == 0 && warp < 8) {
+    float m = 0.f;
+    for (uint32_t c = 0; c < parts; ++c)
+      m += parts > 1 ? cl::peek(&part[tid], c) + cl::peek(&part[tid + 256], c) : part[tid] + part[tid + 256];
+    if (t < sp.len) a.score_out[row * a.out_ld + t] = mass_before(a, sp, row, t) + m;
+  }
+  if (parts > 1) cl::sync();                      // no CTA leaves while another may read its shared memory
 }
 
 template <int D>

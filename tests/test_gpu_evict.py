@@ -82,6 +82,7 @@ class Mass:
     ([1100, 0, 513], [300, 0, 513], 8, 2, 128, 32, dict(decay=0.5)),
     ([260, 40], [150, 40], 10, 2, 64, 16, dict(path=True, vis=True)),
     ([700], [90], 128, 2, 64, 64, dict(causal=False)),
+    ([610], [600], 16, 1, 64, 32, dict()),
     ([90, 35], [20, 35], 6, 2, 128, 32, dict(path=True, vis=True)),
 ])
 def test_mass_matches(tv, lens, counts, Hq, Hkv, d, P, kw, bf16):
