@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
   extern __shared__ __align__(16) uint8_t qs[];
   __shared__ __align__(8) float s_lse[kFewRows];
   __shared__ __align__(8) int s_vis[kFewRows];
+  __shared__ int64_t s_at[kFewRows];              // places in q, -1: none
+  __shared__ int2 s_span[kFewRows / 8];           // least and most that a block's rows see
   __shared__ int s_first;
   griddep_wait();
   griddep_release();
@@ -181,63 +183,86 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
       if (t0 + 16 * i < t_hi) page[i] = __ldg(table + ((t0 + 16 * i) >> ps));
     }
   };
+  // (a page holds codes in every place, so tokens past the end may be read; their sums go nowhere)
+  const int lane_key = k_word(a.P, lane >> 2, (lane & 3) * (D / 4)), lane_sc = k_scale(a.P, D, lane >> 2);
+  const uint8_t* heads = a.cache + static_cast<int64_t>(h) * block_bytes(a.P, D);
+  const int64_t page_bytes = a.Hkv * block_bytes(a.P, D);
+  const bool had = a.score_in && a.decay != 0.f;
+  const float* before = a.score_in + row * a.in_ld;
   auto fetch = [&](int t0, Tile& x) {
     if (t0 >= t_hi) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int page = x.page[i >> 1], t = t0 + (lane >> 2) + 8 * i, slot = t & (a.P - 1);
+    for (int m = 0; m < 2; ++m) {
 #pragma unroll
-      for (int w = 0; w < kRun; ++w) x.w[i][w] = 0;
-      x.sc[i] = 0;
-      if (page >= 0 && page < a.n_pages && t < t_hi) {
-        const uint8_t* blk = a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
-        const uint8_t* at = blk + k_word(a.P, slot, (lane & 3) * (D / 4));
+      for (int i = 2 * m; i < 2 * m + 2; ++i) {
+        x.sc[i] = 0;
+#pragma unroll
+        for (int w = 0; w < kRun; ++w) x.w[i][w] = 0;
+      }
+      if (static_cast<unsigned>(x.page[m]) >= static_cast<unsigned>(a.n_pages)) continue;
+      const int slot = (t0 + 16 * m) & (a.P - 1);
+      const uint8_t* blk = heads + x.page[m] * page_bytes;
+      const uint8_t* at = blk + lane_key + 16 * slot;
+      const uint8_t* sc = blk + lane_sc + 2 * slot;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         if constexpr (D == 128) {
-          const uint4 v = ldg_stream(at);
-          x.w[i][0] = v.x; x.w[i][1] = v.y; x.w[i][2] = v.z; x.w[i][3] = v.w;
+          const uint4 v = ldg_stream(at + 128 * i);
+          x.w[2 * m + i][0] = v.x; x.w[2 * m + i][1] = v.y; x.w[2 * m + i][2] = v.z; x.w[2 * m + i][3] = v.w;
         } else {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-          x.w[i][0] = v.x; x.w[i][1] = v.y;
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + 128 * i));
+          x.w[2 * m + i][0] = v.x; x.w[2 * m + i][1] = v.y;
         }
-        x.sc[i] = __ldg(reinterpret_cast<const uint16_t*>(blk + k_scale(a.P, D, slot)));
+        x.sc[2 * m + i] = __ldg(reinterpret_cast<const uint16_t*>(sc + 16 * i));
       }
     }
     const int t = t0 + (lane >> 2) + 8 * (lane & 3);
-    x.had = t < t_hi ? mass_before(a, sp, row, t) : 0.f;
+    x.had = had && t < min(t_hi, sp.old) ? before[t] : 0.f;
   };
   Tile next;
   int t0 = t_lo + 32 * warp;
   pages(t0, next.page);
 
-  // the rows, in fragment order
-  for (int u = tid; u < 8 * blocks * (D / 8); u += kTile) {
-    const int i = u / (D / 8), x = u % (D / 8);
-    const uint16_t* src = static_cast<const uint16_t*>(a.q);
-    bool some = i < rows;
-    if (some) {
-      const MassRow m = mass_row(a, sp, r, i / g);
-      some = !m.bad;
-      if (some) src += m.src * a.ldq + static_cast<int64_t>(h * g + i % g) * D + 8 * x;
-    }
-    cp16(tc::smem_u32(qs + (i / 8) * kBlock + (x % kRun) * 512 + ((i % 8) * 4 + x / kRun) * 16), src, some);
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  for (int i = tid; i < 8 * blocks; i += kTile) {
+  // where the rows lie, their lse and what they see; then the rows, in fragment order
+  if (tid < 8 * blocks) {
     int vis = 0;
     float l = kInf;
-    if (i < rows) {
-      const MassRow m = mass_row(a, sp, r, i / g);
+    int64_t at = -1;
+    if (tid < rows) {
+      const int j = tid / g;
+      const MassRow m = mass_row(a, sp, r, j);
       if (m.bad && a.err) *a.err = 1;
       if (!m.bad) {
-        l = a.lse[m.src * a.Hq + h * g + i % g];
+        at = m.src * a.ldq + static_cast<int64_t>(h * g + tid - j * g) * D;
+        l = a.lse[m.src * a.Hq + h * g + tid - j * g];
         vis = l == -kInf ? 0 : m.vis;             // (a row that saw nothing weighs nothing)
       }
     }
-    s_vis[i] = vis;
-    s_lse[i] = l == -kInf ? kInf : l * kLog2e;
+    s_at[tid] = at;
+    s_vis[tid] = vis;
+    s_lse[tid] = l == -kInf ? kInf : l * kLog2e;
   }
+  __syncthreads();
+  {
+    // a thread copies the same 16 bytes of every 8 (16) rows
+    constexpr int kStep = kTile / (D / 8);
+    const int i0 = tid / (D / 8), x = tid % (D / 8);
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + 8 * x;
+    const uint32_t dst = tc::smem_u32(qs + (i0 / 8) * kBlock + (x % kRun) * 512 + ((i0 % 8) * 4 + x / kRun) * 16);
+    for (int i = i0; i < 8 * blocks; i += kStep) {
+      const int64_t at = s_at[i];
+      cp16(dst + (i - i0) / 8 * kBlock, q + max(at, static_cast<int64_t>(0)), at >= 0);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   fetch(t0, next);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  if (tid < blocks) {
+    int2 v = make_int2(0x7fffffff, 0);
+    for (int i = 8 * tid; i < 8 * tid + 8; ++i) v = make_int2(min(v.x, s_vis[i]), max(v.y, s_vis[i]));
+    s_span[tid] = v;
+  }
   __syncthreads();
 
   const float scale2 = a.scale * kLog2e;
@@ -266,10 +291,8 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
     fetch(t0 + kTile, next);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int n = 0; n < blocks; ++n) {
-      const int2 vis = *reinterpret_cast<const int2*>(&s_vis[8 * n + 2 * (lane & 3)]);
-      const int vmin = min(vis.x, vis.y), vmax = max(vis.x, vis.y);
-      if (!__any_sync(0xffffffffu, vmax > t0)) continue;
-      const bool whole = __all_sync(0xffffffffu, vmin >= t0 + 32);
+      const int2 span = s_span[n];
+      if (span.y <= t0) continue;
       float acc[2][4] = {};
 #pragma unroll
       for (int w = 0; w < kRun; ++w) {
@@ -281,15 +304,17 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
         }
       }
       const float2 l = *reinterpret_cast<const float2*>(&s_lse[8 * n + 2 * (lane & 3)]);
+      if (span.x >= t0 + 32) {                    // all of them see the whole tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = ex2(fmaf(acc[i >> 1][2 * (i & 1)], fac[i], -l.x));
-        const float y = ex2(fmaf(acc[i >> 1][2 * (i & 1) + 1], fac[i], -l.y));
-        if (whole) {
-          sum[i] += x + y;
-        } else {
+        for (int i = 0; i < 4; ++i)
+          sum[i] += ex2(fmaf(acc[i >> 1][2 * (i & 1)], fac[i], -l.x)) + ex2(fmaf(acc[i >> 1][2 * (i & 1) + 1], fac[i], -l.y));
+      } else {
+        const int2 vis = *reinterpret_cast<const int2*>(&s_vis[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const int t = t0 + (lane >> 2) + 8 * i;
-          sum[i] += (t < vis.x ? x : 0.f) + (t < vis.y ? y : 0.f);
+          if (t < vis.x) sum[i] += ex2(fmaf(acc[i >> 1][2 * (i & 1)], fac[i], -l.x));
+          if (t < vis.y) sum[i] += ex2(fmaf(acc[i >> 1][2 * (i & 1) + 1], fac[i], -l.y));
         }
       }
     }
@@ -305,7 +330,7 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
       const int page = i < 2 ? cur.page[0] : cur.page[1];
       const bool ok = page >= 0 && page < a.n_pages;
       if (!ok && a.err) *a.err = 1;
-      a.score_out[row * a.out_ld + t] = cur.had + (ok ? mine : 0.f);
+      a.score_out[row * a.out_ld + t] = (had ? a.decay * cur.had : 0.f) + (ok ? mine : 0.f);
     }
   }
 }

@@ -47,8 +47,8 @@ struct MassLay {
   static constexpr uint32_t kVis = kLse + kPar * 256;         // int [kPar][64]
   static constexpr uint32_t kSpan = kVis + kPar * 256;        // int2 [kPar][2] least and most visible of 32 rows
   static constexpr uint32_t kPart = kSpan + kPar * 16;        // float [2][256]
-  static constexpr uint32_t kBars = kPart + 2048;             // full, empty [kSt], pfull [kPar], dfull, dempty [kBuf], done
-  static constexpr uint32_t kMisc = kBars + 8 * (2 * kSt + kPar + 2 * kBuf + 1);
+  static constexpr uint32_t kBars = kPart + 2048;             // full, empty [kSt], pfull [kPar], dfull, dempty [kBuf], done, K
+  static constexpr uint32_t kMisc = kBars + 8 * (2 * kSt + kPar + 2 * kBuf + 2);
   // one CTA to an SM: it takes all of the tensor memory
   static constexpr uint32_t kBytes = kMisc + 64 + 1024 > 120 * 1024 ? kMisc + 64 + 1024 : 120 * 1024;
   static constexpr uint32_t tK = 2 * kBuf * kRowsC;           // tensor memory: S [2 tiles][kBuf][64], then K [2 tiles][D / 2]
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
   auto pfull = [&](int s) { return sb + L::kBars + 8u * (2 * kSt + s); };
   auto dfull = [&](int s) { return sb + L::kBars + 8u * (2 * kSt + kPar + s); };
   auto dempty = [&](int s) { return sb + L::kBars + 8u * (2 * kSt + kPar + kBuf + s); };
-  const uint32_t done = sb + L::kBars + 8u * (2 * kSt + kPar + 2 * kBuf);
+  const uint32_t done = sb + L::kBars + 8u * (2 * kSt + kPar + 2 * kBuf), kready = done + 8;
   float* part = reinterpret_cast<float*>(sm + L::kPart);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + L::kMisc);
   volatile int* abort_flag = &s_abort;
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
     for (int s = 0; s < kPar; ++s) mbar_init(pfull(s), 1);
     for (int s = 0; s < kBuf; ++s) { mbar_init(dfull(s), 1); mbar_init(dempty(s), kConsumers); }
     mbar_init(done, 1);
+    mbar_init(kready, kConsumers);
     s_abort = 0;
     s_status = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -144,8 +145,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
     }
     tmem_st_wait();
     tc_fence_before();
+    if (lane == 0) mbar_arrive(kready);
   }
-  __syncthreads();
 
   const uint64_t inv_g = ((1ull << 40) + g - 1) / g;
   // i / g by a multiplication: exact for i < 2^31 and g <= 64
@@ -242,9 +243,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
     }
   } else if (warp == kConsumers + 5) {
     // ---- MMAs
-    tc_fence_after();
     constexpr uint32_t id = idesc_bf16(128, kRowsC, 0);
-    for (int c = 0; c < chunks; ++c) {
+    const bool keys = warp_wait(kready, 0, abort_flag, &s_status, 7);
+    for (int c = 0; c < chunks && keys; ++c) {
       const int s = c % kSt, b = c % kBuf;
       if (c >= kBuf && !warp_wait(dempty(b), (c / kBuf - 1) & 1, abort_flag, &s_status, 2)) break;
       if (!warp_wait(full(s), (c / kSt) & 1, abort_flag, &s_status, 3)) break;
