@@ -198,24 +198,36 @@ struct CompactArgs {
 
 constexpr int kWin = 64;        // tokens that D threads move at a time
 
+// What a window's threads share: where its tokens come from and its groups go.
+struct Window {
+  int4 v[kWin];                 // address of the token's value word at dim 0, rotation that brings its nibble to bit 0
+  int64_t block[kWin];          // byte offset of its source block, -1: does not move
+  int slot[kWin];
+  int64_t to[kWin / 16];        // byte offset of the destination block of 16 tokens, -1: none
+  uint32_t live[kWin / 32];     // tokens that move
+};
+
 // D threads move a window of 64 kept tokens of one (request, KV head): keys
 // and scales token by token in 16-byte units, values dim by dim (thread = dim):
 // the 16 nibbles of a destination word are picked from the words of their
-// source groups.  A group of the destination belongs to one window, so words
-// are written whole; nibbles of tokens that do not move are kept.
+// source groups, each rotated into place.  A group of the destination belongs
+// to one window, so words are written whole; nibbles of tokens that do not move
+// are kept.
 //   kInPlace: the windows of a (request, KV head) are taken in order by one
 //   cluster, blockDim.y windows to a CTA at a time.  Kept tokens only move
 //   towards the front, so what one round writes lies before all that later
 //   rounds read; one cluster barrier between a round's reads and its writes
 //   makes that hold inside the round too.
 //   else: every window is a CTA of its own.
+// Bound by HBM sectors: a kept token's 16-byte units and a group's words are
+// fetched with their neighbours, which may not be kept.
 template <int D, bool kInPlace>
 __global__ void __launch_bounds__(kInPlace ? 4 * D : D) compact_kernel(const CompactArgs a) {
-  __shared__ int64_t s_block[4][kWin];    // byte offset of a token's source block, -1: does not move
-  __shared__ int s_slot[4][kWin];
+  __shared__ Window win[kInPlace ? 4 : 1];
   griddep_wait();
   griddep_release();
   const int dim = threadIdx.x, y = threadIdx.y;
+  Window& sh = win[kInPlace ? y : 0];
   const int r = blockIdx.z, h = blockIdx.y;
   const int len = a.cache_len[r];
   int n = a.new_len[r];
@@ -224,6 +236,7 @@ __global__ void __launch_bounds__(kInPlace ? 4 * D : D) compact_kernel(const Com
   const int32_t* dtable = kInPlace ? table : a.dst_table + static_cast<int64_t>(r) * a.dst_ld;
   const int dld = kInPlace ? a.table_ld : a.dst_ld;
   const int32_t* idx = a.idx + (static_cast<int64_t>(r) * a.Hkv + h) * a.idx_ld;
+  const int ps = 31 - __clz(a.P);
   if (n > a.max_keep || n < 0) {
     if (blockIdx.x == 0 && h == 0 && dim == 0 && y == 0 && a.err) *a.err = 1;
     n = max(0, min(n, a.max_keep));
@@ -234,110 +247,114 @@ __global__ void __launch_bounds__(kInPlace ? 4 * D : D) compact_kernel(const Com
     if ((kInPlace ? w - static_cast<int>(blockIdx.x * blockDim.y) : w) * kWin >= n) return;
     const int j0 = (w + y) * kWin;
     bool bad = false;
-    for (int i = dim; i < kWin; i += D) {
-      const int j = j0 + i;
+    if (dim < kWin) {
+      const int j = j0 + dim;
       int64_t blk = -1;
       int slot = 0;
       if (j < n) {
         const int t = idx[j];
         bad = true;
         if (t >= 0 && t < len && t < cap) {
-          const int page = table[t / a.P];
+          const int page = table[t >> ps];
           if (page >= 0 && page < a.n_pages) {
             bad = false;
-            slot = t % a.P;
+            slot = t & (a.P - 1);
             if (!kInPlace || t != j) blk = (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
           }
         }
       }
-      s_block[y][i] = blk;
-      s_slot[y][i] = slot;
+      int64_t to = -1;
+      if (dim % 16 == 0 && j < n) {
+        const int page = (j >> ps) < dld ? dtable[j >> ps] : -1;
+        if (page >= 0 && page < a.n_pages) to = (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
+        else bad = true;
+        sh.to[dim / 16] = to;
+      }
+      to = __shfl_sync(0xffffffffu, to, dim & 16);
+      if (to < 0) blk = -1;                     // nowhere to go
+      sh.block[dim] = blk;
+      sh.slot[dim] = slot;
+      const uint64_t at = reinterpret_cast<uint64_t>(a.cache) +
+                          (blk >= 0 ? blk + v_group(a.P, D, slot >> 4, 0) + ((slot >> 3) & 1) * 4 : 0);
+      sh.v[dim] = make_int4(static_cast<int>(at), static_cast<int>(at >> 32), 32 - 4 * nibble_of(slot & 7), 0);
+      const unsigned live = __ballot_sync(0xffffffffu, blk >= 0);
+      if ((dim & 31) == 0) sh.live[dim >> 5] = live;
     }
     __syncthreads();
     // reads
     uint4 kc[kUnits];
-    uint2 vw[kWin / 16], vmask[kWin / 16];
+    uint2 vw[kWin / 16];
     uint16_t sc[2 * kWin / D];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int unit = u * D + dim, i = unit % kWin, c = unit / kWin;
-      const int64_t blk = s_block[y][i];
-      if (blk >= 0) kc[u] = *reinterpret_cast<const uint4*>(a.cache + blk + k_word(a.P, s_slot[y][i], 32 * c));
+      const int64_t blk = sh.block[i];
+      if (blk >= 0) kc[u] = *reinterpret_cast<const uint4*>(a.cache + blk + k_word(a.P, sh.slot[i], 32 * c));
     }
 #pragma unroll
     for (int u = 0; u < 2 * kWin / D; ++u) {
       const int unit = u * D + dim, i = unit % kWin;
-      const int64_t blk = s_block[y][i];
+      const int64_t blk = sh.block[i];
       if (blk >= 0)
         sc[u] = *reinterpret_cast<const uint16_t*>(
-            a.cache + blk + (unit < kWin ? k_scale(a.P, D, s_slot[y][i]) : v_scale(a.P, D, s_slot[y][i])));
+            a.cache + blk + (unit < kWin ? k_scale(a.P, D, sh.slot[i]) : v_scale(a.P, D, sh.slot[i])));
     }
 #pragma unroll
     for (int q = 0; q < kWin / 16; ++q) {
+      vw[q] = make_uint2(0u, 0u);
+      if (((sh.live[q >> 1] >> (16 * (q & 1))) & 0xffffu) == 0u) continue;
       uint32_t word[16];
+      int turn[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t blk = s_block[y][16 * q + e];
-        const int s = s_slot[y][16 * q + e];
-        word[e] = 0;
-        if (blk >= 0)
-          word[e] = *reinterpret_cast<const uint32_t*>(a.cache + blk + v_group(a.P, D, s >> 4, dim) + ((s >> 3) & 1) * 4);
+      for (int e = 0; e < 16; ++e) {            // (tokens that do not move: some word, masked when it is stored)
+        const int4 t = sh.v[16 * q + e];
+        const uint64_t at = static_cast<uint32_t>(t.x) | static_cast<uint64_t>(static_cast<uint32_t>(t.y)) << 32;
+        word[e] = *reinterpret_cast<const uint32_t*>(at + 8u * dim);
+        turn[e] = t.z;
       }
-      uint32_t v[2] = {0u, 0u}, m[2] = {0u, 0u};
+      uint32_t v[2] = {0u, 0u};
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int64_t blk = s_block[y][16 * q + e];
-        const int s = s_slot[y][16 * q + e] & 7;
         const int to = 4 * nibble_of(e & 7);
-        v[e >> 3] |= ((word[e] >> (4 * nibble_of(s))) & 15u) << to;
-        if (blk >= 0) m[e >> 3] |= 15u << to;
+        v[e >> 3] |= __funnelshift_l(word[e], word[e], turn[e] + to) & (15u << to);
       }
       vw[q] = make_uint2(v[0], v[1]);
-      vmask[q] = make_uint2(m[0], m[1]);
     }
     if constexpr (kInPlace) cl::sync();
     // writes
-    auto target = [&](int j) -> uint8_t* {
-      const int pg = j / a.P;
-      const int page = pg < dld ? dtable[pg] : -1;
-      if (page < 0 || page >= a.n_pages) {
-        bad = true;
-        return nullptr;
-      }
-      return a.cache + (static_cast<int64_t>(page) * a.Hkv + h) * block_bytes(a.P, D);
-    };
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int unit = u * D + dim, i = unit % kWin, c = unit / kWin;
-      if (s_block[y][i] < 0) continue;
-      if (uint8_t* blk = target(j0 + i)) *reinterpret_cast<uint4*>(blk + k_word(a.P, (j0 + i) % a.P, 32 * c)) = kc[u];
+      if (sh.block[i] < 0) continue;
+      *reinterpret_cast<uint4*>(a.cache + sh.to[i >> 4] + k_word(a.P, (j0 + i) & (a.P - 1), 32 * c)) = kc[u];
     }
 #pragma unroll
     for (int u = 0; u < 2 * kWin / D; ++u) {
-      const int unit = u * D + dim, i = unit % kWin;
-      if (s_block[y][i] < 0) continue;
-      if (uint8_t* blk = target(j0 + i))
-        *reinterpret_cast<uint16_t*>(blk + (unit < kWin ? k_scale(a.P, D, (j0 + i) % a.P)
-                                                        : v_scale(a.P, D, (j0 + i) % a.P))) = sc[u];
+      const int unit = u * D + dim, i = unit % kWin, slot = (j0 + i) & (a.P - 1);
+      if (sh.block[i] < 0) continue;
+      *reinterpret_cast<uint16_t*>(a.cache + sh.to[i >> 4] + (unit < kWin ? k_scale(a.P, D, slot) : v_scale(a.P, D, slot))) =
+          sc[u];
     }
 #pragma unroll
     for (int q = 0; q < kWin / 16; ++q) {
-      if ((vmask[q].x | vmask[q].y) == 0u) continue;
-      const int j = j0 + 16 * q;
-      if (uint8_t* blk = target(j)) {
-        uint2* dst = reinterpret_cast<uint2*>(blk + v_group(a.P, D, j % a.P / 16, dim));
-        uint2 v = vw[q];
-        if ((vmask[q].x & vmask[q].y) != 0xffffffffu) {
-          const uint2 old = *dst;
-          v.x |= old.x & ~vmask[q].x;
-          v.y |= old.y & ~vmask[q].y;
-        }
-        *dst = v;
+      const uint32_t live = (sh.live[q >> 1] >> (16 * (q & 1))) & 0xffffu;
+      if (live == 0u) continue;
+      uint2* dst = reinterpret_cast<uint2*>(a.cache + sh.to[q] + v_group(a.P, D, ((j0 + 16 * q) & (a.P - 1)) >> 4, dim));
+      uint2 v = vw[q];
+      if (live != 0xffffu) {
+        uint32_t m[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (live >> e & 1u) m[e >> 3] |= 15u << (4 * nibble_of(e & 7));
+        const uint2 old = *dst;
+        v.x = (v.x & m[0]) | (old.x & ~m[0]);
+        v.y = (v.y & m[1]) | (old.y & ~m[1]);
       }
+      *dst = v;
     }
     if (bad && a.err) *a.err = 1;
     if constexpr (!kInPlace) return;
-    __syncthreads();                                   // (the next round rewrites s_block)
+    __syncthreads();                                   // (the next round rewrites the window)
   }
 }
 
