@@ -30,23 +30,28 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return x == x ? b ^ (b >> 31 ? 0xffffffffu : 0x80000000u) : 0u;
 }
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 256;
+constexpr int kBins = 2048;
+constexpr int kPick = 512;             // candidates that are compared directly
 
 // A cluster of up to 8 CTAs = one (request, KV head); each CTA stages a slice
 // of the row of scores in shared memory, so that the row is read once and
-// score_out may be the same array.  The threshold is found by four passes over
-// eight bits of the key each (counts per digit, added over the cluster), then
-// kept tokens get their places from counts in index order, ties included.
-// Latency bound: 64 x 8 rows of 512..4096 scores and one row set of 131072.
+// score_out may be the same array.  The threshold is found by counting digits
+// of the keys, 11, 11 and 10 bits (added over the cluster), until the digit that
+// it lies in has at most 512 tokens, which are listed and compared with one
+// another: one count for a few thousand scores.  Then kept tokens get their
+// places from counts in index order, ties included.  Latency bound.
+// 512 threads, 1024 in a cluster of 8.
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const uint32_t csize) {
-  extern __shared__ float xs[];
+  constexpr int kSelWarps = kSelThreads / 32;
+  extern __shared__ __align__(16) float xs[];
   __shared__ uint32_t hist[2][kBins];
-  __shared__ uint32_t tot[kBins];
+  __shared__ __align__(16) uint32_t cand[kPick];       // this CTA's candidates
+  __shared__ __align__(16) uint32_t each[kPick];       // the cluster's
+  __shared__ uint32_t n_cand;
   __shared__ uint32_t pub[2][2];                       // kept-for-sure and tied tokens of this CTA's slice
   __shared__ uint32_t wsum[kSelWarps][2];
-  __shared__ uint32_t s_key, s_need;
+  __shared__ uint32_t s_key, s_need, s_left;
   griddep_wait();
   griddep_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -73,7 +78,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
   const int mid0 = ms, mid1 = len - mr, rest = n - ms - mr;
   const int i0 = min(len, static_cast<int>(rank) * a.slice), i1 = min(len, i0 + a.slice);
   const float* src = a.score + row * a.score_ld;
-  for (int i = i0 + tid; i < i1; i += kSelThreads) xs[i - i0] = src[i];
+  // all on their way at once; slices start at multiples of 4
+  const uint32_t xs0 = static_cast<uint32_t>(__cvta_generic_to_shared(xs));
+  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+  const int i4 = vec ? i0 + (i1 - i0) / 4 * 4 : i0;
+  for (int i = i0 + 4 * tid; i < i4; i += 4 * kSelThreads)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(xs0 + 4u * (i - i0)), "l"(src + i) : "memory");
+  for (int i = i4 + tid; i < i1; i += kSelThreads)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(xs0 + 4u * (i - i0)), "l"(src + i) : "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
   // the `rest`-th highest key between, and how many of its equals are taken
   uint32_t key = 0, need = 0xffffffffu;                // everything between
@@ -82,49 +95,92 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a,
       key = 0xffffffffu;                               // (above every key)
       need = 0;
     } else {
-      uint32_t left = rest;
+      uint32_t left = rest, known = 0;                 // bits of the key that are known, from the top
       const int j0 = max(i0, mid0), j1 = min(i1, mid1);
       key = 0;
       for (int b = tid; b < kBins; b += kSelThreads) hist[0][b] = 0;
+      if (tid == 0) n_cand = 0;
       __syncthreads();
-      for (int pass = 0; pass < 4; ++pass) {
-        const int sh = 24 - 8 * pass;
+      const int own = csize > 1 ? 1 : 4;               // digits of a thread
+      for (int pass = 0;; ++pass) {
+        const int bits = min(csize > 1 ? 8 : 11, 32 - static_cast<int>(known)), down = 32 - static_cast<int>(known) - bits;
         uint32_t* hs = hist[pass & 1];
         for (int i = j0 + tid; i < j1; i += kSelThreads) {
           const uint32_t k = score_key(xs[i - i0]);
-          if (pass == 0 || (k >> (sh + 8)) == (key >> (sh + 8))) atomicAdd(&hs[(k >> sh) & 255u], 1u);
+          if (known == 0 || (k ^ key) >> (32 - known) == 0) atomicAdd(&hs[(k >> down) & ((1u << bits) - 1u)], 1u);
         }
         if (csize > 1) cl::sync();
         else __syncthreads();
-        if (tid < kBins) {
-          uint32_t t = 0;
-          for (uint32_t c = 0; c < csize; ++c) t += csize > 1 ? cl::peek(&hs[tid], c) : hs[tid];
-          tot[tid] = t;
-          hist[(pass & 1) ^ 1][tid] = 0;               // (its readers passed this pass's barrier)
+        // digits from the highest, `own` to a thread
+        const int top = (1 << bits) - 1 - own * tid;
+        uint32_t v[4] = {0, 0, 0, 0}, mine = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (u >= own || top < u) break;
+          if (csize > 1) {
+#pragma unroll
+            for (uint32_t c = 0; c < 8; ++c)
+              if (c < csize) v[u] += cl::peek(&hs[top - u], c);
+          } else {
+            v[u] = hs[top - u];
+          }
+          mine += v[u];
+        }
+        for (int b = tid; b < (1 << bits); b += kSelThreads) hist[(pass & 1) ^ 1][b] = 0;   // (its readers passed this barrier)
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (lane == 31) wsum[warp][0] = inc;
+        __syncthreads();
+        uint32_t before = inc - mine;
+        for (int w = 0; w < warp; ++w) before += wsum[w][0];
+        if (before < left && left <= before + mine) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (before < left && left <= before + v[u]) {
+              s_key = key | (static_cast<uint32_t>(top - u) << down);
+              s_need = left - before;
+              s_left = v[u];
+            }
+            before += v[u];
+          }
         }
         __syncthreads();
-        if (warp == 0) {
-          // digits from the highest: lane l owns 255 - 8 l .. 248 - 8 l
-          uint32_t mine = 0, v[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mine += v[u] = tot[255 - 8 * lane - u];
-          uint32_t inc = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+        key = s_key;
+        left = s_need;
+        known += bits;
+        if (known == 32 || s_left <= kPick) break;
+      }
+      if (known < 32) {                                // few candidates: each compares itself with all
+        for (int i = j0 + tid; i < j1; i += kSelThreads) {
+          const uint32_t k = score_key(xs[i - i0]);
+          if ((k ^ key) >> (32 - known) == 0) cand[atomicAdd(&n_cand, 1u)] = k;
+        }
+        const uint32_t n_all = s_left;
+        if (csize > 1) cl::sync();
+        else __syncthreads();
+        uint32_t to = 0;
+        for (uint32_t c = 0; c < csize; ++c) {
+          const uint32_t m = csize > 1 ? cl::peek(&n_cand, c) : n_cand;
+          if (tid < static_cast<int>(m)) each[to + tid] = csize > 1 ? cl::peek(&cand[tid], c) : cand[tid];
+          to += m;
+        }
+        if (tid < 4 && n_all + tid < kPick) each[n_all + tid] = 0;   // (pads the last four; key 0 is below or equal to all)
+        __syncthreads();
+        const uint32_t k = tid < static_cast<int>(n_all) ? each[tid] : 0;
+        uint32_t more = 0, same = 0;
+        if (32 * warp < static_cast<int>(n_all))
+          for (uint32_t j = 0; j < n_all; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&each[j]);
+            more += (o.x > k) + (o.y > k) + (o.z > k) + (o.w > k);
+            same += (o.x == k) + (o.y == k) + (o.z == k) + (o.w == k);
           }
-          uint32_t before = inc - mine;
-          if (before < left && left <= inc) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if (before < left && left <= before + v[u]) {
-                s_key = key | (static_cast<uint32_t>(255 - 8 * lane - u) << sh);
-                s_need = left - before;
-              }
-              before += v[u];
-            }
-          }
+        if (tid < static_cast<int>(n_all) && more < left && left <= more + same) {
+          s_key = k;
+          s_need = left - more;
         }
         __syncthreads();
         key = s_key;
@@ -387,13 +443,17 @@ TV_API int kv4_evict_select(const float* score, int64_t score_ld, const int32_t*
   if (!cache_len || !budget || !new_len || new_len == cache_len) return TV_EINVAL;
   if ((max_len > 0 && !score) || (idx_ld > 0 && !idx)) return TV_EINVAL;
   if (score_out == score && score_out_ld != score_ld) return TV_EINVAL;
-  const int c = select_cluster(max_len), slice = (max_len + c - 1) / c;
-  const int bytes = std::max(slice, 1) * 4;
-  if (bytes > 40 << 10 && !smem_limit(kv4::select_kernel, kMaxSlice * 4)) return TV_ECUDA;
+  const int c = select_cluster(max_len), slice = ((max_len + c - 1) / c + 3) / 4 * 4;
+  const int bytes = std::max(slice, 4) * 4;
+  if (bytes > 24 << 10 && !smem_limit(kv4::select_kernel<512>, kMaxSlice * 4)) return TV_ECUDA;
+  if (c == 8 && !smem_limit(kv4::select_kernel<1024>, kMaxSlice * 4)) return TV_ECUDA;
   const kv4::SelectArgs a{score, cache_len, budget, idx, score_out, new_len, err, score_ld, idx_ld, score_out_ld,
                           n_sink, n_recent, Hkv, max_len, slice};
-  return cl::launch_pdl(kv4::select_kernel, c, dim3(c, Hkv, B), dim3(kv4::kSelThreads), bytes,
-                        reinterpret_cast<cudaStream_t>(stream), a, static_cast<uint32_t>(c));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid(c, Hkv, B);
+  const auto cs = static_cast<uint32_t>(c);
+  return c == 8 ? cl::launch_pdl(kv4::select_kernel<1024>, c, grid, dim3(1024), bytes, st, a, cs)
+                : cl::launch_pdl(kv4::select_kernel<512>, c, grid, dim3(512), bytes, st, a, cs);
 }
 
 TV_API int kv4_compact(void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
