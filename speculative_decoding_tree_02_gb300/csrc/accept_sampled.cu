@@ -166,6 +166,7 @@ constexpr int kList = 256;         // listed logits of a warp
 constexpr int kSort = 1024;        // listed logits of a row, at most
 constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
 constexpr int kCutPick = 4;        // or, for k up to 64 kCutPick, to a cut found among the threads' maxima
+constexpr float kWorth = 8192.f;   // logits of a bin, at most, that are listed before they are told apart further
 constexpr int kScratch = kBins * kAsThreads * 4;
 static_assert(kScratch >= TV_MAX_NODES * 3, "see judge_children");
 static_assert(kScratch / 2 == kAsWarps * kList * 4, "the lists fill the second half of the scratch");
@@ -346,9 +347,9 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
 // one another, which gives each what lies above it, while the others leave.
 // Where the list does not reach the threshold (flat distributions, large k)
 // or overflows, the logits are binned by powers of two of the weight, the
-// threshold's bin by 16th parts of it, twice, until a bin is short enough to
-// be listed; ties beyond that are told apart by four bits of the ordered bits
-// at a time.  All sums have a fixed order.
+// threshold's bin by parts of it, listed as soon as the lists hold it, until it
+// is short enough to be compared; ties beyond that are told apart by four bits
+// of the ordered bits at a time.  All sums have a fixed order.
 template <typename T, bool kTrunc>
 __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads, 4) row_kernel(const RowArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -572,13 +573,13 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         }
         if (lane == 0) sh.listed[warp] = cnt;
       };
-      // After a cluster barrier: logits on the cluster's lists, -1 when one overflowed or they are too many.
+      // After a cluster barrier: logits on the cluster's lists, -1 when one overflowed, -2 when they are too many to compare.
       int c0, c1;                                 // lane l: the counts of segments l and l + 32 of the 64
       auto usable = [&]() {
         of64(sh.listed, c0, c1);
         const bool over = __any_sync(0xffffffffu, c0 > kList || c1 > kList);
         const int sum = __reduce_add_sync(0xffffffffu, min(c0, kList) + min(c1, kList));
-        return over || sum > kSort ? -1 : sum;
+        return over ? -1 : sum > kSort ? -2 : sum;
       };
       // The first CTA copies the lists of all to the start of its scratch: warp w the segments of CTA w.
       auto copy = [&]() {
@@ -697,9 +698,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
 
       // ---- bins of y = (top - l) c, then of a part of them
       // sums of values per bin over the cluster, into sh.tot: every thread adds in a column of its own
-      auto bins = [&](int nb, auto&& add) {
-        for (int b = 0; b < nb; ++b) hist[b * kAsThreads + tid] = 0.f;
-        each(add);
+      auto sum_bins = [&](int nb) {
         __syncthreads();
         for (int b = warp; b < nb; b += kAsWarps) {
           float t = 0.f;
@@ -710,34 +709,48 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         }
         cluster_sums(sh, e++, nb);
       };
+      auto bins = [&](int nb, auto&& add) {
+        for (int b = 0; b < nb; ++b) hist[b * kAsThreads + tid] = 0.f;
+        each(add);
+        sum_bins(nb);
+      };
       float floor_ = -INFINITY;                   // what top-k leaves
       // The lowest logit that is needed for the tokens counted (or weighed)
-      // from the top to reach the target.  true: this CTA has nothing left to do.
-      auto search = [&](bool weigh, float part) {
-        float lo = floor_, hi = INFINITY, above = 0.f, target = part, y0 = 0.f, inv = 1.f;
-        for (int level = 0; level < 3; ++level) {
-          auto bin_of = [&](float l) { return static_cast<int>(fminf(fmaxf(((top - l) * c - y0) * inv, 0.f), kBins - 1.f)); };
-          if (weigh)
-            bins(kBins, [&](float l) {
+      // from the top to reach the target; bins from y0 on, 1 / inv wide.  true: this CTA has nothing left to do.
+      auto search = [&](bool weigh, float part, float y0, float inv) {
+        float lo = floor_, hi = INFINITY, above = 0.f, target = part;
+        bool listed = false;                      // the lists hold all of [lo, hi]
+        for (int level = 0; level < 5; ++level) {
+          const int nb = listed ? kBins / 2 : kBins;    // (the lists keep their half of the scratch)
+          auto bin_of = [&](float l) { return static_cast<int>(fminf(fmaxf(((top - l) * c - y0) * inv, 0.f), nb - 1.f)); };
+          if (listed) {
+            for (int b = 0; b < nb; ++b) hist[b * kAsThreads + tid] = 0.f;
+            for (int q = lane; q < sh.listed[warp]; q += 32) {
+              const float l = list[warp * kList + q];
+              hist[bin_of(l) * kAsThreads + tid] += weigh ? weight(l) : 1.f;
+            }
+            sum_bins(nb);
+          } else if (weigh) {
+            bins(nb, [&](float l) {
               if (l >= lo && l <= hi) hist[bin_of(l) * kAsThreads + tid] += weight(l);
             });
-          else
-            bins(kBins, [&](float l) {
+          } else {
+            bins(nb, [&](float l) {
               if (l >= lo && l <= hi) hist[bin_of(l) * kAsThreads + tid] += 1.f;
             });
+          }
           if (weigh && level == 0) {
             float t = 0.f;
-            for (int b = 0; b < kBins; ++b) t += sh.tot[b];
+            for (int b = 0; b < nb; ++b) t += sh.tot[b];
             target = part * t;
           }
-          const int bin = crossing(sh.tot, kBins, target, above, above);
+          const int bin = crossing(sh.tot, nb, target, above, above);
           // at most so many logits in the bin, and down to it
           float most = 0.f, whole = 0.f;
           for (int b = 0; b <= bin; ++b) {
             most = weigh ? sh.tot[b] * exp2f(y0 + (b + 1) / inv) : sh.tot[b];
             whole += most;
           }
-          const bool everything = level == 0 && by_k && !weigh && whole <= kSort && bin < kBins - 1;
           // the bin's lowest and highest number, by bisection of the ordered bits
           if (warp == 0) {
             const bool low = lane == 0;
@@ -753,43 +766,66 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
                 else k1 = mid - 1u;
               }
             }
-            if (lane == 0) sh.scan[0] = bin == kBins - 1 && level == 0 ? -INFINITY : key_value(k0);
+            if (lane == 0) sh.scan[0] = bin == nb - 1 && level == 0 ? -INFINITY : key_value(k0);
             if (lane == 1) sh.scan[1] = bin == 0 && level == 0 ? INFINITY : key_value(k0);
           }
           __syncthreads();
           lo = fmaxf(lo, sh.scan[0]);
-          if (!everything) hi = fminf(hi, sh.scan[1]);
+          hi = fminf(hi, sh.scan[1]);
           __syncthreads();
-          if (everything || most <= kSort) {
+          // top-k whose few logits are worth listing as a whole: top-p then needs no search of its own
+          if (level == 0 && !weigh && whole <= kSort && bin < nb - 1) {
+            float u0, u1;
+            make_list(lo, INFINITY, false, u0, u1);
+            cl::sync();
+            cnt = usable();
+            if (cnt > 0) {
+              finish(cnt, 0.f);
+              return true;
+            }
+          } else if (listed) {                    // what of the lists is in the bin
+            int kept = 0;
+            const int had = sh.listed[warp];
+            for (int q = 0; q < had; q += 32) {
+              const float l = q + lane < had ? list[warp * kList + q + lane] : NAN;
+              const bool in = l >= lo && l <= hi;
+              const unsigned m = __ballot_sync(0xffffffffu, in);
+              if (in) list[warp * kList + kept + __popc(m & ((1u << lane) - 1u))] = l;
+              kept += __popc(m);
+              __syncwarp();
+            }
+            if (lane == 0) sh.listed[warp] = kept;
+            cl::sync();
+            cnt = usable();
+          } else if (most <= kWorth) {
             float u0, u1;
             make_list(lo, hi, false, u0, u1);
             cl::sync();
             cnt = usable();
-            if (cnt > 0) {
-              if (everything) {
-                finish(cnt, 0.f);
-                return true;
+            listed = cnt != -1;
+          } else {
+            cnt = -1;
+          }
+          if (listed && cnt > 0) {
+            if (rank == 0) copy();
+            cl::sync();                           // (this and the next: sh.out is written between two barriers)
+            if (rank == 0) {
+              if (weigh) {
+                settle(cnt, 0, above, target, -1.f);
+                out.inv = mass > 0.f ? 1.f / mass : 0.f;
+                publish(out);
+              } else {
+                settle(cnt, max(1, static_cast<int>(target - above)), 0.f, -1.f, -1.f);
+                if (tid == 0) sh.out = out.floor;
               }
-              if (rank == 0) copy();
-              cl::sync();                         // (this and the next: sh.out is written between two barriers)
-              if (rank == 0) {
-                if (weigh) {
-                  settle(cnt, 0, above, target, -1.f);
-                  out.inv = mass > 0.f ? 1.f / mass : 0.f;
-                  publish(out);
-                } else {
-                  settle(cnt, max(1, static_cast<int>(target - above)), 0.f, -1.f, -1.f);
-                  if (tid == 0) sh.out = out.floor;
-                }
-              }
-              if (weigh) return true;
-              cl::sync();
-              floor_ = cl::peek(&sh.out, 0);
-              return false;
             }
+            if (weigh) return true;
+            cl::sync();
+            floor_ = cl::peek(&sh.out, 0);
+            return false;
           }
           y0 += bin / inv;
-          inv *= kBins;
+          inv *= listed ? kBins / 2 : kBins;
         }
         // flat to the last: by four bits of the ordered bits; keys in [klo, khi], those above `bits` the same in both
         uint32_t klo = order_key(lo), khi = order_key(fminf(hi, top));
@@ -814,9 +850,10 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         mass = above + cls;
         return false;
       };
-      if (by_k && search(false, static_cast<float>(k))) return;
+      const bool below = !by_k && cnt > 0;         // the list was complete, the threshold lies below it
+      if (by_k && search(false, static_cast<float>(k), 0.f, 1.f)) return;
       if (by_p) {
-        if (search(true, nucleus)) return;
+        if (search(true, nucleus, below ? kCut : 0.f, below ? 2.f : 1.f)) return;
       } else {                                    // the mass of the k highest
         float t = 0.f;
         each([&](float l) { t += l >= floor_ ? weight(l) : 0.f; });
