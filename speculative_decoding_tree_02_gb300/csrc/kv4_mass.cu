@@ -191,17 +191,15 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
   const float* before = a.score_in + row * a.in_ld;
   auto fetch = [&](int t0, Tile& x) {
     if (t0 >= t_hi) return;
+    const int t = t0 + (lane >> 2) + 8 * (lane & 3);
+    x.had = had && t < min(t_hi, sp.old) ? before[t] : 0.f;
+    if (a.n_pages == 0) return;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-#pragma unroll
-      for (int i = 2 * m; i < 2 * m + 2; ++i) {
-        x.sc[i] = 0;
-#pragma unroll
-        for (int w = 0; w < kRun; ++w) x.w[i][w] = 0;
-      }
-      if (static_cast<unsigned>(x.page[m]) >= static_cast<unsigned>(a.n_pages)) continue;
+      // (a bad page: some page, and the weights are dropped when they are stored)
+      const int page = static_cast<unsigned>(x.page[m]) < static_cast<unsigned>(a.n_pages) ? x.page[m] : 0;
       const int slot = (t0 + 16 * m) & (a.P - 1);
-      const uint8_t* blk = heads + x.page[m] * page_bytes;
+      const uint8_t* blk = heads + page * page_bytes;
       const uint8_t* at = blk + lane_key + 16 * slot;
       const uint8_t* sc = blk + lane_sc + 2 * slot;
 #pragma unroll
@@ -216,10 +214,8 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
         x.sc[2 * m + i] = __ldg(reinterpret_cast<const uint16_t*>(sc + 16 * i));
       }
     }
-    const int t = t0 + (lane >> 2) + 8 * (lane & 3);
-    x.had = had && t < min(t_hi, sp.old) ? before[t] : 0.f;
   };
-  Tile next;
+  Tile next = {};
   int t0 = t_lo + 32 * warp;
   pages(t0, next.page);
 
