@@ -316,7 +316,8 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
  *   temperature float [B] or NULL (1); top_k int32 [B] or NULL (0 or less: off);
  *            top_p float [B] or NULL (1 or more, or NaN: off)
  *   u_node   float [n] in [0, 1); race float [B, ldr], positive
- *   total_nodes  rows of the inputs; max_nodes <= TV_MAX_NODES; V <= 2^20
+ *   total_nodes  rows of the inputs; max_nodes <= TV_MAX_NODES; V <= 2^20, with
+ *            top_k or top_p <= 835584 (bf16) or 417792 (fp32)
  * Outputs: as accept_rejection_sampling (accept_len -1, best_node -1, bonus -1
  *   for a request without nodes).
  * Workspace: accept_sampled_workspace_size(...) bytes, 16-byte aligned.
@@ -652,7 +653,8 @@ int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pa
  * A row with lse = -inf (it saw nothing) weighs nothing; a NaN row makes the
  * tokens that it sees NaN.  A token with a bad page entry gets no weight, a row
  * outside [0, total_rows) gives none, tokens beyond max_len or the table and
- * rows beyond max_rows are left out: each writes 1 to *err.
+ * rows beyond max_rows are left out: each writes 1 to *err.  A device-side wait
+ * that ran out (2 s) makes the tokens concerned NaN, and 1 is written to *err.
  * -------------------------------------------------------------------------- */
 int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype, const void* cache, int n_pages,
                   int page_size, const int32_t* block_table, int table_ld, const int32_t* cache_len,
@@ -669,7 +671,8 @@ int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype, const
  *   score [B, Hkv, score_ld] float; max_len bounds cache_len, at most 393216
  * Outputs: idx int32 [B, Hkv, idx_ld]: the kept tokens, ascending, -1 behind
  *   them; score_out [B, Hkv, score_out_ld] float or NULL: their scores (may be
- *   score: the rows shrink in place); new_len int32 [B]: n.
+ *   score: the rows shrink in place); new_len int32 [B], not cache_len or
+ *   budget: n.
  * More kept tokens than idx_ld: idx_ld of them, and 1 is written to *err; so it
  * is for a negative budget (0).  A cache_len outside [0, max_len]: new_len is
  * cache_len, nothing is kept, 1 is written to *err.
@@ -683,8 +686,8 @@ int kv4_evict_select(const float* score, int64_t score_ld, const int32_t* cache_
  * codes and scales as they are.
  *   idx int32 [B, Hkv, idx_ld]: ascending in each row, as kv4_evict_select
  *           gives it; max_keep <= idx_ld bounds new_len (launch geometry)
- *   dst_table int32 [B, dst_ld] or NULL.  NULL: in place, on the request's own
- *           pages (no two requests share one).  Else the tokens go to these
+ *   dst_table int32 [B, dst_ld] or NULL.  NULL (or block_table): in place, on the
+ *           request's own pages (no two requests share one).  Else the tokens go to these
  *           pages, which are nobody's source in the call: sources may be shared.
  * Other tokens of the destination keep what they hold (in place: those from
  * new_len on).  A token whose index is outside [0, cache_len[r]) or whose

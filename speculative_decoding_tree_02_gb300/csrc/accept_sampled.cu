@@ -23,6 +23,7 @@ constexpr int kAsCluster = 8;
 constexpr int kAsThreads = 256;
 constexpr int kAsWarps = kAsThreads / 32;
 constexpr int kAsMaxVocab = 1 << 20;
+constexpr int kMaxSlice = 220 << 10;   // shared memory of a CTA that stages its slice of a row
 constexpr int kBins = 16;
 
 // What row_kernel says of a row: p(v) = 2^((l - top) c) inv for l >= floor, else 0;
@@ -1112,19 +1113,16 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
   // nodes in the order of their index, the requests' side by side: a row's
   // descendants come late enough to be left out when it ends the walk
   const dim3 rows(static_cast<unsigned>(kAsCluster) * B, ra.max_nodes);
-  int rc;
+  const size_t row_smem =
+      trunc ? ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kScratch : kPruneBytes;
+  if (row_smem > kMaxSlice) return TV_EUNSUPPORTED;
+  if (trunc && !smem_limit(row_kernel<T, true>, kMaxSlice)) return TV_ECUDA;
   if (ra.dead && cudaMemsetAsync(ra.dead, 0, static_cast<size_t>(ra.total) * 4, st) != cudaSuccess) {
     cudaGetLastError();
     return TV_ECUDA;
   }
-  if (trunc) {
-    const size_t smem = ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kScratch;
-    if (smem > 220 << 10) return TV_EUNSUPPORTED;
-    if (!smem_limit(row_kernel<T, true>, 220 << 10)) return TV_ECUDA;
-    rc = launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), smem, st, ra);
-  } else {
-    rc = launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), kPruneBytes, st, ra);
-  }
+  const int rc = trunc ? launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), row_smem, st, ra)
+                       : launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), row_smem, st, ra);
   if (rc != TV_OK) return rc;
   const size_t smem = static_cast<size_t>(wa.max_nodes) * sizeof(RowStat) + static_cast<size_t>(S + 31) / 32 * 4;
   if (smem > 20 << 10 && !smem_limit(walk_kernel<T>, 40 << 10)) return TV_ECUDA;

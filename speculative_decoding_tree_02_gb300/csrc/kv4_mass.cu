@@ -382,6 +382,7 @@ TV_API int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype
   if (total_rows > 0 && max_rows > 0 && (!q || !lse)) return TV_EINVAL;
   if (ldq < static_cast<int64_t>(Hq) * d || ldq % (dtype == TV_BF16 ? 8 : 4)) return TV_EINVAL;
   if ((q && !aligned(q, 16)) || (cache && !aligned(cache, 16))) return TV_EINVAL;
+  if (total_rows == 0) max_rows = 0;      // no row can be read
   const kv4::MassArgs a{q, lse, static_cast<const uint8_t*>(cache), block_table, cache_len, row_off, path, vis_prefix,
                         old_len, score_in, score_out, err, ldq, score_in_ld, score_out_ld, n_pages, page_size, table_ld,
                         path_ld, causal, max_rows, total_rows, max_len, Hq, Hkv, scale, decay};

@@ -130,6 +130,18 @@ def test_mass_bad_pages_rows_and_bounds(tv):
     assert int(err) == 1
 
 
+def test_mass_without_rows_or_pages_only_decays(tv):
+    i32 = lambda *a: dev(np.array(a, np.int32))  # noqa: E731
+    s = torch.rand(1, 2, 40, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        for pages, table in ((3, [[0, 1, 2]]), (0, [[0, 1, 2]])):
+            q = torch.zeros((0, 4, 64), dtype=dt, device="cuda")
+            cache = torch.zeros((pages, 2, 16 * 68), dtype=torch.uint8, device="cuda")
+            out, err = tv.kv4_attn_mass(q, torch.zeros(0, 4, device="cuda"), cache, 16, i32(*table), i32(40), i32(0, 0), 4,
+                                        score=s, decay=0.5)
+            assert torch.equal(out, 0.5 * s) and int(err) == (pages == 0)
+
+
 def test_mass_nan_reaches_only_what_sees_it(tv):
     for bf16 in (True, False):
         m = Mass(9, [90], [6], 4, 2, 64, 16, bf16, causal=False, vis=True)
@@ -290,9 +302,15 @@ def test_compact_skips_what_is_bad(tv):
                     s = idx[0, h, j0 + j]
                     moved = 0 <= s < 64 and not 16 <= s < 32
                     assert torch.equal(y[j, h], x[s, h] if moved else z[j, h])
+    # the request's own table as the destination is in place
+    cache, same = dev(pool[0]), dev(pool[0])
+    idx = choose(rng, [64], [48], H, 48)
+    t = dev(table)
+    assert int(tv.kv4_compact(cache, P, t, i32(64), dev(idx), i32(48), 48, dst_table=t)) == 0
+    assert int(tv.kv4_compact(same, P, t, i32(64), dev(idx), i32(48), 48)) == 0
+    assert torch.equal(cache, same)
     # more than max_keep: the first max_keep
     cache = dev(pool[0])
-    idx = choose(rng, [64], [48], H, 48)
     err = tv.kv4_compact(cache, P, dev(table), i32(64), dev(idx), i32(48), 20)
     now = codes(tv, cache, P, table, [64])[0]
     assert int(err) == 1

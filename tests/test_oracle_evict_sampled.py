@@ -142,7 +142,7 @@ def test_attn_mass_refusals(lib, want, change):
 @pytest.mark.parametrize("want,change", [
     (-1, dict(B=-1)), (-1, dict(H=0)), (-1, dict(sink=-1)), (-1, dict(recent=-1)), (-1, dict(ld=63)), (-1, dict(out_ld=31)),
     (-2, dict(B=70000)), (-2, dict(max_len=500000, ld=500000)), (-1, dict(cache_len=None)), (-1, dict(budget=None)),
-    (-1, dict(new_len=None)), (-1, dict(new_len=B_)), (-1, dict(score=None)), (-1, dict(idx=None)), (-1, dict(out=B_)),
+    (-1, dict(new_len=None)), (-1, dict(new_len=B_)), (-1, dict(budget=ODD)), (-1, dict(score=None)), (-1, dict(idx=None)), (-1, dict(out=B_)),
     (0, dict(B=0))])
 def test_evict_select_refusals(lib, want, change):
     assert call(lib, "kv4_evict_select", SELECT, **change) == want
@@ -159,7 +159,8 @@ def test_compact_refusals(lib, want, change):
 
 @pytest.mark.parametrize("want,change", [
     (-1, dict(dtype=3)), (-1, dict(B=-1)), (-1, dict(V=0)), (-1, dict(ld=99)), (-1, dict(ldr=99)), (-1, dict(ldq=99)),
-    (-1, dict(q=None, drawn=B_)), (-2, dict(max_nodes=1025)), (-2, dict(V=(1 << 20) + 1, ld=1 << 21, ldq=1 << 21, ldr=1 << 21)),
+    (-1, dict(q=None, drawn=B_)), (-2, dict(max_nodes=1025)), (-2, dict(V=840000, ld=840000, ldq=840000, ldr=840000, k=B_)),
+    (-2, dict(V=420000, ld=420000, ldq=420000, ldr=420000, tp=B_, dtype=0)), (-2, dict(V=(1 << 20) + 1, ld=1 << 21, ldq=1 << 21, ldr=1 << 21)),
     (-2, dict(B=70000)), (-1, dict(node_off=None)), (-1, dict(acc=None)), (-1, dict(parent=None)), (-1, dict(p=None)),
     (-1, dict(u=None)), (-1, dict(race=None)), (-4, dict(ws=None)), (-4, dict(ws_bytes=79)), (-4, dict(ws=ODD)),
     (0, dict(B=0))])
