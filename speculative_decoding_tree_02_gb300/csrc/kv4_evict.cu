@@ -41,9 +41,8 @@ constexpr int kPick = 512;             // candidates that are compared directly
 // that it lies in has at most 512 tokens, which are listed and compared with one
 // another: one count for a few thousand scores.  Then kept tokens get their
 // places from counts in index order, ties included.  512 threads, 1024 in a
-// cluster of 8.  Latency bound: 64 x 8 rows of 512..4096 scores 16.7 us with the
-// call (16.3 of them the SMs with four of the longest rows), 8 rows of 131072
-// 22.7 us.
+// cluster of 8.  Latency bound: 64 x 8 rows of 512..4096 scores 16.7 us (8 at the
+// median row, 16 on SMs with four of the longest), 8 rows of 131072 22.7 us.
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a, const uint32_t csize) {
   constexpr int kSelWarps = kSelThreads / 32;
@@ -278,9 +277,9 @@ struct Window {
 //   rounds read; one cluster barrier between a round's reads and its writes
 //   makes that hold inside the round too.
 //   else: every window is a CTA of its own.
-// Kept tokens among others that go cost whole sectors: 26112 of 73800 tokens of
-// 8 heads of 128 read 75 MB for 27.6 MB kept.  Those in 30 us and their values
-// back as rows in 20 (together 50).
+// Kept tokens among others that go cost whole sectors: 24341 of 72097 tokens of 8
+// heads of 128 (25.7 MB) read 75 MB.  27.6 us from cold caches, 36% of the DRAM's
+// peak; waits for memory (resolving a token is three dependent loads).
 template <int D, bool kInPlace>
 __global__ void __launch_bounds__(kInPlace ? 4 * D : D) compact_kernel(const CompactArgs a) {
   __shared__ Window win[kInPlace ? 4 : 1];

@@ -85,7 +85,11 @@ __device__ __forceinline__ float mass_before(const MassArgs& a, const MassSpan& 
   return a.decay * a.score_in[row * a.in_ld + t];
 }
 
-constexpr int kFewRows = 128;   // query rows per KV head up to which mass_few takes a call
+// Query rows per KV head up to which mass_few takes a call: its time grows with the
+// rows (58 us for up to 64 rows of 64 requests), mass_tc's by the set-up of 256
+// tokens (6 us) until rows fill it.  The bound is what fits its shared memory at
+// four CTAs to an SM; between 64 and 128 rows the two were not timed.
+constexpr int kFewRows = 128;
 
 int mass_simt(const MassArgs& a, int B, int d, cudaStream_t st);   // fp32 rows
 int mass_few(const MassArgs& a, int B, int d, cudaStream_t st);    // bf16, few rows per KV head

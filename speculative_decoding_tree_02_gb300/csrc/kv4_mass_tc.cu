@@ -15,6 +15,9 @@
 //   warp 20       the rows' lse and visible lengths
 //   warp 21       issues the MMAs
 // S has three buffers per tile, so that the MMAs run ahead of the exponentials.
+// 8 requests of 1024 rows x 32 heads over 1024..4096 tokens: 193 us (39% of the
+// measured matrix rate); 64 rows take a CTA 1000 cycles, of which the 16384
+// exponentials are 512 and the issue slots 690.
 //
 // Every wait is bounded (2 s); a role whose wait expires raises the CTA's abort
 // flag, all leave, and the CTA's scores become NaN, with 1 in *err.
