@@ -226,23 +226,23 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
   pages(t0, next.page);
 
   // where the rows lie, their lse and what they see; then the rows, in fragment order
-  if (tid < 8 * blocks) {
+  for (int i = tid; i < 8 * blocks; i += kTile) {
     int vis = 0;
     float l = kInf;
     int64_t at = -1;
-    if (tid < rows) {
-      const int j = tid / g;
+    if (i < rows) {
+      const int j = i / g;
       const MassRow m = mass_row(a, sp, r, j);
       if (m.bad && a.err) *a.err = 1;
       if (!m.bad) {
-        at = m.src * a.ldq + static_cast<int64_t>(h * g + tid - j * g) * D;
-        l = a.lse[m.src * a.Hq + h * g + tid - j * g];
+        at = m.src * a.ldq + static_cast<int64_t>(h * g + i - j * g) * D;
+        l = a.lse[m.src * a.Hq + h * g + i - j * g];
         vis = l == -kInf ? 0 : m.vis;             // (a row that saw nothing weighs nothing)
       }
     }
-    s_at[tid] = at;
-    s_vis[tid] = vis;
-    s_lse[tid] = l == -kInf ? kInf : l * kLog2e;
+    s_at[i] = at;
+    s_vis[i] = vis;
+    s_lse[i] = l == -kInf ? kInf : l * kLog2e;
   }
   __syncthreads();
   {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
   fetch(t0, next);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  if (tid < blocks) {
+  if (tid < blocks) {                             // (blocks <= kFewRows / 8)
     int2 v = make_int2(0x7fffffff, 0);
     for (int i = 8 * tid; i < 8 * tid + 8; ++i) v = make_int2(min(v.x, s_vis[i]), max(v.y, s_vis[i]));
     s_span[tid] = v;
@@ -356,6 +356,8 @@ int mass_few(const MassArgs& a, int B, int d, cudaStream_t st) {
   const int run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (16ll * kTile * sm_count())))) * kTile;
   const dim3 grid(static_cast<unsigned>((a.max_len + run - 1) / run), a.Hkv, B);
   const size_t smem = static_cast<size_t>((rows + 7) / 8) * 16 * d;
+  if (smem > 40 << 10 && !(d == 128 ? smem_limit(few_kernel<128>, kFewRows * 256) : smem_limit(few_kernel<64>, kFewRows * 128)))
+    return TV_ECUDA;
   return d == 128 ? launch_pdl(few_kernel<128>, grid, dim3(kTile), smem, st, a, run, kMagic)
                   : launch_pdl(few_kernel<64>, grid, dim3(kTile), smem, st, a, run, kMagic);
 }

@@ -85,11 +85,11 @@ __device__ __forceinline__ float mass_before(const MassArgs& a, const MassSpan& 
   return a.decay * a.score_in[row * a.in_ld + t];
 }
 
-// Query rows per KV head up to which mass_few takes a call: its time grows with the
-// rows (58 us for up to 64 rows of 64 requests), mass_tc's by the set-up of 256
-// tokens (6 us) until rows fill it.  The bound is what fits its shared memory at
-// four CTAs to an SM; between 64 and 128 rows the two were not timed.
-constexpr int kFewRows = 128;
+// Query rows per KV head up to which mass_few takes a call; mass_tc pays the set-up
+// of 256 tokens (5.6 us) before the rows count.  us for 128, 160, 192 and 224 rows
+// of 8 heads of 128, few against tc: 64 requests of 512..4096 tokens 121 146 171
+// 209 against 211 231 235 254, 8 of 8192 72 87 99 127 against 77 86 88 97.
+constexpr int kFewRows = 192;
 
 int mass_simt(const MassArgs& a, int B, int d, cudaStream_t st);   // fp32 rows
 int mass_few(const MassArgs& a, int B, int d, cudaStream_t st);    // bf16, few rows per KV head

@@ -83,6 +83,8 @@ class Mass:
     ([260, 40], [150, 40], 10, 2, 64, 16, dict(path=True, vis=True)),
     ([700], [90], 128, 2, 64, 64, dict(causal=False)),
     ([610], [600], 16, 1, 64, 32, dict()),
+    ([300, 61], [48, 48], 8, 2, 128, 64, dict()),                # the most rows of the kernel for few
+    ([300, 61], [49, 49], 8, 2, 128, 64, dict()),
     ([90, 35], [20, 35], 6, 2, 128, 32, dict(path=True, vis=True)),
 ])
 def test_mass_matches(tv, lens, counts, Hq, Hkv, d, P, kw, bf16):
