@@ -5,11 +5,11 @@
 // Two kernels.  row_kernel takes the nodes' rows of logits side by side: a
 // cluster of 8 CTAs per row finds its maximum, the truncation's threshold and
 // the mass of what is kept, 16 bytes per row; rows that the walk turns out not
-// to reach while others are still waiting are left out.  walk_kernel then needs single logits for
-// the accept tests, and passes over a row only for what a rejected draw leaves
-// and for the last token.  Rejections only ever turn the distribution into
-// max(0, a p - b q) without the tokens that were removed, so two numbers and a
-// bit mask stand for it and no row is written.
+// to reach while others are still waiting are left out.  walk_kernel then needs
+// single logits for the accept tests, and passes over a row only for what a
+// rejected draw leaves and for the last token.  Rejections only ever turn the
+// distribution into max(0, a p - b q) without the tokens that were removed, so
+// two numbers and a bit mask stand for it and no row is written.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -164,7 +164,7 @@ __device__ __forceinline__ bool accepted(float u, bool drawn, float q, float hav
 }
 
 constexpr int kList = 256;         // listed logits of a warp
-constexpr int kSort = 1024;        // listed logits of a row, at most
+constexpr int kCompare = 1024;     // listed logits of a row that are compared with one another, at most
 constexpr float kCut = 12.f;       // the first list goes down to 2^-kCut of the highest weight
 constexpr int kCutPick = 4;        // or, for k up to 64 kCutPick, to a cut found among the threads' maxima
 constexpr float kWorth = 8192.f;   // logits of a bin, at most, that are listed before they are told apart further
@@ -174,10 +174,8 @@ static_assert(kScratch / 2 == kAsWarps * kList * 4, "the lists fill the second h
 
 struct RowShared {
   float xf[2][kBins];              // exchanged with the cluster, by parity
-  int xi[2][2];
   float tot[kBins];
   float wred[kAsWarps];
-  int wred_i[kAsWarps];
   float wmax[kAsWarps], wcut[kAsWarps], wz[kAsWarps], wzl[kAsWarps];   // per warp, read by the cluster, written once
   int wfirst[kAsWarps];
   int listed[kAsWarps];            // logits that passed the list's condition, per warp
@@ -583,7 +581,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
         of64(sh.listed, c0, c1);
         const bool over = __any_sync(0xffffffffu, c0 > kList || c1 > kList);
         const int sum = __reduce_add_sync(0xffffffffu, min(c0, kList) + min(c1, kList));
-        return over ? -1 : sum > kSort ? -2 : sum;
+        return over ? -1 : sum > kCompare ? -2 : sum;
       };
       // The first CTA copies the lists of all to the start of its scratch: warp w the segments of CTA w.
       auto copy = [&]() {
@@ -618,8 +616,8 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       // the mass `target`, or its share of z; below 0: off) keep, whole classes as
       // equals get equal numbers.  Sets out.floor and mass, `above` included.
       auto settle = [&](int cnt, int left, float above, float target, float share) {
-        constexpr int kOwn = kSort / kAsThreads;
-        float* ws = hist + kSort;                 // weights
+        constexpr int kOwn = kCompare / kAsThreads;
+        float* ws = hist + kCompare;                 // weights
         const int pad = (cnt + 3) / 4 * 4;
         for (int q = tid; q < pad; q += kAsThreads) {
           if (q >= cnt) hist[q] = -INFINITY;
@@ -682,7 +680,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       // (all of them, if the list has room for a whole row)
       float z = 0.f, zl = 0.f;
       const float lowest = -3.402823466e38f;
-      make_list(V <= kSort ? lowest : fmaxf(by_cut ? cut : top - kCut / c, lowest), INFINITY, !by_k, z, zl);
+      make_list(V <= kCompare ? lowest : fmaxf(by_cut ? cut : top - kCut / c, lowest), INFINITY, !by_k, z, zl);
       z = warp_sum(z);
       zl = warp_sum(zl);
       if (lane == 0) { sh.wz[warp] = z; sh.wzl[warp] = zl; }
@@ -778,7 +776,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
           hi = fminf(hi, sh.scan[1]);
           __syncthreads();
           // top-k whose few logits are worth listing as a whole: top-p then needs no search of its own
-          if (level == 0 && !weigh && whole <= kSort && bin < nb - 1) {
+          if (level == 0 && !weigh && whole <= kCompare && bin < nb - 1) {
             float u0, u1;
             make_list(lo, INFINITY, false, u0, u1);
             cl::sync();

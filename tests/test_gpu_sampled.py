@@ -12,6 +12,7 @@ import torch
 import synth
 from gpu_util import dev, host
 from oracle import sampled as osm
+from oracle.kv4 import bf16_bits
 
 pytestmark = pytest.mark.gpu
 MARGIN = 1e-5
@@ -113,9 +114,10 @@ def test_one_row_workspace_strides_and_streams(tv):
     assert e.value.status == -4
 
 
-def test_masked_and_odd_logits(tv):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_and_odd_logits(tv, dtype):
     """-inf, the type's lowest, NaN and +inf among the logits; a row with nothing but -inf and NaN."""
-    inf, low = float("inf"), np.finfo(np.float32).min
+    inf, low = float("inf"), float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min)
     for T, k, p in ((1.0, 0, 1.0), (0.5, 3, 1.0), (1.0, 0, 0.6), (2.0, 300, 0.99), (0.0, 0, 1.0)):
         c = Case(3, [6] * 12, 700, dtype="f32", q=None, T=[T], k=[k], p=[p])
         rng = np.random.default_rng(4)
@@ -129,6 +131,8 @@ def test_masked_and_odd_logits(tv):
         x[c.off[4]] = low                                    # a uniform row
         x[c.off[5]] = -inf
         x[c.off[5], 698] = -2.0                              # one token left
+        if dtype == "bf16":
+            c.logits = bf16_bits(x)
         got = c.run(tv)
         want = c.check(got, most=0.25)
         assert host(got[3])[1] == -1 and host(got[3])[2] == -1 and want[3][1] == -1
