@@ -148,9 +148,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool some) {
 // walks over tiles of 32 tokens, the next tile's codes on their way
 // while it works on one.
 
-// 64 requests over 512..4096 tokens, 8 heads of 128: 4 rows per head 30.3 us (43%
+// 64 requests over 512..4096 tokens, 8 heads of 128: 4 rows per head 31.4 us (42%
 // of the measured copy rate for 66 bytes a token and head and the scores), 4..64
-// rows 58.4 us; bound by issue slots (550 instructions per tile, 176 of them the
+// rows 59.7 us; bound by issue slots (550 instructions per tile, 176 of them the
 // codes), then by the MMAs (16 for eight rows, two chains).
 template <int D>
 __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const int run, const uint32_t magic) {
@@ -197,11 +197,8 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
   const float* before = a.score_in + row * a.in_ld;
   auto fetch = [&](int t0, Tile& x) {
     if (t0 >= t_hi) return;
-    const int t = t0 + (lane >> 2) + 8 * (lane & 3);
-    x.had = had && t < min(t_hi, sp.old) ? before[t] : 0.f;
-    if (a.n_pages == 0) return;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < 2 && a.n_pages > 0; ++m) {
       // (a bad page: some page, and the weights are dropped when they are stored)
       const int page = static_cast<unsigned>(x.page[m]) < static_cast<unsigned>(a.n_pages) ? x.page[m] : 0;
       const int slot = (t0 + 16 * m) & (a.P - 1);
@@ -220,6 +217,8 @@ __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const i
         x.sc[2 * m + i] = __ldg(reinterpret_cast<const uint16_t*>(sc + 16 * i));
       }
     }
+    const int t = t0 + (lane >> 2) + 8 * (lane & 3);
+    x.had = had && t < min(t_hi, sp.old) ? before[t] : 0.f;
   };
   Tile next = {};
   int t0 = t_lo + 32 * warp;
