@@ -151,7 +151,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool some) {
 // 64 requests over 512..4096 tokens, 8 heads of 128: 4 rows per head 31.4 us (42%
 // of the measured copy rate for 66 bytes a token and head and the scores), 4..64
 // rows 59.7 us; bound by issue slots (550 instructions per tile, 176 of them the
-// codes), then by the MMAs (16 for eight rows, two chains).
+// codes), then by the rate of mma.sync (16 for eight rows; more
+// chains side by side made no difference).
 template <int D>
 __global__ void __launch_bounds__(kTile, 4) few_kernel(const MassArgs a, const int run, const uint32_t magic) {
   constexpr int kRun = D / 32;                    // words, and 16-byte units of a row, of a lane

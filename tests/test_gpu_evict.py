@@ -189,7 +189,8 @@ def test_mass_agrees_with_the_attention(tv):
 @pytest.mark.parametrize("lens,budget,sink,recent,kind", [
     ([1], [1], 0, 0, "float"), ([5, 0, 9], [3, 4, 20], 1, 1, "float"), ([4000, 333, 1024], [700, 333, 1023], 4, 128, "ties"),
     ([4097, 12], [2048, 1], 3, 4000, "float"), ([9000, 8193], [1, 5000], 0, 0, "ties"), ([40000], [12345], 17, 100, "wild"),
-    ([131072, 77], [16384, 50], 4, 1024, "wild"), ([300], [0], 4, 4, "wild"), ([300] * 70, [37] * 70, 4, 4, "same")])
+    ([131072, 77], [16384, 50], 4, 1024, "wild"), ([300], [0], 4, 4, "wild"), ([300] * 70, [37] * 70, 4, 4, "same"),
+    ([393216], [70001], 4, 1000, "float")])
 def test_select_matches(tv, lens, budget, sink, recent, kind):
     rng = np.random.default_rng(sum(lens))
     H, ld = 2, max(lens) + 3
@@ -319,6 +320,28 @@ def test_compact_skips_what_is_bad(tv):
     for h in range(H):
         assert torch.equal(now[0][:20, h], a[0][torch.from_numpy(idx[0, h, :20].astype(np.int64)).cuda(), h])
         assert torch.equal(now[0][20:, h], a[0][20:, h])
+
+
+def test_pages_beyond_four_gigabytes(tv):
+    """The same tokens on the last pages of a cache of 5.4 GB: weights on every path and the move are the same."""
+    m = Mass(40, [300, 130], [60, 20], 8, 2, 128, 128)
+    small = m.pool[0]
+    far = 160000
+    cache = torch.empty((far + len(small), 2, 128 * 132), dtype=torch.uint8, device="cuda")
+    assert cache.numel() > 1 << 32
+    table = np.where(m.table >= 0, m.table + far, m.table).astype(np.int32)
+    i32 = lambda a: dev(np.array(a, np.int32))  # noqa: E731
+    idx = choose(np.random.default_rng(0), m.lens, [100, 77], 2, 100)
+    for q, rows in ((m.q, 60), (m.q, 8), (m.q.float(), 60)):
+        out = []
+        for c, t, base in ((dev(small), m.table, 0), (cache, table, far)):
+            c[base:base + len(small)] = dev(small)
+            s, err = tv.kv4_attn_mass(q, dev(m.lse), c, 128, dev(t), i32(m.lens), dev(m.off), rows, max_len=300)
+            assert int(err) == int(rows == 8)
+            e = tv.kv4_compact(c, 128, dev(t), i32(m.lens), dev(idx), i32([100, 77]), 100)
+            assert int(e) == 0
+            out.append((s, c[base:base + len(small)].clone()))
+        assert torch.equal(torch.nan_to_num(out[0][0]), torch.nan_to_num(out[1][0])) and torch.equal(out[0][1], out[1][1])
 
 
 # ------------------------------------------------------------------- together
