@@ -691,7 +691,8 @@ def kv4_attn_mass(q, lse, cache, page_size, block_table, cache_len, row_off, max
     """Adds to ``score`` float32 [B, Hkv, columns] (None: zeros) the attention weight that the cached tokens received
     from rows of q [n, Hq, d] (row stride free) whose attention gave ``lse`` float32 [n, Hq].  ``path`` int32 [B, m]
     picks rows as in kv4_append; ``causal``: row j sees old_len + j + 1 cached tokens.  ``max_len`` bounds cache_len
-    (default: what the scores and the table have room for).  ``score_out`` may be ``score``.  Returns score_out, err."""
+    (default: what the scores and the table have room for; a tight bound saves empty CTAs).  ``score_out`` may be
+    ``score``.  Returns score_out, err."""
     dev = q.get_device()
     n, Hq, d = q.shape
     n_pages, Hkv, dc = _cache_geometry(cache, page_size)
