@@ -307,7 +307,7 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
       const bool dc = __shfl_sync(0xffffffffu, drawn, ch), inc = __shfl_sync(0xffffffffu, in, ch);
       bool yes;
       if (st.inv < 0.f) {
-        yes = xc == __float_as_int(st.floor);
+        yes = xc >= 0 && xc == __float_as_int(st.floor);
       } else {
         if (!(left > 0.f)) break;
         // (a token that a rejected sibling had is removed)
@@ -1003,7 +1003,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
     for (int ch = child(cur, cur + 1); ch >= 0; ch = child(cur, ch + 1)) {
       const int x = sh.tok[ch];
       if (greedy) {
-        if (x == __float_as_int(st.floor)) { next = ch; break; }
+        if (x >= 0 && x == __float_as_int(st.floor)) { next = ch; break; }
         continue;
       }
       if (left < 0.f) {                           // after a rejected draw

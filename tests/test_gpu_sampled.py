@@ -138,6 +138,16 @@ def test_masked_and_odd_logits(tv, dtype):
         assert host(got[3])[1] == -1 and host(got[3])[2] == -1 and want[3][1] == -1
 
 
+def test_tokens_outside_the_vocabulary_are_refused(tv):
+    """Also by a greedy row that has no token to choose."""
+    for q in (None, "drawn"):
+        c = Case(11, [5] * 4, 50, "star", dtype="f32", q=q, T=[0.0, 1.0])
+        c.tok[:] = np.tile([-1, -1, 50, -2, 2 ** 31 - 1], 4)
+        c.logits[c.off[0]], c.logits[c.off[1]] = -np.inf, -np.inf
+        want = c.check(c.run(tv), most=0.5)
+        assert (want[0] == 0).all() and (want[3][:2] == -1).all()
+
+
 def test_ties_and_repeated_tokens(tv):
     """Equal logits stay together in a truncation; a retrieved token that comes twice is refused the second time; a
     request at temperature 0 takes the lowest index of the highest logits."""
