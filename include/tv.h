@@ -316,7 +316,9 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
  *   temperature float [B] or NULL (1); top_k int32 [B] or NULL (0 or less: off);
  *            top_p float [B] or NULL (1 or more, or NaN: off)
  *   u_node   float [n] in [0, 1); race float [B, ldr], positive
- *   total_nodes  rows of the inputs; max_nodes <= TV_MAX_NODES; V <= 2^20, with
+ *   total_nodes  rows of the inputs; max_nodes <= TV_MAX_NODES bounds a request's
+ *            nodes (launch geometry; further ones are left out, and with 0 of
+ *            either no request has any); V <= 2^20, with
  *            top_k or top_p <= 835584 (bf16) or 417792 (fp32)
  * Outputs: as accept_rejection_sampling (accept_len -1, best_node -1, bonus -1
  *   for a request without nodes).

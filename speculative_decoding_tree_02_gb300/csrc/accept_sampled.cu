@@ -1116,6 +1116,7 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
   // nodes in the order of their index, the requests' side by side: a row's
   // descendants come late enough to be left out when it ends the walk
   const dim3 rows(static_cast<unsigned>(kAsCluster) * B, ra.max_nodes);
+  const bool some = ra.max_nodes > 0 && ra.total > 0;     // (else no array but the offsets and outputs is there)
   const size_t row_smem =
       trunc ? ((static_cast<size_t>(S) * sizeof(T) + 15) & ~static_cast<size_t>(15)) + kScratch : kPruneBytes;
   if (row_smem > kMaxSlice) return TV_EUNSUPPORTED;
@@ -1124,8 +1125,9 @@ int run(const RowArgs& ra, const WalkArgs& wa, int B, cudaStream_t st) {
     cudaGetLastError();
     return TV_ECUDA;
   }
-  const int rc = trunc ? launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), row_smem, st, ra)
-                       : launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), row_smem, st, ra);
+  const int rc = !some   ? TV_OK
+                 : trunc ? launch_pdl(row_kernel<T, true>, rows, dim3(kAsThreads), row_smem, st, ra)
+                         : launch_pdl(row_kernel<T, false>, rows, dim3(kAsThreads), row_smem, st, ra);
   if (rc != TV_OK) return rc;
   const size_t smem = static_cast<size_t>(wa.max_nodes) * sizeof(RowStat) + static_cast<size_t>(S + 31) / 32 * 4;
   if (smem > 20 << 10 && !smem_limit(walk_kernel<T>, 40 << 10)) return TV_ECUDA;
@@ -1166,7 +1168,7 @@ TV_API int accept_sampled(const int32_t* parent, const int32_t* tok, const void*
   // what runs at a time (four CTAs to an SM).
   const bool prune = static_cast<int64_t>(B) * max_nodes * kAsCluster > 8ll * sm_count() && total_nodes > 0;
   auto* stat = static_cast<RowStat*>(ws);
-  const RowArgs ra{p_logits, node_off, temperature, top_k, top_p, stat, ld, V, std::max(max_nodes, 1), total_nodes, vec_p,
+  const RowArgs ra{p_logits, node_off, temperature, top_k, top_p, stat, ld, V, max_nodes, total_nodes, vec_p,
                    prune ? reinterpret_cast<int32_t*>(stat + total_nodes) : nullptr, parent, tok, q_prob, drawn, u_node,
                    ldq};
   const WalkArgs wa{parent, tok, p_logits, q_prob, drawn, node_off, u_node, race, static_cast<const RowStat*>(ws),
