@@ -151,9 +151,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) mass_tc_kernel(const MassArgs a,
     if (lane == 0) mbar_arrive(kready);
   }
 
-  const uint64_t inv_g = ((1ull << 40) + g - 1) / g;
-  // i / g by a multiplication: exact for i < 2^31 and g <= 64
-  auto node_of = [&](int i) { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(i)) * inv_g >> 40); };
+  // i / g by a multiplication, exact for 0 <= i < 2^31: with 2^s >= g the factor m = floor(2^(31+s) / g) + 1 < 2^32 makes
+  // i m / 2^(31+s) too large by i e / (g 2^(31+s)), 0 < e = m g - 2^(31+s) <= g <= 2^s, that is by less than 1 / g.
+  const int shift = 31 + 32 - __clz(g - 1);
+  const auto inv_g = static_cast<uint32_t>((1ull << shift) / g + 1);
+  auto node_of = [&](int i) { return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(i)) * inv_g >> shift); };
   if (warp >= kConsumers && warp < kConsumers + 4) {
     // ---- copies of the rows
     const int p = tid - 32 * kConsumers;
