@@ -634,12 +634,17 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
           mine[u] = 0.f;
           int more = 0;
           if (u * kAsThreads + 32 * warp < cnt) { // (for the warp as a whole)
-            for (int j = 0; j < pad; j += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(hist + j), w = *reinterpret_cast<const float4*>(ws + j);
-              if (l.x > own[u]) { ++more; mine[u] += w.x; }
-              if (l.y > own[u]) { ++more; mine[u] += w.y; }
-              if (l.z > own[u]) { ++more; mine[u] += w.z; }
-              if (l.w > own[u]) { ++more; mine[u] += w.w; }
+            // (sums of 32 at a time: one sum of all would lose the small weights behind a large one)
+            for (int j0 = 0; j0 < pad; j0 += 32) {
+              float part = 0.f;
+              for (int j = j0; j < min(j0 + 32, pad); j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(hist + j), w = *reinterpret_cast<const float4*>(ws + j);
+                if (l.x > own[u]) { ++more; part += w.x; }
+                if (l.y > own[u]) { ++more; part += w.y; }
+                if (l.z > own[u]) { ++more; part += w.z; }
+                if (l.w > own[u]) { ++more; part += w.w; }
+              }
+              mine[u] += part;
             }
           }
           keep[u] = q < cnt && (left == 0 || more < left);
