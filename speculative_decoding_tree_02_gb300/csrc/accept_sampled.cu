@@ -158,6 +158,11 @@ struct RowArgs {
   int64_t ldq;
 };
 
+// Mass left after a refused proposal is what was left less its probability,
+// until less than this part of the last sum is: a difference of nearly equal
+// numbers is off by the whole's rounding, so the remainder is then summed.
+constexpr float kResum = 0.25f;
+
 // A node's token is accepted: u q < p' for a drawn one, u < p' otherwise.
 __device__ __forceinline__ bool accepted(float u, bool drawn, float q, float have, float left) {
   return u * (drawn ? q : 1.f) < have / left;
@@ -261,8 +266,8 @@ constexpr int kPruneBytes = TV_MAX_NODES * 3;
 
 // What is certain about the children of node i, whose row's stat is known: the
 // walk's own tests in its order and arithmetic, as far as they need nothing
-// but single probabilities, up to the first acceptance, the first rejected
-// draw (which leaves a residual) or the 32nd child.  Rejected children and
+// but single probabilities, up to the first acceptance, the first rejection that
+// leaves a mass to be summed (a draw's, or one below kResum) or the 32nd child.  Rejected children and
 // those behind an accepted one cannot be reached, nor can their descendants:
 // all of these get a.dead = 1.  By a CTA, `room` being shared memory.
 template <typename T>
@@ -309,7 +314,6 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
       if (st.inv < 0.f) {
         yes = xc >= 0 && xc == __float_as_int(st.floor);
       } else {
-        if (!(left > 0.f)) break;
         // (a token that a rejected sibling had is removed)
         const bool twice = __any_sync(0xffffffffu, in && x == xc && (dead >> lane & 1u));
         const float have = twice ? 0.f : pc;
@@ -318,7 +322,13 @@ __device__ __forceinline__ void judge_children(const RowArgs& a, int n0, int nod
           dead |= 1u << ch;
           break;
         }
-        if (!yes && inc && !twice) left -= have;
+        if (!yes && inc && !twice) {
+          left -= have;
+          if (!(left >= kResum)) {
+            dead |= 1u << ch;
+            break;
+          }
+        }
       }
       if (yes) {                                  // the others behind it
         dead |= ch < 31 ? ~0u << (ch + 1) : 0u;
@@ -981,8 +991,9 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
     const T* prow = pl + row * a.ld;
     const float* qrow = a.q ? a.q + row * a.ldq : nullptr;
     const bool greedy = st.inv < 0.f;
-    // what is left of the distribution: max(0, fa p - fb q), removed tokens apart; its mass (-1: not known)
-    float fa = 1.f, fb = 0.f, left = 1.f;
+    // what is left of the distribution: max(0, fa p - fb q), removed tokens apart; its mass (-1: not known), and the
+    // least that a difference may leave of it
+    float fa = 1.f, fb = 0.f, left = 1.f, least = kResum;
     // what is left at eight tokens from v on, w their logits
     auto rest8 = [&](int v, const Raw8<T>& w, float (&y)[8]) {
       float q[8], x[8];
@@ -1000,6 +1011,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
       fa = 1.f;
       fb = 0.f;
       left = 1.f;
+      least = kResum;
       if (kills) revive();
       for (int i = tid; i < n; i += kWalkThreads) sh.flag[i] &= 1;
       __syncthreads();
@@ -1011,7 +1023,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         if (x >= 0 && x == __float_as_int(st.floor)) { next = ch; break; }
         continue;
       }
-      if (left < 0.f) {                           // after a rejected draw
+      if (left < 0.f) {                           // after a rejected draw, or with little left
         float z = 0.f;
         sweep<kWalkThreads, 3>(prow, v0, v1, a.vec_p, [&](int v, const Raw8<T>& w) {
           if (!(max8(w) >= st.floor)) return;     // (none of them is kept)
@@ -1031,6 +1043,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         left = 0.f;
         for (uint32_t c = 0; c < kAsCluster; ++c) left += cl::peek(&sh.xf[e & 1], c);
         ++e;
+        least = kResum * left;
       }
       if (!(left > 0.f)) reset();                 // nothing left (rounding only): the target's own again
       const bool is_drawn = sh.flag[ch] & 1;
@@ -1042,6 +1055,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kWalkThread
         left = -1.f;
       } else if (x >= 0 && x < V && !(sh.flag[ch] & 2)) {
         left -= have;
+        if (!(left >= least)) left = -1.f;
         __syncthreads();                          // (every thread has read its flags)
         if (tid == 0) {
           sh.kills[kills] = x;

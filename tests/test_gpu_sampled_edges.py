@@ -69,3 +69,105 @@ def test_a_nucleus_of_many_small_tokens(tv, V, k, total, dtype):
     got = tv.accept_sampled(dev(np.full(B, -1, np.int32)), dev(np.zeros(B, np.int32)), p, dev(one), dev(np.zeros(B, np.float32)),
                             dev(race), top_k=dev(np.full(B, k, np.int32)), top_p=dev(top_p), max_nodes=1)
     assert np.array_equal(host(got[3]), want)
+
+
+def remainder_case(seed, top, dtype, B=96, V=1000, kids=6, T=1.0, **kw):
+    """Stars whose root gives its first child's token a probability near ``top``; that child is refused, those behind it
+    meet uniforms within 1e-4..1e-1 (relative) of what they are compared with.  All are proposals."""
+    c = Case(seed, [1 + kids] * B, V, "star", dtype="f32", q=None, T=[T], spread=1.0, **kw)
+    rng = np.random.default_rng(seed)
+    x = c.logits
+    if dtype == "bf16":
+        x = ok.f32(ok.bf16_bits(x))
+    for r in range(B):
+        a = c.off[r]
+        e = np.exp(x[a].astype(np.float64) / T)
+        first = int(rng.integers(0, V))
+        x[a, first] = T * np.log((e.sum() - e[first]) * top / (1 - top))
+        if dtype == "bf16":
+            x[a, first] = ok.f32(ok.bf16_bits(x[a, first:first + 1]))[0]
+        p = osm.target_probs(x[a], T, 0 if c.k is None else int(c.k[r]), 1.0 if c.p is None else float(c.p[r]))
+        others = np.setdiff1d(np.argsort(-p)[:60], [first])
+        c.tok[a + 1:a + 1 + kids] = [first, *rng.permutation(others)[:kids - 1]]
+        c.u[a + 1] = np.nextafter(np.float32(1), np.float32(0))
+        left = p.copy()
+        left[first] = 0.0
+        for i in range(a + 2, a + 1 + kids):
+            left /= left.sum()
+            t = c.tok[i]
+            # mostly above (refused, so that the next child is tried too)
+            side = 10.0 ** rng.uniform(-4, -1) * rng.choice([1, 1, 1, 1, -1])
+            c.u[i] = min(left[t] * (1 + side), 0.99)
+            left[t] = 0.0
+    c.logits = ok.bf16_bits(x) if dtype == "bf16" else x
+    return c
+
+
+def other_nuclei(c, r):
+    """Answers for request r where top-p at the root keeps as much within 40 2^-24 of the whole mass: the sums of at most
+    40 roundings each that it compares cannot tell these apart.  The tokens there hold 1e-8..1e-7 of the mass, and what is
+    left after the first child 1e-4, so one of them more or less moves p' by up to 1e-3."""
+    a, b = int(c.off[r]), int(c.off[r + 1])
+    T, k = 1.0 if c.T is None else float(c.T[r]), 0 if c.k is None else int(c.k[r])
+    x = ok.f32(c.logits[a:b]) if c.logits.dtype == np.uint16 else c.logits[a:b]
+    kept = np.stack([np.where(osm.target_probs(row, T, k, float(c.p[r])) > 0, row, -np.inf) for row in x])
+    p = osm.target_probs(x[0], T, k)
+    order = np.argsort(-p, kind="stable")
+    p = p[order]
+    for m in np.flatnonzero(np.abs(np.cumsum(p) - float(c.p[r])) <= 40 * 2.0 ** -24 + p) + 1:
+        kept[0] = -np.inf
+        kept[0, order[:m]] = x[0, order[:m]]
+        yield osm.verify(c.parent[a:b], c.tok[a:b], kept, [0, b - a], c.u[a:b], c.race[r:r + 1], c.depth, None, None, [T])[:4]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top,kw", [(0.9, {}), (0.999, {}), (0.9999, {}), (0.99997, {}), (0.999, dict(T=0.5)),
+                                    (0.999, dict(k=[300])), (0.9999, dict(k=[900], p=[0.99999])), (0.7, {})])
+def test_little_is_left_after_a_refused_proposal(tv, top, kw, dtype):
+    """Relative to one another the remaining probabilities are off by twice 30 2^-23 ln 2 for exponents up to 30, 2^-22 for
+    the exponential each, and the remainder's sum of at most 40 roundings by 40 2^-24 of itself, up to four times that
+    after further refusals: 5.0e-6 + 0.5e-6 + 9.6e-6 < 1.6e-5.  Decisions nearer than 2e-5 are left out; the inputs
+    have next to none."""
+    for B in (3, 96):                                # (in the second, rows out of reach are left out)
+        c = remainder_case(60, top, dtype, B=B, **kw)
+        got = c.run(tv)
+        want = osm.verify(c.parent, c.tok, c.logits, c.off, c.u, c.race, c.depth, None, None, c.T, c.k, c.p)
+        sure = want[4] > 2e-5
+        assert (~sure).mean() <= 0.05
+        same = np.all([(host(g) == w).reshape(B, -1).all(1) for g, w in zip(got, want[:4])], 0)
+        if c.p is not None:                          # (see other_nuclei)
+            for r in np.flatnonzero(sure & ~same):
+                same[r] = any(all(np.array_equal(host(g)[r], w[0]) for g, w in zip(got, o)) for o in other_nuclei(c, r))
+        assert same[sure].all()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(T=[0.5]), dict(k=[490])])
+def test_a_remainder_that_rounding_would_swallow(tv, kw):
+    """Proposals that leave a thousandth of what was left each time, down to 1e-9 of the target's mass: all are refused,
+    stay refused, and what is left decides.  Exponents reach 45, so 8e-6 + 0.5e-6 + 9.6e-6 < 2e-5 (as above)."""
+    V, B = 500, 64
+    for most in (B, 3):
+        c = Case(61, [7] * B, V, "star", dtype="f32", q=None, **kw)
+        T = 1.0 if c.T is None else float(c.T[0])
+        rng = np.random.default_rng(61)
+        for r in range(B):
+            a = c.off[r]
+            t = rng.permutation(V)[:6]
+            x = 0.3 * rng.standard_normal(V) - 21 - np.log(V)
+            x[t[:3]] = [0.0, -7.0, -14.0]
+            c.logits[a] = x * T
+            c.tok[a + 1:a + 7] = t
+            c.u[a + 1:a + 4] = np.nextafter(np.float32(1), np.float32(0))
+            c.u[a + 4:a + 7] = rng.random(3) * 0.005             # (the others hold 1 / 500 each)
+        n = int(c.off[most])
+        c.off = c.off[:most + 1]
+        for name in ("parent", "tok", "logits", "u"):
+            setattr(c, name, getattr(c, name)[:n])
+        for name in ("race", "T", "k"):
+            setattr(c, name, None if getattr(c, name) is None else getattr(c, name)[:most])
+        got = c.run(tv)
+        want = osm.verify(c.parent, c.tok, c.logits, c.off, c.u, c.race, c.depth, None, None, c.T, c.k)
+        sure = want[4] > 2e-5
+        assert (~sure).mean() <= 0.05 and (most == 3 or len(set(want[1].tolist())) > 2)
+        for g, w in zip(got, want[:4]):
+            assert np.array_equal(host(g)[sure], w[sure])
