@@ -323,8 +323,13 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
  * Outputs: as accept_rejection_sampling (accept_len -1, best_node -1, bonus -1
  *   for a request without nodes).
  * Workspace: accept_sampled_workspace_size(...) bytes, 16-byte aligned.
- * Arithmetic: fp32; a decision whose numbers lie
- *   within ~1e-6 (relative) of each other may differ from exact arithmetic.
+ * Arithmetic: fp32.  A decision whose numbers lie nearer to each other than
+ *   this may differ from exact arithmetic: p, and what is left of it after
+ *   refused proposals, are off by at most ~2e-5 of themselves; after refused
+ *   draws p'(x) is a difference, off by ~5e-6 (p(x) + p'(x)) / z, z the masses
+ *   that the refusals left multiplied together (small for a draft near the
+ *   target).  Masses that top-p compares are off by (200 + V / 2048) 2^-24 of
+ *   what top-k left, at most; logits are compared as they are.
  * -------------------------------------------------------------------------- */
 size_t accept_sampled_workspace_size(int B, int total_nodes, int V);
 int accept_sampled(const int32_t* parent, const int32_t* tok, const void* p_logits, int dtype, int V, int64_t ld,

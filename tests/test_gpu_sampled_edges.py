@@ -171,3 +171,55 @@ def test_a_remainder_that_rounding_would_swallow(tv, kw):
         assert (~sure).mean() <= 0.05 and (most == 3 or len(set(want[1].tolist())) > 2)
         for g, w in zip(got, want[:4]):
             assert np.array_equal(host(g)[sure], w[sure])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("noise", [0.1, 0.02, 0.005])
+def test_a_draft_near_the_target(tv, noise, dtype):
+    """Two draws from a q whose total variation to p is small, the first refused: what is left are differences, whose
+    numbers are off by 5e-6 (p + p') / z, z the masses that the refusals left multiplied together.  Every decision and
+    every last token lies on the side, or is a maximum, that this allows; most decisions allow one alone."""
+    B, V = 256, 2000
+    c = Case(70, [3] * B, V, "star", dtype="f32", q="drawn", spread=1.0)
+    rng = np.random.default_rng(70)
+    x = c.logits if dtype == "f32" else ok.f32(ok.bf16_bits(c.logits))
+    draft = x.astype(np.float64) + noise * rng.standard_normal(x.shape)
+    e = np.exp(draft - draft.max(1, keepdims=True))
+    c.q = (e / e.sum(1, keepdims=True)).astype(np.float32)
+    p = [osm.target_probs(x[c.off[r]]) for r in range(B)]
+    for r in range(B):
+        a = c.off[r]
+        q = c.q[a].astype(np.float64)
+        worse = np.flatnonzero(q > p[r] * (1 + noise / 4))
+        c.tok[a + 1] = rng.choice(worse)                             # drawn where q is above p: nothing of it is left
+        c.u[a + 1] = np.nextafter(np.float32(1), np.float32(0))
+        rest = np.maximum(0.0, p[r] - q)
+        ratio = rest / rest.sum() / q
+        c.tok[a + 2] = rng.choice(np.flatnonzero((ratio > 0.2) & (ratio < 0.9)))
+        t = c.tok[a + 2]
+        c.u[a + 2] = np.clip(ratio[t] * (1 + 10.0 ** rng.uniform(-3, 0) * rng.choice([-1, 1])), 0, 0.999)
+    c.logits = ok.bf16_bits(x) if dtype == "bf16" else x
+    acc, best, _, bonus = (host(t) for t in c.run(tv))
+    alone = 0
+    for r in range(B):
+        a = c.off[r]
+        q, t = c.q[a].astype(np.float64), int(c.tok[a + 2])
+        r1 = np.maximum(0.0, p[r] - q)
+        z = r1.sum()
+        r1 /= z
+        side = float(c.u[a + 2]) * q[t]
+        tol = 5e-6 * (p[r][t] + r1[t]) / z
+        yes = acc[r] == 1
+        assert acc[r] == 0 or best[r] == 2
+        if abs(side - r1[t]) > tol:
+            assert yes == (side < r1[t])
+            alone += 1
+        if not yes:
+            left = np.maximum(0.0, r1 - q)
+            z2 = left.sum()
+            left /= z2
+            slack = 5e-6 * (p[r] / z + left) / (z * z2)              # (p' before it: at most p / z)
+            f, s = left / c.race[r], slack / c.race[r]
+            v = int(bonus[r])
+            assert f[v] + s[v] >= (f - s).max()
+    assert alone > 0.6 * B and 0.2 * B < (acc == 1).sum() < 0.8 * B
