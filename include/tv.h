@@ -644,7 +644,8 @@ int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pa
  *   q [total_rows, ldq] dtype, Hq heads of d from the row's start, rotated as
  *           for the attention; lse float [total_rows, Hq]
  *   row_off, path, path_ld: the rows of each request, as in kv4_append (after
- *           an append: the accepted rows); max_rows bounds their number
+ *           an append: the accepted rows); max_rows bounds their number (a path
+ *           that goes on behind max_rows entries has more rows than that)
  *   causal  1: row j of a request sees its first old_len[r] + j + 1 cached
  *           tokens (the rows' own tokens follow old_len); 0: all of them
  *   vis_prefix int32 [total_rows] or NULL: a row sees at most the first

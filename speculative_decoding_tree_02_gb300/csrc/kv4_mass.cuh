@@ -50,6 +50,8 @@ __device__ __forceinline__ MassSpan mass_span(const MassArgs& a, int r, int* s_f
       }
     __syncthreads();
     s.count = *s_first;
+    s.bad |= s.count == a.max_rows && a.max_rows < a.path_ld &&
+             a.path[static_cast<int64_t>(r) * a.path_ld + a.max_rows] >= 0;
   } else {
     const int n = a.row_off[r + 1] - s.base;
     s.count = max(0, min(n, a.max_rows));

@@ -40,3 +40,23 @@ def test_mass_of_more_than_two_to_the_24_rows(tv, g, path):
     tol = tol + live.size * g * 2.0 ** -24 * want
     off = np.abs(host(out)[0] - want) > tol
     assert off.sum() == 0
+
+
+@pytest.mark.parametrize("rows", [4, 60])            # 16 and 240 per KV head: both bf16 kernels
+@pytest.mark.parametrize("bf16", [True, False])
+def test_mass_tells_of_a_path_beyond_max_rows(tv, rows, bf16):
+    """Accepted rows behind the first max_rows are left out, and *err says so; a path that ends there is whole."""
+    m = Mass(11, [90, 70], [rows, rows], 8, 2, 64, 16, bf16, path=True)
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 0 and m.path[0, rows] == -1
+    m.max_rows = rows - 1
+    out, err = m.run(tv)
+    assert int(err) == 1
+    m.check(out)
+    m.path[:, rows - 1] = -1                             # the same rows without the entry that was left out
+    again, err = m.run(tv)
+    assert int(err) == 0 and torch.equal(out, again)
+    m.path = m.path[:, :rows - 1].copy()                 # no column behind max_rows
+    again, err = m.run(tv)
+    assert int(err) == 0 and torch.equal(out, again)
