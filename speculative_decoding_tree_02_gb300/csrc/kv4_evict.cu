@@ -445,7 +445,7 @@ TV_API int kv4_evict_select(const float* score, int64_t score_ld, const int32_t*
   if (B == 0) return TV_OK;
   if (!cache_len || !budget || !new_len || new_len == cache_len || new_len == budget) return TV_EINVAL;
   if ((max_len > 0 && !score) || (idx_ld > 0 && !idx)) return TV_EINVAL;
-  if (score_out == score && score_out_ld != score_ld) return TV_EINVAL;
+  if (score_out && score_out == score && score_out_ld != score_ld) return TV_EINVAL;
   const int c = select_cluster(max_len), slice = ((max_len + c - 1) / c + 3) / 4 * 4;
   const int bytes = std::max(slice, 4) * 4;
   if (bytes > 24 << 10 && !smem_limit(kv4::select_kernel<512>, kMaxSlice * 4)) return TV_ECUDA;

@@ -382,7 +382,7 @@ TV_API int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype
     return TV_EUNSUPPORTED;
   if (!(scale > 0.f) || scale > 3.402823466e38f || !(decay >= 0.f && decay <= 1.f)) return TV_EINVAL;
   if (score_out_ld < max_len || (score_in && score_in_ld < max_len)) return TV_EINVAL;
-  if (score_in == score_out && score_in_ld != score_out_ld) return TV_EINVAL;
+  if (score_in && score_in == score_out && score_in_ld != score_out_ld) return TV_EINVAL;
   if (B == 0 || max_len == 0) return TV_OK;
   if (!cache_len || !row_off || !score_out || (causal && !old_len) || (path && path_ld <= 0)) return TV_EINVAL;
   if (table_ld > 0 && !block_table) return TV_EINVAL;

@@ -1,0 +1,29 @@
+"""CPU checks of what the entry points of eviction and sampled verification answer before any launch, at the edges."""
+import pytest
+
+from test_oracle_evict_sampled import COMPACT, MASS, SAMPLED, SELECT, call, lib  # noqa: F401
+
+NOTHING = {k: None for k in ("q", "lse", "cache", "table", "cache_len", "row_off", "old", "s_in", "s_out")}
+
+
+@pytest.mark.parametrize("fn,base,change", [
+    ("kv4_attn_mass", MASS, dict(B=0, rows=0, in_ld=0, **NOTHING)),               # no scores before: two absent arrays
+    ("kv4_attn_mass", MASS, dict(B=0, rows=0, in_ld=80, out_ld=64, **NOTHING)),   # empty scores of two widths
+    ("kv4_attn_mass", MASS, dict(max_len=0, in_ld=0, s_in=None, s_out=None)),
+    ("kv4_evict_select", SELECT, dict(B=0, score=None, cache_len=None, budget=None, idx=None, out=None, new_len=None)),
+    ("kv4_compact", COMPACT, dict(B=0, cache=None, table=None, cache_len=None, idx=None, new_len=None)),
+    ("accept_sampled", SAMPLED, dict(B=0, rows=0, parent=None, tok=None, p=None, q=None, ldq=0, node_off=None, u=None, race=None,
+                                     acc=None, best=None, path=None, bonus=None, ws=None, ws_bytes=0)),
+])
+def test_an_empty_batch_is_no_error(lib, fn, base, change):  # noqa: F811
+    assert call(lib, fn, base, **change) == 0
+
+
+def test_one_array_of_two_widths_is_refused(lib):  # noqa: F811
+    assert call(lib, "kv4_attn_mass", MASS, in_ld=80, out_ld=64) == -1
+    assert call(lib, "kv4_evict_select", SELECT, out=SELECT["score"], ld=64, out_ld=80) == -1
+
+
+def test_choice_without_scores_of_no_tokens(lib):  # noqa: F811
+    """No token, no scores and none wanted: nothing to refuse (without a device the launch is what fails)."""
+    assert call(lib, "kv4_evict_select", SELECT, max_len=0, score=None, ld=0, out=None, out_ld=32) != -1

@@ -60,3 +60,28 @@ def test_mass_tells_of_a_path_beyond_max_rows(tv, rows, bf16):
     m.path = m.path[:, :rows - 1].copy()                 # no column behind max_rows
     again, err = m.run(tv)
     assert int(err) == 0 and torch.equal(out, again)
+
+
+def test_empty_batches(tv):
+    """No request: all four operators return empty outputs and no error."""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = tv.kv4_new_cache(3, 16, 2, 64)
+    q, lse = torch.zeros(0, 4, 64, device="cuda"), torch.zeros(0, 4, device="cuda")
+    score = torch.zeros(0, 2, 40, device="cuda")
+    for kw in (dict(score=score), dict(max_len=40), dict(score=score, score_out=torch.zeros(0, 2, 48, device="cuda"))):
+        out, err = tv.kv4_attn_mass(q, lse, cache, 16, z(0, 3), z(0), z(1), 4, old_len=z(0), **kw)
+        assert out.shape[0] == 0 and int(err) == 0
+    idx, kept, new_len, err = tv.kv4_evict_select(score, z(0), z(0), 40, max_keep=8)
+    assert idx.shape == (0, 2, 8) and kept.shape == (0, 2, 8) and new_len.numel() == 0 and int(err) == 0
+    assert int(tv.kv4_compact(cache, 16, z(0, 3), z(0), idx, new_len, 8)) == 0
+    outs = tv.accept_sampled(z(0), z(0), torch.zeros(0, 50, device="cuda"), z(1), torch.zeros(0, device="cuda"),
+                             torch.zeros(0, 50, device="cuda"), max_nodes=4)
+    assert [t.numel() for t in outs] == [0, 0, 0, 0]
+
+
+def test_requests_without_tokens(tv):
+    """Two requests that hold nothing, with and without room for scores."""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for room in (0, 7):
+        idx, kept, new_len, err = tv.kv4_evict_select(torch.zeros(2, 3, room, device="cuda"), z(2), z(2) + 5, room, 1, 1, max_keep=4)
+        assert bool((idx == -1).all()) and new_len.tolist() == [0, 0] and int(err) == 0
