@@ -549,6 +549,16 @@ def _table(t, B: int, dev: int, name="block_table"):
     return _dense(t, name, torch.int32, dev, (B, cols)), cols
 
 
+def _given_table(t, B: int, dev: int, name: str):
+    """The same of a table that may be left out; (None, 0) for None.  The library tells by the address whether there is
+    one, which a table without columns does not have."""
+    if t is None:
+        return None, 0
+    if t.dim() == 2 and t.shape[1] == 0:
+        raise ValueError(f"{name} has no columns")
+    return _table(t, B, dev, name)
+
+
 def tv_rope(q, k, pos, rope, interleaved=False, outputs=None, err=None):
     """Rotates q [n, Hq, d] and k [n, Hkv, d] (or None) at ``pos`` int32 [n] with the table ``rope`` float32
     [max_pos, rot_dim] (cosines, then sines).  Row strides are free.  Returns q_out, k_out, err."""
@@ -597,7 +607,7 @@ def kv4_append(k, v, cache, page_size, block_table, cache_len, row_off, max_new,
     table, max_pos, rot = _rope_args(rope, dev)
     i32 = torch.int32
     _call_on(dev, "kv4_append", pk, ldk, pv, ldv, dt, n, _dense(row_off, "row_off", i32, dev, (B + 1,)),
-             *(_table(path, B, dev, "path") if path is not None else (None, 0)), B, max_new,
+             *_given_table(path, B, dev, "path"), B, max_new,
              _dense(pos, "pos", i32, dev, (n,)), table, max_pos, rot, int(interleaved), cache.data_ptr(), n_pages,
              page_size, *_table(block_table, B, dev),
              _dense(cache_len, "cache_len", i32, dev, (B,)), Hkv, d, _dense(new_len, "new_len", i32, dev, (B,)), perr)
@@ -676,12 +686,15 @@ def tree_verify_attn_kv4(q, cache, page_size, block_table, cache_len, k_tree, v_
 
 
 # ------------------------------------------------- eviction from the 4-bit cache
-def _scores(t: Optional[torch.Tensor], name: str, dev: int, B: int, H: int):
-    """(address, columns) of float32 [B, H, columns] scores; (None, 0) for None."""
+def _scores(t: Optional[torch.Tensor], name: str, dev: int, B: int, H: int, need: int = 0):
+    """(address, columns) of float32 [B, H, columns] scores; (None, 0) for None.  Where ``need`` columns are to be read
+    or written, none at all would pass for None."""
     if t is None:
         return None, 0
     if t.dim() != 3:
         raise ValueError(f"{name} must be [{B}, {H}, columns]")
+    if t.shape[2] == 0 and need > 0:
+        raise ValueError(f"{name} has no columns")
     return _dense(t, name, torch.float32, dev, (B, H, t.shape[2])), t.shape[2]
 
 
@@ -706,7 +719,7 @@ def kv4_attn_mass(q, lse, cache, page_size, block_table, cache_len, row_off, max
         scale = 1.0 / d ** 0.5
     pq, ldq = _rows(q, "q", q.dtype, dev, n, Hq, d)
     table, cols = _table(block_table, B, dev)
-    pin, ld_in = _scores(score, "score", dev, B, Hkv)
+    pin, ld_in = _scores(score, "score", dev, B, Hkv, max_len or 0)
     if score_out is None:
         if score is None and max_len is None:
             raise ValueError("kv4_attn_mass needs score, score_out or max_len")
@@ -721,7 +734,7 @@ def kv4_attn_mass(q, lse, cache, page_size, block_table, cache_len, row_off, max
     _call_on(dev, "kv4_attn_mass", pq, ldq, _dense(lse, "lse", torch.float32, dev, (n, Hq)), dt, cache.data_ptr(), n_pages,
              page_size, table, cols, _dense(cache_len, "cache_len", i32, dev, (B,)),
              _dense(row_off, "row_off", i32, dev, (B + 1,)),
-             *(_table(path, B, dev, "path") if path is not None else (None, 0)),
+             *_given_table(path, B, dev, "path"),
              _dense(vis_prefix, "vis_prefix", i32, dev, (n,)), _dense(old_len, "old_len", i32, dev, (B,)), int(causal), B,
              max_rows, n, max_len, Hq, Hkv, d, float(scale), float(decay), pin, ld_in, pout, ld_out, perr)
     return score_out, err
@@ -742,7 +755,7 @@ def kv4_evict_select(score, cache_len, budget, max_len, n_sink=0, n_recent=0, ma
     pidx = _dense(idx, "idx", i32, dev, (B, H, idx.shape[-1]))
     if score_out is None:
         score_out = torch.empty((B, H, idx.shape[2]), dtype=torch.float32, device=score.device)
-    pout, ld_out = _scores(score_out, "score_out", dev, B, H)
+    pout, ld_out = _scores(score_out, "score_out", dev, B, H, min(idx.shape[2], max_len))
     if new_len is None:
         new_len = torch.empty(B, dtype=i32, device=score.device)
     err, perr = _new_err(err, score)
@@ -763,7 +776,7 @@ def kv4_compact(cache, page_size, block_table, cache_len, idx, new_len, max_keep
     err, perr = _new_err(err, cache)
     i32 = torch.int32
     table, cols = _table(block_table, B, dev)
-    dst, dst_cols = _table(dst_table, B, dev, "dst_table") if dst_table is not None else (None, 0)
+    dst, dst_cols = _given_table(dst_table, B, dev, "dst_table")
     _call_on(dev, "kv4_compact", cache.data_ptr(), n_pages, page_size, table, cols,
              _dense(cache_len, "cache_len", i32, dev, (B,)), _dense(idx, "idx", i32, dev, (B, Hkv, idx.shape[2])),
              idx.shape[2], _dense(new_len, "new_len", i32, dev, (B,)), B, max_keep, dst, dst_cols, Hkv, d, perr)

@@ -27,3 +27,30 @@ def test_one_array_of_two_widths_is_refused(lib):  # noqa: F811
 def test_choice_without_scores_of_no_tokens(lib):  # noqa: F811
     """No token, no scores and none wanted: nothing to refuse (without a device the launch is what fails)."""
     assert call(lib, "kv4_evict_select", SELECT, max_len=0, score=None, ld=0, out=None, out_ld=32) != -1
+
+
+def test_binding_refuses_tables_without_columns(lib):  # noqa: F811
+    """An empty tensor has no address, and none means something else: all rows, in place, no scores."""
+    import torch
+
+    import speculative_decoding_tree_02_gb300 as tv
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    cache, q = torch.zeros(2, 1, 16 * 68, dtype=torch.uint8), torch.zeros(3, 2, 64)
+    score = torch.zeros(1, 1, 32)
+    mass = (q, torch.zeros(3, 2), cache, 16, z(1, 2), z(1), z(2), 3)
+    with pytest.raises(ValueError, match="path has no columns"):
+        tv.kv4_attn_mass(*mass, score=score, path=z(1, 0))
+    with pytest.raises(ValueError, match="path has no columns"):
+        tv.kv4_append(q[:, :1], q[:, :1], cache, 16, z(1, 2), z(1), z(2), 3, path=z(1, 0))
+    with pytest.raises(ValueError, match="dst_table has no columns"):
+        tv.kv4_compact(cache, 16, z(1, 2), z(1), z(1, 1, 4), z(1), 4, dst_table=z(1, 0))
+    with pytest.raises(ValueError, match="score has no columns"):
+        tv.kv4_attn_mass(*mass, score=score[:, :, :0], max_len=8, score_out=score)
+    with pytest.raises(ValueError, match="score_out has no columns"):
+        tv.kv4_evict_select(score, z(1), z(1), 32, max_keep=4, score_out=score[:, :, :0])
+    with pytest.raises(ValueError, match="takes device tensors"):                       # (the calls themselves are in order)
+        tv.kv4_attn_mass(*mass, score=score, path=z(1, 2))
+    with pytest.raises(ValueError, match="takes device tensors"):
+        tv.kv4_compact(cache, 16, z(1, 2), z(1), z(1, 1, 4), z(1), 4, dst_table=z(1, 1))
+    with pytest.raises(ValueError, match="takes device tensors"):
+        tv.kv4_evict_select(score, z(1), z(1), 32, max_keep=4, score_out=score)
