@@ -9,6 +9,7 @@ from test_gpu_evict import Mass
 from test_gpu_kv4 import prefixes, random_pool, tables
 
 pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.mark.parametrize("g,path", [(1, False), (3, True)])
@@ -85,3 +86,72 @@ def test_requests_without_tokens(tv):
     for room in (0, 7):
         idx, kept, new_len, err = tv.kv4_evict_select(torch.zeros(2, 3, room, device="cuda"), z(2), z(2) + 5, room, 1, 1, max_keep=4)
         assert bool((idx == -1).all()) and new_len.tolist() == [0, 0] and int(err) == 0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("rows,g,path", [(120, 4, False), (50, 4, True), (520, 1, False), (90, 7, True)])
+def test_mass_of_many_rows_with_nan(tv, rows, g, path, d, P, bf16):
+    """More than 192 rows per KV head, split over the CTAs of a cluster: NaN keys, lse and rows reach only what sees them."""
+    H, L = 2, 700
+    m = Mass(rows + d, [L], [rows], g * H, H, d, P, bf16, path=path, causal=False, vis=True)
+    src = m.path[0, :rows] if path else np.arange(rows)
+    m.vis[:] = m.rng.integers(0, 600, m.vis.size)
+    a, b, c, e = (int(src[i]) for i in (rows // 5, rows // 3, rows // 2, rows - 1))
+    m.vis[[a, b, c, e]] = [L, 60, 0, 130]
+    m.lse[[a, b, c, e]] = 2.0
+    m.lse[c] = NAN                                       # sees nothing
+    page, slot = m.table[0, 650 // P], 650 % P           # a key whose scale is NaN, seen by row a alone
+    cache, kn, ks, vn, vs = m.pool
+    cache[page, 1, P * d + 2 * slot:P * d + 2 * slot + 2] = [0xC0, 0x7F]
+    ks[page, 1, slot] = NAN
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 0 and bool(out[0, 1, 650].isnan()) and int(out.isnan().sum()) == 1
+    m.lse[b, g] = NAN                                    # of KV head 1
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 0 and int(out.isnan().sum()) == 61 and bool(out[0, 1, :60].isnan().all())
+    m.q[e, 0], m.hq[e, 0] = NAN, NAN                     # a row of KV head 0
+    out, _ = m.run(tv)
+    m.check(out)
+    assert int(out[0, 0].isnan().sum()) == 130
+    m.lse[e, 0] = -INF                                   # which now saw nothing, it is said
+    out, _ = m.run(tv)
+    m.check(out)
+    assert not bool(out[0, 0].isnan().any())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows,g", [(120, 4), (600, 1), (60, 6)])
+def test_mass_of_many_rows_with_bad_pages_and_rows(tv, rows, g, bf16):
+    """More than 192 rows per KV head: bad page entries, rows outside the tensor, lengths and rows beyond their bounds."""
+    H, lens = 2, [600, 333]
+    m = Mass(rows, lens, [rows, rows - 7], g * H, H, 64, 32, bf16, causal=False)
+    m.table[0, 3], m.table[0, 17], m.table[1, 0] = -1, 10 ** 6, m.pool[0].shape[0]
+    m.page_ok = [~np.isin(np.arange(600) // 32, [3, 17]), np.arange(333) // 32 != 0]
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 1
+    # rows outside the tensor, at both ends and in the middle of a path
+    m = Mass(rows + 1, lens, [rows, rows - 7], g * H, H, 64, 32, bf16, path=True, causal=True)
+    n = m.lse.shape[0]
+    m.path[0, [0, rows // 2, rows - 1]] = [n, 2 ** 31 - 1, n + 5]
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 1
+    # an offset that begins before the tensor
+    m = Mass(rows + 2, lens, [rows, rows - 7], g * H, H, 64, 32, bf16, causal=False)
+    m.off = m.off - 3
+    out, err = m.run(tv)
+    m.check(out)
+    assert int(err) == 1
+    # rows past max_rows, tokens past max_len
+    m = Mass(rows + 3, lens, [rows, rows - 7], g * H, H, 64, 32, bf16, causal=False)
+    m.max_rows = rows - 9
+    out, err = m.run(tv)
+    assert int(err) == 1
+    m.check(out)
+    before = torch.full((2, H, m.cols), 9.0, device="cuda")
+    out, err = m.run(tv, max_len=301, score_out=before.clone())
+    assert int(err) == 1 and bool((out[:, :, 301:] == 9).all())
