@@ -692,7 +692,7 @@ int kv4_evict_select(const float* score, int64_t score_ld, const int32_t* cache_
 /* --------------------------------------------------------------------------
  * kv4_compact — moves token idx[r,h,j] of each head to token j, j < new_len[r]:
  * codes and scales as they are.
- *   idx int32 [B, Hkv, idx_ld]: ascending in each row, as kv4_evict_select
+ *   idx int32 [B, Hkv, idx_ld]: ascending in each row, no token twice, as kv4_evict_select
  *           gives it; max_keep <= idx_ld bounds new_len (launch geometry)
  *   dst_table int32 [B, dst_ld] or NULL.  NULL (or block_table): in place, on the
  *           request's own pages (no two requests share one).  Else the tokens go to these

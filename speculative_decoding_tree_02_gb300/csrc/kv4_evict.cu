@@ -471,7 +471,8 @@ TV_API int kv4_compact(void* cache, int n_pages, int page_size, const int32_t* b
     return TV_EUNSUPPORTED;
   if (max_keep > idx_ld) return TV_EINVAL;
   if (B == 0 || max_keep == 0) return TV_OK;
-  if (!cache || !block_table || !cache_len || !idx || !new_len || !aligned(cache, 16)) return TV_EINVAL;
+  if ((n_pages > 0 && !cache) || (table_ld > 0 && !block_table) || !cache_len || !idx || !new_len || !aligned(cache, 16))
+    return TV_EINVAL;
   if (dst_table == block_table) dst_table = nullptr;    // in place
   const kv4::CompactArgs a{static_cast<uint8_t*>(cache), block_table, dst_table, cache_len, new_len, idx, err, idx_ld,
                            n_pages, page_size, table_ld, dst_ld, Hkv, max_keep};

@@ -54,3 +54,9 @@ def test_binding_refuses_tables_without_columns(lib):  # noqa: F811
         tv.kv4_compact(cache, 16, z(1, 2), z(1), z(1, 1, 4), z(1), 4, dst_table=z(1, 1))
     with pytest.raises(ValueError, match="takes device tensors"):
         tv.kv4_evict_select(score, z(1), z(1), 32, max_keep=4, score_out=score)
+
+
+@pytest.mark.parametrize("change", [dict(table=None, table_ld=0), dict(cache=None, n_pages=0)])
+def test_move_without_pages_or_columns(lib, change):  # noqa: F811
+    """A table of no columns, a cache of no pages: nothing to refuse (without a device the launch is what fails)."""
+    assert call(lib, "kv4_compact", COMPACT, **change) != -1

@@ -155,3 +155,14 @@ def test_mass_of_many_rows_with_bad_pages_and_rows(tv, rows, g, bf16):
     before = torch.full((2, H, m.cols), 9.0, device="cuda")
     out, err = m.run(tv, max_len=301, score_out=before.clone())
     assert int(err) == 1 and bool((out[:, :, 301:] == 9).all())
+
+
+@pytest.mark.parametrize("pages,cols", [(3, 0), (0, 2)])
+def test_move_without_pages_or_columns(tv, pages, cols):
+    """Requests that hold nothing, over a table of no columns or a cache of no pages; a token to be kept is an error."""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = torch.full((pages, 2, 16 * 68), 7, dtype=torch.uint8, device="cuda")
+    for dst in (None, z(2, 3)):
+        assert int(tv.kv4_compact(cache, 16, z(2, cols), z(2), z(2, 2, 4), z(2), 4, dst_table=dst)) == 0
+        assert int(tv.kv4_compact(cache, 16, z(2, cols), z(2) + 5, z(2, 2, 4), z(2) + 1, 4, dst_table=dst)) == 1
+    assert bool((cache == 7).all())
