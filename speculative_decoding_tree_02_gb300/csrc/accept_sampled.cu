@@ -562,7 +562,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
           }
           if (!__any_sync(0xffffffffu, m8 >= lo) || cnt > kList) continue;
           uint32_t in = 0;
-          if (m8 >= lo) {
+          if (v < n && m8 >= lo) {                // (lo may be -inf, as m8 is behind the slice)
             widen8(raw, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) in |= (x[j] >= lo && x[j] <= hi ? 1u : 0u) << j;

@@ -223,3 +223,43 @@ def test_a_draft_near_the_target(tv, noise, dtype):
             v = int(bonus[r])
             assert f[v] + s[v] >= (f - s).max()
     assert alone > 0.6 * B and 0.2 * B < (acc == 1).sum() < 0.8 * B
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k,top_p,masked", [(3100, 3000, 1.0, 0.0), (4347, 3000, 1.0, 0.3), (4347, 3000, 0.99, 0.3),
+                                              (5700, 0, 0.9999, 0.0), (20000, 19000, 1.0, 0.0), (151936, 150000, 1.0, 0.0),
+                                              (9000, 0, 0.99999, 0.5), (700, 690, 1.0, 0.0)])
+def test_a_threshold_below_a_65536th_of_the_highest(tv, V, k, top_p, masked, dtype):
+    """Truncations that end far below the highest logit, positive and negative logits around them.  As above, one token of
+    each request is favoured by race; its class lies away from the border."""
+    B = 24
+    rng = np.random.default_rng(V)
+    x = (3 * rng.standard_normal((B, V)) + rng.uniform(-3, 9, (B, 1))).astype(np.float32)
+    x[np.arange(B), rng.integers(0, V, B)] = x.max(1) + 3
+    x[rng.random(x.shape) < masked] = -np.inf
+    if dtype == "bf16":
+        x = ok.f32(ok.bf16_bits(x))
+    race, want, probes = np.ones((B, V), np.float32), np.zeros(B, np.int64), np.zeros(B, bool)
+    for r in range(B):
+        p = osm.target_probs(x[r], 1.0, k)
+        value, group = np.unique(p, return_inverse=True)
+        mass = np.bincount(group, weights=p)
+        off = ((mass.sum() - np.cumsum(mass)) - float(np.float32(top_p)))[group] if top_p < 1 else np.where(p > 0, -1.0, 1.0)
+        sure = (np.abs(off) > (100 + V / 2048) * 2.0 ** -24) & np.isfinite(x[r])
+        kept = sure & (off < 0)
+        # near the border on either side, where the last ones kept or the first ones left out are
+        order = np.argsort(-x[r], kind="stable")
+        pool = order[kept[order]][-40:] if r % 2 else order[(sure & (off > 0))[order]][:40]
+        if pool.size == 0:
+            pool = order[kept[order]][-40:]
+        t = int(rng.choice(pool))
+        race[r, t] = 1e-30
+        probes[r] = kept[t]
+        q = osm.target_probs(x[r], 1.0, k, float(np.float32(top_p)))
+        want[r] = t if kept[t] else int(np.argmax(q))
+    assert probes.any()
+    one = np.arange(B + 1, dtype=np.int32)
+    p = dev(ok.bf16_bits(x)).view(torch.bfloat16) if dtype == "bf16" else dev(x)
+    got = tv.accept_sampled(dev(np.full(B, -1, np.int32)), dev(np.zeros(B, np.int32)), p, dev(one), dev(np.zeros(B, np.float32)),
+                            dev(race), top_k=dev(np.full(B, k, np.int32)), top_p=dev(np.full(B, top_p, np.float32)), max_nodes=1)
+    assert np.array_equal(host(got[3]), want)
