@@ -628,7 +628,7 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
       auto settle = [&](int cnt, int left, float above, float target, float share) {
         constexpr int kOwn = kCompare / kAsThreads;
         float* ws = hist + kCompare;                 // weights
-        const int pad = (cnt + 3) / 4 * 4;
+        const int pad = (cnt + 31) / 32 * 32;
         for (int q = tid; q < pad; q += kAsThreads) {
           if (q >= cnt) hist[q] = -INFINITY;
           ws[q] = q < cnt ? weight(hist[q]) : 0.f;
@@ -646,15 +646,16 @@ __global__ void __cluster_dims__(kAsCluster, 1, 1) __launch_bounds__(kAsThreads,
           if (u * kAsThreads + 32 * warp < cnt) { // (for the warp as a whole)
             // (sums of 32 at a time: one sum of all would lose the small weights behind a large one)
             for (int j0 = 0; j0 < pad; j0 += 32) {
-              float part = 0.f;
-              for (int j = j0; j < min(j0 + 32, pad); j += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(hist + j), w = *reinterpret_cast<const float4*>(ws + j);
-                if (l.x > own[u]) { ++more; part += w.x; }
-                if (l.y > own[u]) { ++more; part += w.y; }
-                if (l.z > own[u]) { ++more; part += w.z; }
-                if (l.w > own[u]) { ++more; part += w.w; }
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(hist + j0 + j), w = *reinterpret_cast<const float4*>(ws + j0 + j);
+                if (l.x > own[u]) { ++more; part[0] += w.x; }
+                if (l.y > own[u]) { ++more; part[1] += w.y; }
+                if (l.z > own[u]) { ++more; part[2] += w.z; }
+                if (l.w > own[u]) { ++more; part[3] += w.w; }
               }
-              mine[u] += part;
+              mine[u] += (part[0] + part[1]) + (part[2] + part[3]);
             }
           }
           keep[u] = q < cnt && (left == 0 || more < left);
