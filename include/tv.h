@@ -328,7 +328,7 @@ int accept_rejection_sampling(const int32_t* parent, const int32_t* tok, const v
  *   refused proposals, are off by at most ~2e-5 of themselves; after refused
  *   draws p'(x) is a difference, off by ~5e-6 (p(x) + p'(x)) / z, z the masses
  *   that the refusals left multiplied together (small for a draft near the
- *   target).  Masses that top-p compares are off by (200 + V / 2048) 2^-24 of
+ *   target; z is also how likely draws from q are to be refused).  Masses that top-p compares are off by (200 + V / 2048) 2^-24 of
  *   what top-k left, at most; logits are compared as they are.
  * -------------------------------------------------------------------------- */
 size_t accept_sampled_workspace_size(int B, int total_nodes, int V);
@@ -661,7 +661,9 @@ int tree_verify_attn_kv4(const void* q, int64_t ldq, const void* cache, int n_pa
  * A row with lse = -inf (it saw nothing) weighs nothing; a NaN row makes the
  * tokens that it sees NaN.  A token with a bad page entry gets no weight, a row
  * outside [0, total_rows) gives none, tokens beyond max_len or the table and
- * rows beyond max_rows are left out: each writes 1 to *err.  A device-side wait
+ * rows beyond max_rows are left out: each writes 1 to *err (the rows of a
+ * request without cached tokens are not looked at, and with max_len 0 the call
+ * does nothing).  A device-side wait
  * that ran out (2 s) makes the tokens concerned NaN, and 1 is written to *err.
  * -------------------------------------------------------------------------- */
 int kv4_attn_mass(const void* q, int64_t ldq, const float* lse, int dtype, const void* cache, int n_pages,
@@ -700,7 +702,8 @@ int kv4_evict_select(const float* score, int64_t score_ld, const int32_t* cache_
  * Other tokens of the destination keep what they hold (in place: those from
  * new_len on).  A token whose index is outside [0, cache_len[r]) or whose
  * source or destination page is bad is not moved, and 1 is written to *err; so
- * it is for a new_len outside [0, max_keep] (clamped).
+ * it is for a new_len outside [0, max_keep] (clamped).  With max_keep 0 the
+ * call does nothing.
  * -------------------------------------------------------------------------- */
 int kv4_compact(void* cache, int n_pages, int page_size, const int32_t* block_table, int table_ld,
                 const int32_t* cache_len, const int32_t* idx, int64_t idx_ld, const int32_t* new_len, int B, int max_keep,

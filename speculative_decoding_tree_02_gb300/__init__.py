@@ -703,9 +703,9 @@ def kv4_attn_mass(q, lse, cache, page_size, block_table, cache_len, row_off, max
                   err=None):
     """Adds to ``score`` float32 [B, Hkv, columns] (None: zeros) the attention weight that the cached tokens received
     from rows of q [n, Hq, d] (row stride free) whose attention gave ``lse`` float32 [n, Hq].  ``path`` int32 [B, m]
-    picks rows as in kv4_append; ``causal``: row j sees old_len + j + 1 cached tokens.  ``max_len`` bounds cache_len
-    (default: what the scores and the table have room for; a tight bound saves empty CTAs).  ``score_out`` may be
-    ``score``.  Returns score_out, err."""
+    picks rows as in kv4_append, ``max_rows`` of a request at most; ``causal``: row j sees old_len + j + 1 cached tokens.
+    ``max_len`` bounds cache_len (default: what the scores and the table have room for; a tight bound saves empty CTAs).
+    ``score_out`` may be ``score``.  Returns score_out, err."""
     dev = q.get_device()
     n, Hq, d = q.shape
     n_pages, Hkv, dc = _cache_geometry(cache, page_size)
@@ -808,8 +808,10 @@ def accept_sampled(parent, tok, p_logits, node_off, u_node, race, q_prob=None, d
     """Verifies drafted tokens against the target's distribution at each request's ``temperature`` float32 [B], ``top_k``
     int32 [B] and ``top_p`` float32 [B].  p_logits [n, V] (row stride free); ``q_prob`` float32 [n, V]: what a node's
     drawn children came from; ``drawn`` uint8 [n] (None: all, if q_prob is given); ``u_node`` float32 [n] uniforms;
-    ``race`` float32 [B, V] exponential variates.  Returns accept_len, best_node int32 [B], path int32
-    [B, max_depth + 1], bonus int32 [B]."""
+    ``race`` float32 [B, V] exponential variates.  ``max_nodes`` bounds a request's nodes (default: as many as there are
+    in all, 1024 at most; further ones are left out; give the tightest, as B * max_nodes clusters are launched: 64 chains
+    of 16 take 105 us with 16, 650 without), ``max_depth`` the accepted ones (default: max_nodes - 1).  Returns accept_len, best_node int32 [B], path
+    int32 [B, max_depth + 1], bonus int32 [B]."""
     n, V = p_logits.shape
     dev = p_logits.get_device()
     dt = _act_dtype(p_logits, "p_logits")

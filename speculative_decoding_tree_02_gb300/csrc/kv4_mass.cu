@@ -148,9 +148,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool some) {
 // walks over tiles of 32 tokens, the next tile's codes on their way
 // while it works on one.
 
-// 64 requests over 512..4096 tokens, 8 heads of 128: 4 rows per head 31.4 us (42%
+// 64 requests over 512..4096 tokens, 8 heads of 128: 4 rows per head 31.1 us (42%
 // of the measured copy rate for 66 bytes a token and head and the scores), 4..64
-// rows 59.7 us; bound by issue slots (550 instructions per tile, 176 of them the
+// rows 59.5 us; bound by issue slots (550 instructions per tile, 176 of them the
 // codes), then by the rate of mma.sync (16 for eight rows; more
 // chains side by side made no difference).
 template <int D>
