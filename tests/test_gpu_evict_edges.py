@@ -166,3 +166,34 @@ def test_move_without_pages_or_columns(tv, pages, cols):
         assert int(tv.kv4_compact(cache, 16, z(2, cols), z(2), z(2, 2, 4), z(2), 4, dst_table=dst)) == 0
         assert int(tv.kv4_compact(cache, 16, z(2, cols), z(2) + 5, z(2, 2, 4), z(2) + 1, 4, dst_table=dst)) == 1
     assert bool((cache == 7).all())
+
+
+def test_the_largest_batches(tv):
+    """65535 requests through the weights, the choice and the move: as the same requests in batches of 8192."""
+    B, H, P, d = 65535, 1, 16, 64
+    rng = np.random.default_rng(90)
+    lens = rng.integers(0, 17, B).astype(np.int32)
+    cache = torch.from_numpy(rng.integers(0, 256, (B, H, P * (d + 4)), dtype=np.uint8)).cuda()
+    scales = torch.rand((B, H, 2 * P), device="cuda") * 0.2 + 0.2
+    cache[:, :, P * d:] = scales.to(torch.bfloat16).view(torch.uint8)
+    table = np.stack([rng.permutation(B)], 1).astype(np.int32)
+    budget = rng.integers(0, 12, B).astype(np.int32)
+    lse = (3 + rng.random((B, 2))).astype(np.float32)
+    for bf16 in (True, False):
+        q = torch.from_numpy(rng.standard_normal((B, 2, d)).astype(np.float32)).cuda().to(torch.bfloat16 if bf16 else torch.float32)
+
+        def run(b0, b1, pool):
+            n = b1 - b0
+            off = dev(np.arange(n + 1, dtype=np.int32))
+            s, e = tv.kv4_attn_mass(q[b0:b1], dev(lse[b0:b1]), pool, P, dev(table[b0:b1]), dev(lens[b0:b1]), off, 1, max_len=16)
+            idx, kept, new, _ = tv.kv4_evict_select(s, dev(lens[b0:b1]), dev(budget[b0:b1]), 16, 1, 1, max_keep=12, err=e)
+            tv.kv4_compact(pool, P, dev(table[b0:b1]), dev(lens[b0:b1]), idx, new, 12, err=e)
+            assert int(e) == 0
+            return s, idx, torch.where(idx >= 0, kept, torch.zeros_like(kept)), new
+        a, b = cache.clone(), cache.clone()
+        whole = run(0, B, a)
+        parts = [run(b0, min(b0 + 8192, B), b) for b0 in range(0, B, 8192)]
+        for t, w in zip(zip(*parts), whole):
+            assert torch.equal(torch.cat(t), w)
+        assert torch.equal(a, b) and bool((whole[0] > 0).any())
+        assert np.array_equal(host(whole[3]), np.minimum(lens, budget))

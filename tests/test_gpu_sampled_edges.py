@@ -263,3 +263,68 @@ def test_a_threshold_below_a_65536th_of_the_highest(tv, V, k, top_p, masked, dty
     got = tv.accept_sampled(dev(np.full(B, -1, np.int32)), dev(np.zeros(B, np.int32)), p, dev(one), dev(np.zeros(B, np.float32)),
                             dev(race), top_k=dev(np.full(B, k, np.int32)), top_p=dev(np.full(B, top_p, np.float32)), max_nodes=1)
     assert np.array_equal(host(got[3]), want)
+
+
+@pytest.mark.parametrize("V,dtype,kw", [(835584, "bf16", dict(T=[1.0], p=[0.9])), (417792, "f32", dict(T=[0.7], k=[300], p=[0.95])),
+                                        (1 << 20, "bf16", {}), (1 << 20, "f32", {})])
+def test_the_largest_vocabularies(tv, V, dtype, kw):
+    """All that a row's slices have room for in shared memory, and all that is allowed where nothing is truncated."""
+    c = Case(80, [4, 3], V, "star", dtype=dtype, q=None, **kw)
+    c.check(c.run(tv, max_nodes=4), most=0.5)
+    with pytest.raises(tv.TVError) as e:                 # a slice more
+        wide = torch.zeros((7, V + 64), dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+        tv.accept_sampled(dev(c.parent), dev(c.tok), wide, dev(c.off), dev(c.u), torch.ones((2, V + 64), device="cuda"),
+                          temperature=dev(c.T), top_k=dev(c.k), top_p=dev(c.p), max_nodes=4)
+    assert e.value.status == -2
+
+
+@pytest.mark.parametrize("kind,q", [("star", None), ("chain", "drawn"), ("random", None)])
+def test_the_largest_trees(tv, kind, q):
+    """1024 nodes in a request, next to one of a single node; in the star all children are refused one after another."""
+    c = Case(81, [1024, 1, 700], 3000, kind, dtype="f32", q=q, spread=0.5)
+    rng = np.random.default_rng(81)
+    if kind == "star":
+        for a, n in ((c.off[0], 1024), (c.off[2], 700)):
+            c.tok[a + 1:a + n] = rng.permutation(3000)[:n - 1]
+            c.u[a + 1:a + n] = np.float32(0.99)
+    if kind == "chain":                                  # the draft is the target's own
+        x = c.logits.astype(np.float64)
+        e = np.exp(x - x.max(1, keepdims=True))
+        c.q = (e / e.sum(1, keepdims=True)).astype(np.float32)
+        c.u = (c.u * 0.999).astype(np.float32)
+    got = c.run(tv, max_nodes=1024)
+    c.check(got, most=0.4)
+    if kind == "chain":
+        assert host(got[0])[0] == 1023 and host(got[2])[0, -1] == 1023
+    if kind == "star":
+        assert (host(got[0]) == 0).all()
+
+
+def test_the_largest_batch(tv):
+    """65535 requests of 0 to 2 nodes: as in batches of 4096."""
+    B, V = 65535, 9
+    rng = np.random.default_rng(82)
+    counts = rng.integers(0, 3, B)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    n = int(off[-1])
+    first = np.zeros(n, bool)
+    first[off[:-1][counts > 0]] = True
+    parent = np.where(first, -1, 0).astype(np.int32)
+    tok, u = rng.integers(0, V, n).astype(np.int32), rng.random(n).astype(np.float32)
+    x, race = rng.standard_normal((n, V)).astype(np.float32), rng.exponential(size=(B, V)).astype(np.float32)
+    T, k = rng.uniform(0.2, 2, B).astype(np.float32), rng.integers(0, 6, B).astype(np.int32)
+    p = rng.uniform(0.5, 1.1, B).astype(np.float32)
+
+    def run(b0, b1):
+        a, b = off[b0], off[b1]
+        return tv.accept_sampled(dev(parent[a:b]), dev(tok[a:b]), dev(x[a:b]), dev(off[b0:b1 + 1] - a), dev(u[a:b]),
+                                 dev(race[b0:b1]), temperature=dev(T[b0:b1]), top_k=dev(k[b0:b1]), top_p=dev(p[b0:b1]),
+                                 max_nodes=2)
+    whole = run(0, B)
+    parts = [run(b0, min(b0 + 4096, B)) for b0 in range(0, B, 4096)]
+    for t, w in zip(zip(*parts), whole):
+        assert torch.equal(torch.cat(t), w)
+    want = osm.verify(parent, tok, x, off[:301], u, race, 1, None, None, T, k, p)
+    sure = want[4] > 2e-5
+    for g, w in zip(whole, want[:4]):
+        assert np.array_equal(host(g)[:300][sure], w[sure])
